@@ -553,3 +553,17 @@ class Plan:
     def checkpoint_load(self, directory: str, begin: int = 0, end: Optional[int] = None,
                         restore_scalars: bool = True, stream=None) -> None:
         dp_checkpoint_load(self.handle, directory, begin, self.P if end is None else end, restore_scalars, stream)
+
+    # layer operators (dplayer.h; the functions of the same names in layers.py)
+    def embed(self, tensor: int, ids, out, scale: float = 1.0, stream=None) -> None:
+        dpl_embed(self, tensor, ids, out, scale, stream)
+
+    def embed_workspace(self, tensor: int, dim: int, tokens: int) -> int:
+        return dpl_embed_workspace(self, tensor, dim, tokens)
+
+    def accumulate_embed(self, tensor: int, ids: Sequence, dy: Sequence, first: bool, workspace,
+                         scale: float = 1.0, more: bool = False, stream=None) -> None:
+        dpl_accumulate_embed(self, tensor, ids, dy, first, workspace, scale, more, stream)
+
+
+from .layers import dpl_accumulate_embed, dpl_embed, dpl_embed_workspace  # noqa: E402

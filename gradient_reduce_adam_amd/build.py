@@ -4,6 +4,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -16,6 +17,9 @@ HIP_FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
              "-Wall", "-Wno-unused-result"]
 
 
+SOURCES = ("kernels.hip", "api.cpp", "checkpoint.cpp", "noalloc.hip", "layers.cpp", "embed.hip")
+
+
 def _run(cmd):
     r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
     if r.returncode != 0:
@@ -26,13 +30,15 @@ def _run(cmd):
 def build(verbose: bool = False) -> str:
     src = os.path.join(HERE, "csrc")
     inc = ["-I", os.path.join(ROOT, "include"), "-I", src]
-    objs = []
-    for name in ("kernels.hip", "api.cpp", "checkpoint.cpp", "noalloc.hip"):
-        obj = os.path.join(src, name + ".o")
-        out = _run(["hipcc", *HIP_FLAGS, *inc, "-c", os.path.join(src, name), "-o", obj])
-        if verbose and out:
-            sys.stdout.write(out)
-        objs.append(obj)
+    objs = [os.path.join(src, name + ".o") for name in SOURCES]
+
+    def compile_one(name, obj):
+        return _run(["hipcc", *HIP_FLAGS, *inc, "-c", os.path.join(src, name), "-o", obj])
+
+    with ThreadPoolExecutor(4) as pool:
+        for out in pool.map(compile_one, SOURCES, objs):
+            if verbose and out:
+                sys.stdout.write(out)
     _run(["hipcc", "--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", LIB + ".tmp"])
     os.replace(LIB + ".tmp", LIB)
     for o in objs:

@@ -8,6 +8,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <exception>
 #include <new>
 #include <string>
 #include <vector>
@@ -184,7 +185,7 @@ const char* bucket_kind(int mode) {
     switch (mode) {
         case 1: return "reduction (dp_accumulate_reduce_range or dp_reduce_replicas_range)";
         case 2: return "single pass (dp_reduce_adam_range, then dp_reduce_adam_finish)";
-        case 3: return "micro-step (dp_accumulate_all_range)";
+        case 3: return "micro-step (dp_accumulate_all_range, dpl_accumulate_*)";
     }
     return "call";
 }
@@ -193,7 +194,7 @@ const char* bucket_kind(int mode) {
 // is half done; a bucketed call may not start while buckets of another kind
 // are open (mode: the caller's kind, 0 for a whole-space call).
 dp_status no_open_buckets(const dp_plan* p, const char* where, int mode = 0) {
-    if (!p->buckets.empty() && p->bucket_mode != mode)
+    if (p->call_open() && p->bucket_mode != mode)
         return fail(DP_ERR_STATE, "%s while a bucketed %s covers %lld of %lld elements", where,
                     bucket_kind(p->bucket_mode), static_cast<long long>(p->bucket_elems),
                     static_cast<long long>(p->P));
@@ -209,6 +210,14 @@ dp_status same_micro_step(const dp_plan* p, bool first) {
             return fail(DP_ERR_STATE, "replicas are at different micro-steps (replica %d: %d, replica 0: %d)", r,
                         p->micro[r], p->micro[0]);
     }
+    return DP_OK;
+}
+
+// The buckets of one micro-step take the same first flag.
+dp_status same_first(const dp_plan* p, bool first) {
+    if (p->bucket_mode == 3 && p->call_open() && first != (p->bucket_first != 0))
+        return fail(DP_ERR_INVALID_ARG, "the buckets of one micro-step take the same first flag (%d here, %d before)",
+                    first, p->bucket_first != 0);
     return DP_OK;
 }
 
@@ -248,6 +257,10 @@ dp_status bucket_span(dp_plan* p, int64_t begin, int64_t end, int64_t* p0, int64
             return fail(DP_ERR_STATE, "bucket [%lld, %lld) overlaps bucket [%lld, %lld) of this reduction",
                         static_cast<long long>(begin), static_cast<long long>(end),
                         static_cast<long long>(b.first), static_cast<long long>(b.second));
+    for (const int32_t t : p->open_terms)
+        if (begin < p->prefix[t + 1] && p->prefix[t] < end)
+            return fail(DP_ERR_STATE, "bucket [%lld, %lld) overlaps tensor %d, which has terms still to come",
+                        static_cast<long long>(begin), static_cast<long long>(end), t);
     if (p0) *p0 = q0;
     if (p1) *p1 = q1;
     return DP_OK;
@@ -711,6 +724,7 @@ dp_status dp_state_init(dp_plan* p, const dp_state_cfg* cfg, hipStream_t stream)
     p->partials_valid = false;
     p->stats_current = false;
     p->buckets.clear();
+    p->open_terms.clear();
     p->bucket_elems = 0;
     p->bucket_mode = 0;
     return DP_OK;
@@ -849,13 +863,24 @@ dp_status dp_accumulate_all(dp_plan* p, int32_t first, hipStream_t stream) {
     return DP_OK;
 }
 
+// After a bucket of a micro-step: the accumulators changed, and once the
+// buckets cover [0, P) the micro-step is complete.
+static void close_micro_step(dp_plan* p, bool first) {
+    p->stats_current = false;
+    p->partials_valid = false;
+    if (p->bucket_elems != p->P) return;
+    p->buckets.clear();
+    p->bucket_elems = 0;
+    p->bucket_mode = 0;
+    for (int32_t r = 0; r < p->n; ++r) p->micro[r] = first ? 1 : p->micro[r] + 1;
+}
+
 dp_status dp_accumulate_all_range(dp_plan* p, int32_t first, int64_t begin, int64_t end, hipStream_t stream) {
     if (!p) return fail(DP_ERR_INVALID_ARG, "dp_accumulate_all_range: null plan");
     dp_status s = no_open_buckets(p, "dp_accumulate_all_range", 3);
     if (s != DP_OK) return s;
-    if (p->bucket_mode == 3 && !p->buckets.empty() && (first != 0) != (p->bucket_first != 0))
-        return fail(DP_ERR_INVALID_ARG, "the buckets of one micro-step take the same first flag (%d here, %d before)",
-                    first != 0, p->bucket_first != 0);
+    s = same_first(p, first != 0);
+    if (s != DP_OK) return s;
     dpk::Srcs grads{}, accs{};
     s = bound_replicas(p, DP_ROLE_GRAD, &grads);
     if (s == DP_OK) s = bound_replicas(p, DP_ROLE_ACC, &accs);
@@ -886,19 +911,12 @@ dp_status dp_accumulate_all_range(dp_plan* p, int32_t first, int64_t begin, int6
         if (s != DP_OK) return s;
     }
     if (end > begin) {
-        if (p->buckets.empty()) p->bucket_first = first != 0;
+        if (!p->call_open()) p->bucket_first = first != 0;
         p->buckets.emplace_back(begin, end);
         p->bucket_elems += end - begin;
         p->bucket_mode = 3;
     }
-    p->stats_current = false;
-    p->partials_valid = false;
-    if (p->bucket_elems == p->P) {  // the buckets cover [0, P): the micro-step is complete
-        p->buckets.clear();
-        p->bucket_elems = 0;
-        p->bucket_mode = 0;
-        for (int32_t r = 0; r < p->n; ++r) p->micro[r] = first ? 1 : p->micro[r] + 1;
-    }
+    close_micro_step(p, first != 0);
     return DP_OK;
 }
 
@@ -1251,3 +1269,68 @@ dp_status dp_read_state(dp_plan* p, dp_step_state* out, hipStream_t stream) {
 }
 
 }  // extern "C"
+
+namespace dpapi {
+
+dp_status part_begin(dp_plan* p, const int32_t* tensors, int count, bool first, const char* where, float** acc,
+                     bool* overwrite) {
+    dp_status s = no_open_buckets(p, where, 3);
+    if (s == DP_OK) s = same_first(p, first);
+    dpk::Srcs accs{};
+    if (s == DP_OK) s = bound_replicas(p, DP_ROLE_ACC, &accs);
+    if (s == DP_OK) s = same_micro_step(p, first);
+    if (s != DP_OK) return s;
+    for (int i = 0; i < count; ++i) {
+        const int32_t t = tensors[i];
+        const bool open = std::find(p->open_terms.begin(), p->open_terms.end(), t) != p->open_terms.end();
+        if (open) {
+            s = ensure_full(p);
+        } else {
+            s = bucket_span(p, p->prefix[t], p->prefix[t + 1], nullptr, nullptr);
+        }
+        if (s != DP_OK) return s;
+        overwrite[i] = first && !open;
+        for (int32_t r = 0; r < p->n; ++r) {
+            const Binding& b = p->roles[DP_ROLE_ACC][r];
+            acc[i * p->n + r] = b.flat ? static_cast<float*>(b.flat) + p->prefix[t]
+                                       : static_cast<float*>(b.tensors[static_cast<size_t>(t)]);
+        }
+    }
+    // room for part_end, which cannot fail once the kernels are launched
+    try {
+        p->buckets.reserve(p->buckets.size() + count);
+        p->open_terms.reserve(p->open_terms.size() + count);
+    } catch (const std::exception&) {
+        return fail(DP_ERR_OOM, "%s: host allocation failed", where);
+    }
+    return DP_OK;
+}
+
+void part_end(dp_plan* p, const int32_t* tensors, int count, bool first, bool more) {
+    if (!p->call_open()) p->bucket_first = first;
+    p->bucket_mode = 3;
+    for (int i = 0; i < count; ++i) {
+        const int32_t t = tensors[i];
+        const auto it = std::find(p->open_terms.begin(), p->open_terms.end(), t);
+        if (more) {
+            if (it == p->open_terms.end()) p->open_terms.push_back(t);
+            continue;
+        }
+        if (it != p->open_terms.end()) p->open_terms.erase(it);
+        p->buckets.emplace_back(p->prefix[t], p->prefix[t + 1]);
+        p->bucket_elems += p->numel[t];
+    }
+    close_micro_step(p, first);
+}
+
+dp_status param_of(dp_plan* p, int32_t tensor, const void** out) {
+    const Binding& b = p->roles[DP_ROLE_PARAM][0];
+    dp_status s = need(&b, "PARAM");
+    if (s == DP_OK) s = ensure_device(p);
+    if (s != DP_OK) return s;
+    *out = b.flat ? static_cast<const char*>(b.flat) + p->prefix[tensor] * static_cast<int64_t>(esize(p->pdt))
+                  : static_cast<const char*>(b.tensors[static_cast<size_t>(tensor)]);
+    return DP_OK;
+}
+
+}  // namespace dpapi

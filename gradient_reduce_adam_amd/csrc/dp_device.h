@@ -1,0 +1,124 @@
+// Device helpers of the layer operators: element types, rows read and written
+// in vectors, reductions over a wave.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "dpstep.h"
+
+namespace dpk {
+
+#define DP_GLOBAL __attribute__((address_space(1)))
+
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+
+template <typename V>
+__device__ __forceinline__ V gload(const void* p, int64_t i) {
+    return ((const DP_GLOBAL V*)p)[i];
+}
+template <typename V>
+__device__ __forceinline__ void gstore(void* p, int64_t i, V x) {
+    ((DP_GLOBAL V*)p)[i] = x;
+}
+template <typename V>
+__device__ __forceinline__ V gload_nt(const void* p, int64_t i) {
+    return __builtin_nontemporal_load(((const DP_GLOBAL V*)p) + i);
+}
+template <typename V>
+__device__ __forceinline__ void gstore_nt(void* p, int64_t i, V x) {
+    __builtin_nontemporal_store(x, ((DP_GLOBAL V*)p) + i);
+}
+
+// Two binary32 values as two 16-bit elements in one word and back (to nearest
+// even; one conversion instruction each way).
+template <dp_dtype DT>
+__device__ __forceinline__ unsigned int pack2(float a, float b) {
+    if constexpr (DT == DP_BF16) {
+        return __builtin_bit_cast(unsigned int, __builtin_convertvector((f32x2{a, b}), bf16x2));
+    } else {
+        return __builtin_bit_cast(unsigned int, __builtin_convertvector((f32x2{a, b}), f16x2));
+    }
+}
+template <dp_dtype DT>
+__device__ __forceinline__ void unpack2(unsigned int u, float* o) {
+    if constexpr (DT == DP_BF16) {
+        o[0] = __builtin_bit_cast(float, u << 16);
+        o[1] = __builtin_bit_cast(float, u & 0xffff0000u);
+    } else {
+        const f16x2 h = __builtin_bit_cast(f16x2, u);
+        o[0] = static_cast<float>(h[0]);
+        o[1] = static_cast<float>(h[1]);
+    }
+}
+
+template <dp_dtype DT>
+__device__ __forceinline__ float load1(const void* p, int64_t i) {
+    if constexpr (DT == DP_F32) return gload<float>(p, i);
+    if constexpr (DT == DP_F16) return static_cast<float>(gload<_Float16>(p, i));
+    return __builtin_bit_cast(float, static_cast<unsigned int>(gload<unsigned short>(p, i)) << 16);
+}
+template <dp_dtype DT>
+__device__ __forceinline__ void store1(void* p, int64_t i, float x) {
+    if constexpr (DT == DP_F32) {
+        gstore<float>(p, i, x);
+    } else {
+        gstore<unsigned short>(p, i, static_cast<unsigned short>(pack2<DT>(x, 0.0f)));
+    }
+}
+
+// N (4 or 8) consecutive elements from element i of p, of which the first
+// `valid` exist (the others come back as zero, or are not written).  `vec`:
+// the address is a multiple of the vector's bytes (16 at most), so that whole
+// vectors go in one or two accesses.
+template <dp_dtype DT, int N>
+__device__ __forceinline__ void load_n(const void* p, int64_t i, int valid, bool vec, float* o) {
+    if (vec && valid >= N) {
+        if constexpr (DT == DP_F32) {
+#pragma unroll
+            for (int k = 0; k < N / 4; ++k) {
+                const f32x4 v = gload<f32x4>(static_cast<const float*>(p) + i, k);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[4 * k + j] = v[j];
+            }
+        } else if constexpr (N == 8) {
+            const u32x4 v = gload<u32x4>(static_cast<const unsigned short*>(p) + i, 0);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) unpack2<DT>(v[j], o + 2 * j);
+        } else {
+            const u32x2 v = gload<u32x2>(static_cast<const unsigned short*>(p) + i, 0);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) unpack2<DT>(v[j], o + 2 * j);
+        }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j) o[j] = j < valid ? load1<DT>(p, i + j) : 0.0f;
+}
+template <dp_dtype DT, int N>
+__device__ __forceinline__ void store_n(void* p, int64_t i, int valid, bool vec, const float* x) {
+    if (vec && valid >= N) {
+        if constexpr (DT == DP_F32) {
+#pragma unroll
+            for (int k = 0; k < N / 4; ++k)
+                gstore<f32x4>(static_cast<float*>(p) + i, k, f32x4{x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]});
+        } else if constexpr (N == 8) {
+            gstore<u32x4>(static_cast<unsigned short*>(p) + i, 0,
+                          u32x4{pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3]), pack2<DT>(x[4], x[5]),
+                                pack2<DT>(x[6], x[7])});
+        } else {
+            gstore<u32x2>(static_cast<unsigned short*>(p) + i, 0, u32x2{pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3])});
+        }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+        if (j < valid) store1<DT>(p, i + j, x[j]);
+}
+
+}  // namespace dpk

@@ -111,18 +111,38 @@ struct dp_plan {
     // same sources, complete once they cover [0, P); 2:
     // single-pass buckets (dp_reduce_adam_range), with the update
     // hyperparameters of the first one, complete at dp_reduce_adam_finish;
-    // 3: buckets of one micro-step of every replica (dp_accumulate_all_range),
-    // with the `first` flag of the first one, complete once they cover [0, P)
+    // 3: buckets of one micro-step of every replica (dp_accumulate_all_range,
+    // dpl_accumulate_*), with the `first` flag of the first one, complete once
+    // they cover [0, P)
     std::vector<std::pair<int64_t, int64_t>> buckets;
     int64_t bucket_elems = 0;
     int bucket_mode = 0;
     dp_adam_hparams bucket_hp{};
     int32_t bucket_first = 0;
     int bucket_src = 0;  // mode 1: 0 the last micro-step fused, else the role reduced
+    // mode 3: tensors with a term of this micro-step in their accumulators and
+    // more to come (dpl_accumulate_* with more != 0); they are not in buckets yet
+    std::vector<int32_t> open_terms;
+
+    // a bucketed call, or a micro-step of layer operators, is half done
+    bool call_open() const { return !buckets.empty() || !open_terms.empty(); }
 };
 
 namespace dpapi {
 // Binds the plan to the current device on first use; DP_ERR_STATE if another
 // device is current later.
 dp_status ensure_device(dp_plan* p);
+
+// A call that writes the gradients of whole tensors into every replica's
+// accumulators, as buckets of one micro-step (dpl_accumulate_*).  part_begin
+// checks the bindings and the order of calls (the tensors are valid indices of
+// non-empty tensors, none twice) and gives each tensor's accumulators,
+// acc[i * n + r], and whether its term is added to them or overwrites them.
+// After the launches part_end marks the tensors as covered, or as open for
+// another term.
+dp_status part_begin(dp_plan* p, const int32_t* tensors, int count, bool first, const char* where, float** acc,
+                     bool* overwrite);
+void part_end(dp_plan* p, const int32_t* tensors, int count, bool first, bool more);
+// The low-precision parameters of one tensor (PARAM bound, plan's device current).
+dp_status param_of(dp_plan* p, int32_t tensor, const void** out);
 }  // namespace dpapi
