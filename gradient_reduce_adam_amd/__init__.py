@@ -565,5 +565,17 @@ class Plan:
                          scale: float = 1.0, more: bool = False, stream=None) -> None:
         dpl_accumulate_embed(self, tensor, ids, dy, first, workspace, scale, more, stream)
 
+    def block_norm(self, norms: "BlockNorm", h, y, s, x=None, stream=None) -> None:
+        dpl_block_norm(self, norms, h, y, s, x, stream)
 
-from .layers import dpl_accumulate_embed, dpl_embed, dpl_embed_workspace  # noqa: E402
+    def block_norm_workspace(self, norms: "BlockNorm", dim: int, tokens: int) -> int:
+        return dpl_block_norm_workspace(self, norms, dim, tokens)
+
+    def accumulate_block_norm(self, norms: "BlockNorm", s, y, dx, ds, dh, dy, first: bool, workspace,
+                              more: bool = False, stream=None) -> None:
+        dpl_accumulate_block_norm(self, norms, s, y, dx, ds, dh, dy, first, workspace, more, stream)
+
+
+from .layers import (BlockNorm, dpl_accumulate_block_norm, dpl_accumulate_embed, dpl_block_norm,  # noqa: E402
+                     dpl_block_norm_workspace, dpl_embed, dpl_embed_workspace, dpl_pack_activations,
+                     dpl_unpack_activations)

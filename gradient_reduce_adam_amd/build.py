@@ -17,7 +17,8 @@ HIP_FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
              "-Wall", "-Wno-unused-result"]
 
 
-SOURCES = ("kernels.hip", "api.cpp", "checkpoint.cpp", "noalloc.hip", "layers.cpp", "embed.hip")
+SOURCES = ("kernels.hip", "api.cpp", "checkpoint.cpp", "noalloc.hip", "layers.cpp", "embed.hip",
+           "block_norm.hip", "block_grad.hip", "act8.hip")
 
 
 def _run(cmd):
@@ -35,7 +36,7 @@ def build(verbose: bool = False) -> str:
     def compile_one(name, obj):
         return _run(["hipcc", *HIP_FLAGS, *inc, "-c", os.path.join(src, name), "-o", obj])
 
-    with ThreadPoolExecutor(4) as pool:
+    with ThreadPoolExecutor(8) as pool:
         for out in pool.map(compile_one, SOURCES, objs):
             if verbose and out:
                 sys.stdout.write(out)

@@ -1,0 +1,353 @@
+// gfx950 kernels of the norms around a block, backward, with the gradients of
+// weights and gate.
+//
+// Mathematics.  Let d = s - mean(s) (or s), r = 1 / sqrt(mean(d^2) + eps),
+// n = d r, e = dx w_pre.  Then
+//   t = ds + r (e - [mean(e)] - n mean(e n)),  dh = alpha t,
+// the bracket only with the mean subtracted, and the same step on y with e =
+// t gate w_post gives dy.  Column sums over the tokens: C = sum dx n(s) and E =
+// sum dx are the gradients of w_pre and b_pre.  With A = sum t n(y) and B =
+// sum t the others follow per column: dw_post = gate A, db_post = gate B, dgate
+// = w_post A + b_post B, so a thread keeps two sums per column (four with the
+// mean subtracted) instead of five.
+//
+// Bound by HBM: four rows read and two written per token, all of them held in
+// registers as in the forward.  The sums of a row that do not depend on each
+// other go through one reduction (RMS: 2 a row, centred: 3).  The column sums
+// of a workgroup go to the workspace, and a second launch adds the
+// workgroups' sums in a fixed order, so the bits depend on the sizes alone.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "block_norm.h"
+#include "dp_device.h"
+#include "dp_layers.h"
+
+namespace dpk {
+namespace {
+
+// ---- backward ------------------------------------------------------------------
+struct GradArgs {
+    dpl_norm_rows rows[DP_MAX_REPLICAS];
+    float* part;  // [n][groups][quantities][dim]
+    int64_t tokens, ld;
+    int32_t dim;
+    float eps, alpha;
+    bool vec;
+    Weights w;
+};
+
+// Column sums a workgroup leaves: C = sum dx n(s), A = sum t n(y) (t y without
+// a post norm), and with the mean subtracted E = sum dx, B = sum t.
+template <bool kCentered>
+constexpr int kSums = kCentered ? 4 : 2;
+
+template <dp_dtype DT, dp_dtype PT, int NT, int NV, bool kCentered, bool kPost>
+__global__ void __launch_bounds__(block_of(NT)) k_block_grad(GradArgs a) {
+    constexpr int kRows = block_of(NT) / NT, kStep = 8 * NT, Q = kSums<kCentered>;
+    __shared__ float lds[sum_scratch(NT)];
+    __shared__ float fold[kRows > 1 ? kRows - 1 : 1][kRows > 1 ? NT * 8 * NV : 1];
+    int turn = 0;
+    const dpl_norm_rows p = a.rows[blockIdx.y];
+    const int lane = threadIdx.x % NT, c0 = 8 * lane;
+    const float dim = static_cast<float>(a.dim), inv = 1.0f / dim;
+    const bool has_gate = a.w.gate != nullptr, has_x = p.dx != nullptr, has_ds = p.ds != nullptr;
+    const bool has_y = kPost || has_gate;
+    Column<PT, NV> post_w, gate, pre_w;
+    if constexpr (kPost) post_w.load(a.w.post_w, c0, kStep, a.dim, a.w.vec);
+    if (has_gate) gate.load(a.w.gate, c0, kStep, a.dim, a.w.vec);
+    if (has_x) pre_w.load(a.w.pre_w, c0, kStep, a.dim, a.w.vec);
+    float sum[Q][NV][8];
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum[q][k][j] = 0.0f;
+
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * kRows;
+    int64_t base = static_cast<int64_t>(blockIdx.x) * kRows;
+    int64_t row = base + threadIdx.x / NT;
+    Raw<DT> ns[NV], ny[NV], nx[NV], nd[NV];
+    auto fetch = [&](int64_t t) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int c = c0 + k * kStep;
+            const int valid = t < a.tokens ? valid_of(a.dim, c) : 0;
+            const int64_t at = t * a.ld + c;
+            ns[k] = load_raw<DT>(p.s, at, has_x ? valid : 0, a.vec && has_x);
+            nx[k] = load_raw<DT>(p.dx, at, has_x ? valid : 0, a.vec && has_x);
+            ny[k] = load_raw<DT>(p.y, at, has_y ? valid : 0, a.vec && has_y);
+            nd[k] = load_raw<DT>(p.ds, at, has_ds ? valid : 0, a.vec && has_ds);
+        }
+    };
+    fetch(row);
+    for (; base < a.tokens; base += stride, row += stride) {
+        float s[NV][8], y[NV][8], e[NV][8], t[NV][8];
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            expand<DT>(ns[k], s[k]);
+            expand<DT>(nx[k], e[k]);
+            expand<DT>(ny[k], y[k]);
+            expand<DT>(nd[k], t[k]);
+        }
+        if (base + stride < a.tokens) fetch(row + stride);
+        if constexpr (kCentered) {
+            float m[2] = {0.0f, 0.0f};
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    m[0] += s[k][j];
+                    m[1] += y[k][j];
+                }
+            row_sum<NT>(m, lds, turn);
+            const float mean_s = m[0] / dim, mean_y = m[1] / dim;
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const bool in = j < valid_of(a.dim, c0 + k * kStep);
+                    s[k][j] = in ? s[k][j] - mean_s : 0.0f;
+                    if constexpr (kPost) y[k][j] = in ? y[k][j] - mean_y : 0.0f;
+                }
+        }
+        // sums of s^2 and e s, of e with the mean subtracted, of y^2 with a post norm (e = dx w_pre)
+        constexpr int kE = 2, kY = 2 + kCentered;
+        float v[2 + kCentered + kPost] = {};
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            float w[8];
+            expand<PT>(pre_w.q[k], w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float f = has_x ? e[k][j] * w[j] : 0.0f;
+                v[0] += s[k][j] * s[k][j];
+                v[1] += f * s[k][j];
+                if constexpr (kCentered) v[kE] += f;
+                if constexpr (kPost) v[kY] += y[k][j] * y[k][j];
+            }
+        }
+        row_sum<NT>(v, lds, turn);
+        const float r = 1.0f / sqrtf(v[0] * inv + a.eps), mean_en = v[1] * r * inv;
+        float ry = 1.0f, mean_e = 0.0f;
+        if constexpr (kPost) ry = 1.0f / sqrtf(v[kY] * inv + a.eps);
+        if constexpr (kCentered) mean_e = v[kE] * inv;
+        if (has_x) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                float w[8];
+                expand<PT>(pre_w.q[k], w);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float n = s[k][j] * r;
+                    sum[0][k][j] += e[k][j] * n;
+                    if constexpr (kCentered) sum[2][k][j] += e[k][j];
+                    t[k][j] += r * (e[k][j] * w[j] - mean_e - n * mean_en);
+                }
+            }
+        }
+        // t is the gradient of s; columns beyond the row's end hold what is never stored
+        float g[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            float w[8], f[8];
+            const int c = c0 + k * kStep, valid = row < a.tokens ? valid_of(a.dim, c) : 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = a.alpha * t[k][j];
+            if (p.dh) store_n<DT, 8>(p.dh, row * a.ld + c, valid, a.vec, f);
+            if constexpr (kCentered) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum[3][k][j] += j < valid ? t[k][j] : 0.0f;
+            }
+            if (kPost || has_gate) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum[1][k][j] += t[k][j] * (kPost ? y[k][j] * ry : y[k][j]);
+            }
+            if (has_gate) {
+                expand<PT>(gate.q[k], w);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) t[k][j] *= w[j];
+            }
+            if constexpr (kPost) {
+                expand<PT>(post_w.q[k], w);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    t[k][j] *= w[j];
+                    g[0] += t[k][j] * y[k][j];
+                    g[1] += j < valid_of(a.dim, c) ? t[k][j] : 0.0f;
+                }
+            }
+        }
+        if (!p.dy) continue;
+        if constexpr (kPost) {
+            row_sum<NT>(g, lds, turn);
+            const float mean_tn = g[0] * ry * inv, mean_t = kCentered ? g[1] * inv : 0.0f;
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) t[k][j] = ry * (t[k][j] - mean_t - y[k][j] * ry * mean_tn);
+        }
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int c = c0 + k * kStep, valid = row < a.tokens ? valid_of(a.dim, c) : 0;
+            store_n<DT, 8>(p.dy, row * a.ld + c, valid, a.vec, t[k]);
+        }
+    }
+    // the rows' sums of this workgroup, in row order, then one slot of the workspace
+    float* out = a.part + (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * Q * a.dim;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+        if constexpr (kRows > 1) {
+            __syncthreads();
+            const int w = threadIdx.x / NT;
+            if (w > 0)
+#pragma unroll
+                for (int k = 0; k < NV; ++k)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) fold[w - 1][(k * 8 + j) * NT + lane] = sum[q][k][j];
+            __syncthreads();
+            if (w == 0)
+                for (int i = 0; i < kRows - 1; ++i)
+#pragma unroll
+                    for (int k = 0; k < NV; ++k)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) sum[q][k][j] += fold[i][(k * 8 + j) * NT + lane];
+        }
+        if (threadIdx.x < NT)
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+                store_n<DP_F32, 8>(out + q * a.dim, c0 + k * kStep, valid_of(a.dim, c0 + k * kStep), a.dim % 4 == 0,
+                                   sum[q][k]);
+    }
+}
+
+struct JoinArgs {
+    const float* part;
+    float* acc[5][DP_MAX_REPLICAS];  // post_w, post_b, gate, pre_w, pre_b; null: none
+    bool overwrite[5];
+    int32_t dim, groups, sums;
+    Weights w;
+};
+
+constexpr int kJoinColumns = 32, kJoinLanes = 16;
+
+template <dp_dtype PT>
+__device__ __forceinline__ float weight_at(const void* p, int c, float none) {
+    return p ? load1<PT>(p, c) : none;
+}
+
+// Adds the workgroups' sums of 32 columns of one replica: 16 threads a column
+// each take every 16th group, then their sums are added in order.
+template <dp_dtype PT>
+__global__ void __launch_bounds__(kJoinColumns* kJoinLanes) k_block_join(JoinArgs a) {
+    __shared__ float lds[kJoinLanes][kJoinColumns];
+    const int col = threadIdx.x % kJoinColumns, lane = threadIdx.x / kJoinColumns;
+    const int c = blockIdx.x * kJoinColumns + col, r = blockIdx.y;
+    const float* part = a.part + static_cast<int64_t>(r) * a.groups * a.sums * a.dim;
+    float total[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int q = 0; q < a.sums; ++q) {
+        float s = 0.0f;
+        if (c < a.dim)
+#pragma unroll 4
+            for (int g = lane; g < a.groups; g += kJoinLanes) s += part[(static_cast<int64_t>(g) * a.sums + q) * a.dim + c];
+        __syncthreads();
+        lds[lane][col] = s;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kJoinLanes; ++i) total[q] += lds[i][col];
+    }
+    if (lane != 0 || c >= a.dim) return;
+    const float C = total[0], A = total[1], E = total[2], B = total[3];
+    const float gate = weight_at<PT>(a.w.gate, c, 1.0f);
+    const float grads[5] = {gate * A, gate * B,
+                            a.w.post_w ? weight_at<PT>(a.w.post_w, c, 1.0f) * A + weight_at<PT>(a.w.post_b, c, 0.0f) * B : A,
+                            C, E};
+#pragma unroll
+    for (int i = 0; i < 5; ++i)
+        if (a.acc[i][r]) a.acc[i][r][c] = a.overwrite[i] ? grads[i] : a.acc[i][r][c] + grads[i];
+}
+
+Shape shape_of(int64_t dim) {
+    if (dim <= 512) return {64, 1};
+    if (dim <= 1024) return {128, 1};
+    if (dim <= 2048) return {256, 1};
+    if (dim <= 4096) return {512, 1};
+    return {512, 2};
+}
+
+#define DP_SHAPES(GO)                  \
+    if (sh.nt == 64) GO(64, 1)         \
+    else if (sh.nt == 128) GO(128, 1)  \
+    else if (sh.nt == 256) GO(256, 1)  \
+    else if (sh.nv == 1) GO(512, 1)    \
+    else GO(512, 2)
+
+// Workgroups of one replica's backward: about as many as the chip holds at a
+// time, shared by the replicas, each with rows to walk over.
+int64_t groups_of(int64_t dim, int64_t tokens, int n) {
+    const int nt = shape_of(dim).nt;
+    const int64_t most = (256 * 1024 / block_of(nt) + n - 1) / n, rows = block_of(nt) / nt;
+    const int64_t want = (tokens + rows - 1) / rows;
+    return want < most ? want : most;
+}
+
+template <dp_dtype DT, dp_dtype PT, bool kCentered, bool kPost>
+void backward(const GradArgs& a, int groups, int n, hipStream_t stream) {
+    const Shape sh = shape_of(a.dim);
+    const dim3 grid(static_cast<unsigned>(groups), static_cast<unsigned>(n));
+#define GO(T, V) \
+    { hipLaunchKernelGGL((k_block_grad<DT, PT, T, V, kCentered, kPost>), grid, dim3(block_of(T)), 0, stream, a); }
+    DP_SHAPES(GO)
+#undef GO
+}
+
+}  // namespace
+
+size_t block_norm_workspace(int64_t dim, int64_t tokens, int n, bool centered) {
+    return static_cast<size_t>(4) * n * groups_of(dim, tokens, n) * (centered ? 4 : 2) * dim;
+}
+
+hipError_t launch_block_grad(dp_dtype dt, dp_dtype pdt, const BlockNorm& b, int64_t tokens, int n,
+                             const dpl_norm_rows* rows, int64_t ld, bool vec, float* const* acc, const int* at,
+                             const bool* overwrite, void* workspace, hipStream_t stream) {
+    GradArgs a{};
+    for (int r = 0; r < n; ++r) a.rows[r] = rows[r];
+    a.part = static_cast<float*>(workspace);
+    a.tokens = tokens;
+    a.ld = ld;
+    a.dim = static_cast<int32_t>(b.dim);
+    a.eps = b.eps;
+    a.alpha = b.alpha;
+    a.vec = vec;
+    a.w = weights_of(b);
+    const bool post = b.weight[0] != nullptr;
+    const int groups = static_cast<int>(groups_of(b.dim, tokens, n));
+    if (tokens > 0) {
+#define GO(D, P, C, O) backward<D, P, C, O>(a, groups, n, stream)
+        DP_KINDS(GO);
+#undef GO
+        hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    JoinArgs j{};
+    bool any = false;
+    for (int i = 0; i < 5; ++i) {
+        if (at[i] < 0) continue;
+        any = true;
+        j.overwrite[i] = overwrite[at[i]];
+        for (int r = 0; r < n; ++r) j.acc[i][r] = acc[at[i] * n + r];
+    }
+    if (!any) return hipSuccess;
+    j.part = a.part;
+    j.dim = a.dim;
+    j.groups = tokens > 0 ? groups : 0;
+    j.sums = b.centered ? 4 : 2;
+    j.w = a.w;
+    const dim3 grid(static_cast<unsigned>((b.dim + kJoinColumns - 1) / kJoinColumns), static_cast<unsigned>(n));
+    if (pdt == DP_BF16) hipLaunchKernelGGL((k_block_join<DP_BF16>), grid, dim3(kJoinColumns * kJoinLanes), 0, stream, j);
+    else hipLaunchKernelGGL((k_block_join<DP_F16>), grid, dim3(kJoinColumns * kJoinLanes), 0, stream, j);
+    return hipGetLastError();
+}
+
+}  // namespace dpk

@@ -1,0 +1,145 @@
+// What the forward and the backward of the block norms share: rows in
+// registers, reductions over a row, the choices of a launch.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "dp_device.h"
+#include "dp_layers.h"
+
+namespace dpk {
+
+// Eight elements as they lie in memory.
+template <dp_dtype DT>
+struct Raw {
+    static constexpr int kWords = DT == DP_F32 ? 8 : 4;
+    unsigned int w[kWords];
+};
+
+template <dp_dtype DT>
+__device__ __forceinline__ Raw<DT> load_raw(const void* p, int64_t i, int valid, bool vec) {
+    Raw<DT> q;
+    if (vec && valid >= 8) {
+        const u32x4* at = reinterpret_cast<const u32x4*>(static_cast<const char*>(p) + i * (DT == DP_F32 ? 4 : 2));
+#pragma unroll
+        for (int k = 0; k < Raw<DT>::kWords / 4; ++k) {
+            const u32x4 v = gload<u32x4>(at, k);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) q.w[4 * k + j] = v[j];
+        }
+        return q;
+    }
+    if constexpr (DT == DP_F32) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) q.w[j] = j < valid ? gload<unsigned int>(p, i + j) : 0u;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const unsigned int lo = 2 * j < valid ? gload<unsigned short>(p, i + 2 * j) : 0u;
+            const unsigned int hi = 2 * j + 1 < valid ? gload<unsigned short>(p, i + 2 * j + 1) : 0u;
+            q.w[j] = lo | hi << 16;
+        }
+    }
+    return q;
+}
+
+template <dp_dtype DT>
+__device__ __forceinline__ void expand(const Raw<DT>& q, float* o) {
+    if constexpr (DT == DP_F32) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = __builtin_bit_cast(float, q.w[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) unpack2<DT>(q.w[j], o + 2 * j);
+    }
+}
+
+// Threads of a workgroup whose rows are held by nt threads each.
+constexpr int block_of(int nt) { return nt < 256 ? 256 : nt; }
+
+// Scratch of row_sum: 4 floats a wave for each of two turns, taken in
+// alternation, so that one barrier a reduction is enough.
+constexpr int sum_scratch(int nt) { return nt > 64 ? 2 * 4 * (block_of(nt) / 64) : 1; }
+
+// Sums of K <= 4 values over the NT threads of a row, the same in each of them.
+template <int NT, int K>
+__device__ __forceinline__ void row_sum(float (&v)[K], float* lds, int& turn) {
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1)
+#pragma unroll
+        for (int k = 0; k < K; ++k) v[k] += __shfl_xor(v[k], d);
+    if constexpr (NT > 64) {
+        constexpr int kWaves = NT / 64;  // of a row
+        float* at = lds + turn * (block_of(NT) / 64) * 4;
+        turn ^= 1;
+        if ((threadIdx.x & 63) == 0)
+#pragma unroll
+            for (int k = 0; k < K; ++k) at[(threadIdx.x >> 6) * 4 + k] = v[k];
+        __syncthreads();
+        at += threadIdx.x / NT * kWaves * 4;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            v[k] = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) v[k] += at[w * 4 + k];
+        }
+    }
+}
+
+struct Weights {
+    const void *post_w, *post_b, *gate, *pre_w, *pre_b;  // null: none
+    bool vec;
+};
+
+// The weights of this thread's columns stay packed in registers over all rows.
+template <dp_dtype PT, int NV>
+struct Column {
+    Raw<PT> q[NV];
+    __device__ __forceinline__ void load(const void* p, int c0, int step, int dim, bool vec) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int left = dim - (c0 + k * step);
+            const int valid = !p || left <= 0 ? 0 : left < 8 ? left : 8;
+            q[k] = load_raw<PT>(p, c0 + k * step, valid, vec);
+        }
+    }
+};
+
+__device__ __forceinline__ int valid_of(int dim, int c) { return dim - c >= 8 ? 8 : dim - c > 0 ? dim - c : 0; }
+
+
+// Threads of a row and 8-element vectors of a thread, by the row's width.
+struct Shape {
+    int nt, nv;
+};
+
+inline Weights weights_of(const BlockNorm& b) {
+    Weights w{};
+    w.post_w = b.weight[0];
+    w.post_b = b.weight[1];
+    w.gate = b.weight[2];
+    w.pre_w = b.weight[3];
+    w.pre_b = b.weight[4];
+    w.vec = b.vec_w;
+    return w;
+}
+
+
+// Calls GO with the compile-time choices of a call: row type, weight type, mean, post norm.
+#define DP_KINDS(GO)                                                        \
+    do {                                                                    \
+        if (dt == DP_F32 && pdt == DP_BF16) DP_KINDS2(GO, DP_F32, DP_BF16)  \
+        else if (dt == DP_F32) DP_KINDS2(GO, DP_F32, DP_F16)                \
+        else if (dt == DP_F16) DP_KINDS2(GO, DP_F16, DP_F16)                \
+        else DP_KINDS2(GO, DP_BF16, DP_BF16)                                \
+    } while (0)
+#define DP_KINDS2(GO, D, P)                           \
+    {                                                 \
+        if (b.centered && post) GO(D, P, true, true); \
+        else if (b.centered) GO(D, P, true, false);   \
+        else if (post) GO(D, P, false, true);         \
+        else GO(D, P, false, false);                  \
+    }
+
+}  // namespace dpk

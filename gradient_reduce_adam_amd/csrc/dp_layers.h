@@ -32,4 +32,29 @@ size_t embed_workspace(int64_t dim, int64_t tokens, int n);
 int64_t embed_waves(const EmbedGrad& a);  // workgroups of its largest launch, for one replica
 hipError_t launch_embed_grad(dp_dtype dt, const EmbedGrad& a, void* workspace, hipStream_t stream);
 
+// ---- norms around a block (block_norm.hip) -----------------------------------
+struct BlockNorm {
+    const void* weight[5];  // post_w, post_b, gate, pre_w, pre_b in the parameter dtype; null: none
+    int64_t dim;
+    float eps, alpha;
+    bool centered;
+    bool vec_w;  // every weight can be read 16 bytes at a time
+};
+// vec: of h, y, s, x.
+hipError_t launch_block_norm(dp_dtype dt, dp_dtype pdt, const BlockNorm& b, int64_t tokens, const void* h,
+                             int64_t ld_h, const void* y, int64_t ld_y, void* s, int64_t ld_s, void* x, int64_t ld_x,
+                             const bool* vec, hipStream_t stream);
+size_t block_norm_workspace(int64_t dim, int64_t tokens, int n, bool centered);
+// at[i]: which accumulator (acc[at * n + r], overwrite[at]) takes the gradient
+// of weight i, -1 for none.
+hipError_t launch_block_grad(dp_dtype dt, dp_dtype pdt, const BlockNorm& b, int64_t tokens, int n,
+                             const dpl_norm_rows* rows, int64_t ld, bool vec, float* const* acc, const int* at,
+                             const bool* overwrite, void* workspace, hipStream_t stream);
+
+// ---- activations in 8 bits (act8.hip) ------------------------------------------
+hipError_t launch_pack(dp_dtype dt, int64_t tokens, int64_t dim, const void* x, int64_t ld, void* codes,
+                       int64_t ld_codes, void* scales, int64_t ld_scales, bool vec, hipStream_t stream);
+hipError_t launch_unpack(dp_dtype dt, int64_t tokens, int64_t dim, const void* codes, int64_t ld_codes,
+                         const void* scales, int64_t ld_scales, void* x, int64_t ld, bool vec, hipStream_t stream);
+
 }  // namespace dpk

@@ -89,6 +89,83 @@ dp_status check_ids(const char* where, const void* ids, int64_t tokens, int32_t 
     return DP_OK;
 }
 
+// ---- norms around a block ----------------------------------------------------
+// The tensors of a dpl_norms in the kernels' order, and their parameters.
+struct Norms {
+    dpk::BlockNorm b{};
+    int32_t tensors[5];  // those that are there
+    int at[5];           // weight i is tensors[at[i]], -1: none
+    int count = 0;
+};
+
+dp_status check_norms(const char* where, const dp_plan* plan, const dpl_norms* d, Norms* out) {
+    if (!plan || !d) return fail(DP_ERR_INVALID_ARG, "%s: null argument", where);
+    if (d->dim < 1 || d->dim > DPL_MAX_NORM_DIM)
+        return fail(DP_ERR_INVALID_ARG, "%s: rows of %lld elements outside [1, %d]", where, ll(d->dim), DPL_MAX_NORM_DIM);
+    const float eps = static_cast<float>(d->eps), alpha = static_cast<float>(d->residual_scale);
+    if (!(eps > 0.0f) || !std::isfinite(eps)) return fail(DP_ERR_INVALID_ARG, "%s: eps must be a positive binary32 number", where);
+    if (!std::isfinite(alpha)) return fail(DP_ERR_INVALID_ARG, "%s: the residual scale is not finite", where);
+    const int32_t t[5] = {d->post_w, d->post_b, d->gate, d->pre_w, d->pre_b};
+    const char* names[5] = {"post_w", "post_b", "gate", "pre_w", "pre_b"};
+    for (int i = 0; i < 5; ++i) {
+        out->at[i] = -1;
+        if (t[i] < 0) continue;
+        dp_status s = check_tensor(where, plan, t[i]);
+        if (s != DP_OK) return s;
+        if (plan->numel[static_cast<size_t>(t[i])] != d->dim)
+            return fail(DP_ERR_INVALID_ARG, "%s: %s is tensor %d of %lld elements, rows have %lld", where, names[i], t[i],
+                        ll(plan->numel[static_cast<size_t>(t[i])]), ll(d->dim));
+        for (int k = 0; k < out->count; ++k)
+            if (out->tensors[k] == t[i]) return fail(DP_ERR_INVALID_ARG, "%s: tensor %d is named twice", where, t[i]);
+        out->at[i] = out->count;
+        out->tensors[out->count++] = t[i];
+    }
+    if ((d->post_b >= 0 && d->post_w < 0) || (d->pre_b >= 0 && d->pre_w < 0))
+        return fail(DP_ERR_INVALID_ARG, "%s: a bias without its weight", where);
+    out->b.dim = d->dim;
+    out->b.eps = eps;
+    out->b.alpha = alpha;
+    out->b.centered = d->centered != 0;
+    return DP_OK;
+}
+
+// The weights' addresses, once everything else is checked.
+dp_status norm_weights(const char* where, dp_plan* plan, Norms* n) {
+    n->b.vec_w = true;
+    if (n->count == 0) return dpapi::ensure_device(plan);
+    for (int i = 0; i < 5; ++i) {
+        if (n->at[i] < 0) continue;
+        dp_status s = dpapi::param_of(plan, n->tensors[n->at[i]], &n->b.weight[i]);
+        if (s != DP_OK) return s;
+        if (!multiple(n->b.weight[i], 2)) return fail(DP_ERR_INVALID_ARG, "%s: a weight is not aligned to its elements", where);
+        n->b.vec_w = n->b.vec_w && multiple(n->b.weight[i], 16);
+    }
+    return DP_OK;
+}
+
+// Rows of 16-bit elements go with parameters of the same type.
+dp_status check_norm_dtype(const char* where, const dp_plan* plan, dp_dtype dtype) {
+    if (!dtype_ok(dtype)) return fail(DP_ERR_INVALID_ARG, "%s: unknown dtype %d", where, static_cast<int>(dtype));
+    if (dtype != DP_F32 && dtype != plan->pdt)
+        return fail(DP_ERR_INVALID_ARG, "%s: 16-bit rows must have the parameters' dtype", where);
+    return DP_OK;
+}
+
+// ---- activations in 8 bits -----------------------------------------------------
+dp_status check_packed(const char* where, int64_t tokens, int64_t dim, dp_dtype dtype, const void* codes,
+                       int64_t ld_codes, const void* scales, int64_t ld_scales) {
+    dp_status s = check_tokens(where, tokens);
+    if (s != DP_OK) return s;
+    if (dim < 1 || dim > (int64_t{1} << 24)) return fail(DP_ERR_INVALID_ARG, "%s: rows of %lld elements outside [1, 2^24]", where, ll(dim));
+    if (!dtype_ok(dtype)) return fail(DP_ERR_INVALID_ARG, "%s: unknown dtype %d", where, static_cast<int>(dtype));
+    s = check_rows(where, "codes", codes, tokens, dim, ld_codes, 1);
+    if (s == DP_OK) s = check_rows(where, "scales", scales, tokens, (dim + DPL_GROUP - 1) / DPL_GROUP, ld_scales, 1);
+    if (s != DP_OK) return s;
+    if ((dim + DPL_GROUP - 1) / DPL_GROUP * tokens > (int64_t{1} << 31))
+        return fail(DP_ERR_INVALID_ARG, "%s: %lld rows of %lld elements are too many for one call", where, ll(tokens), ll(dim));
+    return DP_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -160,6 +237,118 @@ dp_status dpl_accumulate_embed(dp_plan* plan, const dpl_table* table, int64_t to
     if (s != DP_OK) return s;
     dpapi::part_end(plan, &table->tensor, 1, first != 0, more != 0);
     return DP_OK;
+}
+
+dp_status dpl_block_norm(dp_plan* plan, const dpl_norms* norms, int64_t tokens, dp_dtype dtype, const void* h,
+                         int64_t ld_h, const void* y, int64_t ld_y, void* s_out, int64_t ld_s, void* x, int64_t ld_x,
+                         hipStream_t stream) {
+    const char* where = "dpl_block_norm";
+    Norms n;
+    dp_status s = check_norms(where, plan, norms, &n);
+    if (s == DP_OK) s = check_tokens(where, tokens);
+    if (s == DP_OK) s = check_norm_dtype(where, plan, dtype);
+    if (s != DP_OK) return s;
+    const int64_t e = esize(dtype);
+    const bool has_x = n.at[3] >= 0;
+    s = check_rows(where, "h", h, tokens, n.b.dim, ld_h, e);
+    if (s == DP_OK) s = check_rows(where, "y", y, tokens, n.b.dim, ld_y, e);
+    if (s == DP_OK) s = check_rows(where, "s", s_out, tokens, n.b.dim, ld_s, e);
+    if (s == DP_OK && has_x) s = check_rows(where, "x", x, tokens, n.b.dim, ld_x, e);
+    if (s != DP_OK) return s;
+    if (!has_x && x) return fail(DP_ERR_INVALID_ARG, "%s: x without a norm before the next block", where);
+    if ((s_out == h && ld_s != ld_h) || (s_out == y && ld_s != ld_y))
+        return fail(DP_ERR_INVALID_ARG, "%s: s in place of an input needs its row stride", where);
+    if (tokens > 0 && x && (x == h || x == y || x == s_out))
+        return fail(DP_ERR_INVALID_ARG, "%s: x must not overlap another tensor", where);
+    s = norm_weights(where, plan, &n);
+    if (s != DP_OK) return s;
+    const bool vec[4] = {vec_rows(h, ld_h, e, 16), vec_rows(y, ld_y, e, 16), vec_rows(s_out, ld_s, e, 16),
+                         vec_rows(x, ld_x, e, 16)};
+    return launched(dpk::launch_block_norm(dtype, plan->pdt, n.b, tokens, h, ld_h, y, ld_y, s_out, ld_s,
+                                           has_x ? x : nullptr, ld_x, vec, stream),
+                    "block norm launch");
+}
+
+dp_status dpl_block_norm_workspace(const dp_plan* plan, const dpl_norms* norms, int64_t tokens, size_t* bytes) {
+    Norms n;
+    dp_status s = check_norms("dpl_block_norm_workspace", plan, norms, &n);
+    if (s == DP_OK) s = check_tokens("dpl_block_norm_workspace", tokens);
+    if (s == DP_OK && !bytes) s = fail(DP_ERR_INVALID_ARG, "dpl_block_norm_workspace: null argument");
+    if (s != DP_OK) return s;
+    *bytes = dpk::block_norm_workspace(n.b.dim, tokens, plan->n, n.b.centered);
+    return DP_OK;
+}
+
+dp_status dpl_accumulate_block_norm(dp_plan* plan, const dpl_norms* norms, int64_t tokens, dp_dtype dtype,
+                                    const dpl_norm_rows* rows, int64_t ld, int32_t first, int32_t more,
+                                    void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    const char* where = "dpl_accumulate_block_norm";
+    Norms n;
+    dp_status s = check_norms(where, plan, norms, &n);
+    if (s == DP_OK) s = check_tokens(where, tokens);
+    if (s == DP_OK) s = check_norm_dtype(where, plan, dtype);
+    if (s != DP_OK) return s;
+    if (!rows) return fail(DP_ERR_INVALID_ARG, "%s: null argument", where);
+    if (n.count == 0) return fail(DP_ERR_INVALID_ARG, "%s: no norm and no gate", where);
+    const int64_t e = esize(dtype);
+    const bool has_x = n.at[3] >= 0, has_y = n.at[0] >= 0 || n.at[2] >= 0;
+    bool vec = ld * e % 16 == 0;
+    for (int32_t r = 0; r < plan->n; ++r) {
+        const dpl_norm_rows& p = rows[r];
+        const void* all[6] = {p.s, p.y, p.dx, p.ds, p.dh, p.dy};
+        const char* names[6] = {"s", "y", "dx", "ds", "dh", "dy"};
+        const void* zero[6] = {rows[0].s, rows[0].y, rows[0].dx, rows[0].ds, rows[0].dh, rows[0].dy};
+        for (int i = 0; i < 6; ++i) {
+            if (tokens > 0 && !all[i] != !zero[i])
+                return fail(DP_ERR_INVALID_ARG, "%s: %s is null for some replicas only", where, names[i]);
+            s = check_rows(where, names[i], all[i], 0, n.b.dim, ld, e);
+            if (s != DP_OK) return s;
+            vec = vec && multiple(all[i], 16);
+        }
+        if (tokens > 0 && !p.dx != !has_x)
+            return fail(DP_ERR_INVALID_ARG, "%s: dx is given exactly with a norm before the next block", where);
+        if (tokens > 0 && has_x && !p.s) return fail(DP_ERR_INVALID_ARG, "%s: s is null", where);
+        if (tokens > 0 && has_y && !p.y) return fail(DP_ERR_INVALID_ARG, "%s: y is null", where);
+        if (tokens > 0 && !has_x && !p.ds) return fail(DP_ERR_INVALID_ARG, "%s: no gradient: dx and ds are null", where);
+        if (tokens > 0 && ((p.dh && (p.dh == p.dy || p.dh == p.s || p.dh == p.y)) || (p.dy && p.dy == p.s)))
+            return fail(DP_ERR_INVALID_ARG, "%s: outputs overlap each other, s or y", where);
+    }
+    s = check_workspace(where, workspace, workspace_bytes, dpk::block_norm_workspace(n.b.dim, tokens, plan->n, n.b.centered));
+    if (s == DP_OK) s = norm_weights(where, plan, &n);
+    if (s != DP_OK) return s;
+    float* acc[5 * DP_MAX_REPLICAS];
+    bool overwrite[5];
+    s = dpapi::part_begin(plan, n.tensors, n.count, first != 0, where, acc, overwrite);
+    if (s == DP_OK) s = check_acc(where, acc, n.count * plan->n);
+    if (s != DP_OK) return s;
+    s = launched(dpk::launch_block_grad(dtype, plan->pdt, n.b, tokens, plan->n, rows, ld, vec, acc, n.at, overwrite,
+                                        workspace, stream),
+                 "block norm gradient launch");
+    if (s != DP_OK) return s;
+    dpapi::part_end(plan, n.tensors, n.count, first != 0, more != 0);
+    return DP_OK;
+}
+
+dp_status dpl_pack_activations(int64_t tokens, int64_t dim, dp_dtype dtype, const void* x, int64_t ld, void* codes,
+                               int64_t ld_codes, void* scales, int64_t ld_scales, hipStream_t stream) {
+    const char* where = "dpl_pack_activations";
+    dp_status s = check_packed(where, tokens, dim, dtype, codes, ld_codes, scales, ld_scales);
+    if (s == DP_OK) s = check_rows(where, "x", x, tokens, dim, ld, esize(dtype));
+    if (s != DP_OK) return s;
+    const bool vec = vec_rows(x, ld, esize(dtype), 16) && vec_rows(codes, ld_codes, 1, 16);
+    return launched(dpk::launch_pack(dtype, tokens, dim, x, ld, codes, ld_codes, scales, ld_scales, vec, stream),
+                    "activation packing launch");
+}
+
+dp_status dpl_unpack_activations(int64_t tokens, int64_t dim, dp_dtype dtype, const void* codes, int64_t ld_codes,
+                                 const void* scales, int64_t ld_scales, void* x, int64_t ld, hipStream_t stream) {
+    const char* where = "dpl_unpack_activations";
+    dp_status s = check_packed(where, tokens, dim, dtype, codes, ld_codes, scales, ld_scales);
+    if (s == DP_OK) s = check_rows(where, "x", x, tokens, dim, ld, esize(dtype));
+    if (s != DP_OK) return s;
+    const bool vec = vec_rows(x, ld, esize(dtype), 16) && vec_rows(codes, ld_codes, 1, 16);
+    return launched(dpk::launch_unpack(dtype, tokens, dim, codes, ld_codes, scales, ld_scales, x, ld, vec, stream),
+                    "activation unpacking launch");
 }
 
 }  // extern "C"

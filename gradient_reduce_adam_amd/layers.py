@@ -18,16 +18,45 @@ from typing import Optional, Sequence
 from . import DP_BF16, DP_F16, DP_F32, _check, _stream, lib
 
 DPL_MAX_TOKENS = 1 << 24
-DPL_MAX_NORM_DIM = 16384
+DPL_MAX_NORM_DIM = 8192
 DPL_GROUP = 32
 
 # every exported symbol of dplayer.h
-EXPORTS = ("dpl_embed", "dpl_embed_workspace", "dpl_accumulate_embed")
+EXPORTS = ("dpl_embed", "dpl_embed_workspace", "dpl_accumulate_embed", "dpl_block_norm", "dpl_block_norm_workspace",
+           "dpl_accumulate_block_norm", "dpl_pack_activations", "dpl_unpack_activations")
 
 
 class Table(ctypes.Structure):
     _fields_ = [("tensor", ctypes.c_int32), ("id_bytes", ctypes.c_int32), ("dim", ctypes.c_int64),
                 ("scale", ctypes.c_double)]
+
+
+class Norms(ctypes.Structure):
+    _fields_ = [("post_w", ctypes.c_int32), ("post_b", ctypes.c_int32), ("gate", ctypes.c_int32),
+                ("pre_w", ctypes.c_int32), ("pre_b", ctypes.c_int32), ("centered", ctypes.c_int32),
+                ("dim", ctypes.c_int64), ("eps", ctypes.c_double), ("residual_scale", ctypes.c_double)]
+
+
+class NormRows(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_void_p) for k in ("s", "y", "dx", "ds", "dh", "dy")]
+
+
+@dataclass(frozen=True)
+class BlockNorm:
+    """The norms around a block (``dpl_norms``): plan tensors of the weights,
+    biases and the gate, None where there is none."""
+    pre_w: Optional[int] = None
+    pre_b: Optional[int] = None
+    post_w: Optional[int] = None
+    post_b: Optional[int] = None
+    gate: Optional[int] = None
+    centered: bool = False
+    eps: float = 1e-5
+    residual_scale: float = 1.0
+
+    def struct(self, dim: int) -> Norms:
+        at = [-1 if t is None else int(t) for t in (self.post_w, self.post_b, self.gate, self.pre_w, self.pre_b)]
+        return Norms(*at, int(self.centered), dim, self.eps, self.residual_scale)
 
 
 def _register() -> None:
@@ -37,6 +66,12 @@ def _register() -> None:
         "dpl_embed": [vp, ctypes.POINTER(Table), i64, vp, c_int, vp, i64, vp],
         "dpl_embed_workspace": [vp, ctypes.POINTER(Table), i64, PS],
         "dpl_accumulate_embed": [vp, ctypes.POINTER(Table), i64, PP, c_int, PP, i64, i32, i32, vp, sz, vp],
+        "dpl_block_norm": [vp, ctypes.POINTER(Norms), i64, c_int, vp, i64, vp, i64, vp, i64, vp, i64, vp],
+        "dpl_block_norm_workspace": [vp, ctypes.POINTER(Norms), i64, PS],
+        "dpl_accumulate_block_norm": [vp, ctypes.POINTER(Norms), i64, c_int, ctypes.POINTER(NormRows), i64, i32, i32,
+                                      vp, sz, vp],
+        "dpl_pack_activations": [i64, i64, c_int, vp, i64, vp, i64, vp, i64, vp],
+        "dpl_unpack_activations": [i64, i64, c_int, vp, i64, vp, i64, vp, i64, vp],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -147,3 +182,69 @@ def dpl_accumulate_embed(plan, tensor: int, ids: Sequence, dy: Sequence, first: 
     addr, nbytes = _workspace(workspace)
     _check(lib.dpl_accumulate_embed(plan.handle, ctypes.byref(table), tokens, _array(ids), _dtype(dy[0]), _array(dy),
                                     ld, int(bool(first)), int(bool(more)), addr, nbytes, _stream(stream)))
+
+
+# ---- norms around a block ----------------------------------------------------------
+def dpl_block_norm(plan, norms: BlockNorm, h, y, s, x=None, stream=None) -> None:
+    """s = residual_scale * h + gate * N_post(y) and, with a norm before the
+    next block, x = N_pre(s)."""
+    tokens, dim = h.shape
+    lds = [_rows(k, t, tokens, dim, h.dtype) if t is not None else dim
+           for k, t in (("h", h), ("y", y), ("s", s), ("x", x))]
+    d = norms.struct(dim)
+    _check(lib.dpl_block_norm(plan.handle, ctypes.byref(d), tokens, _dtype(h), h.data_ptr(), lds[0], y.data_ptr(),
+                              lds[1], s.data_ptr(), lds[2], x.data_ptr() if x is not None else None, lds[3],
+                              _stream(stream)))
+
+
+def dpl_block_norm_workspace(plan, norms: BlockNorm, dim: int, tokens: int) -> int:
+    return _query(lib.dpl_block_norm_workspace, plan.handle, ctypes.byref(norms.struct(dim)), tokens)
+
+
+def dpl_accumulate_block_norm(plan, norms: BlockNorm, s: Optional[Sequence], y: Optional[Sequence],
+                              dx: Optional[Sequence], ds: Optional[Sequence], dh: Optional[Sequence],
+                              dy: Optional[Sequence], first: bool, workspace, more: bool = False,
+                              stream=None) -> None:
+    """The backward from every replica's rows: dh, dy, and the gradients of
+    the weights and the gate into the accumulators.  None for what is not there
+    or not wanted."""
+    given = {k: None if v is None else _replicas(plan, k, v)
+             for k, v in (("s", s), ("y", y), ("dx", dx), ("ds", ds), ("dh", dh), ("dy", dy))}
+    one = next((v[0] for v in given.values() if v is not None), None)
+    if one is None:
+        raise ValueError("no rows are given")
+    tokens, dim = one.shape
+    ld = _same_stride("rows", [_rows(k, t, tokens, dim, one.dtype) for k, v in given.items() if v is not None
+                               for t in v])
+    rows = (NormRows * plan.n)(*[NormRows(*[v[r].data_ptr() if v is not None else None for v in given.values()])
+                                 for r in range(plan.n)])
+    addr, nbytes = _workspace(workspace)
+    d = norms.struct(dim)
+    _check(lib.dpl_accumulate_block_norm(plan.handle, ctypes.byref(d), tokens, _dtype(one), rows, ld,
+                                         int(bool(first)), int(bool(more)), addr, nbytes, _stream(stream)))
+
+
+# ---- activations in 8 bits -----------------------------------------------------------
+def _packed(codes, scales, tokens: int, dim: int):
+    import torch
+    return (_rows("codes", codes, tokens, dim, torch.uint8),
+            _rows("scales", scales, tokens, -(-dim // DPL_GROUP), torch.uint8))
+
+
+def dpl_pack_activations(x, codes, scales, stream=None) -> None:
+    """x [tokens, dim] as e4m3 bytes, codes [tokens, dim], and a scale byte for
+    32 channels, scales [tokens, ceil(dim / 32)]."""
+    tokens, dim = x.shape
+    ld = _rows("x", x)
+    ld_c, ld_s = _packed(codes, scales, tokens, dim)
+    _check(lib.dpl_pack_activations(tokens, dim, _dtype(x), x.data_ptr(), ld, codes.data_ptr(), ld_c,
+                                    scales.data_ptr(), ld_s, _stream(stream)))
+
+
+def dpl_unpack_activations(codes, scales, x, stream=None) -> None:
+    """The values that codes and scales stand for, into x."""
+    tokens, dim = x.shape
+    ld = _rows("x", x)
+    ld_c, ld_s = _packed(codes, scales, tokens, dim)
+    _check(lib.dpl_unpack_activations(tokens, dim, _dtype(x), codes.data_ptr(), ld_c, scales.data_ptr(), ld_s,
+                                      x.data_ptr(), ld, _stream(stream)))

@@ -57,7 +57,7 @@ extern "C" {
 /* Most tokens of one call (each replica's). */
 #define DPL_MAX_TOKENS (INT64_C(1) << 24)
 /* Widest row of the block norms. */
-#define DPL_MAX_NORM_DIM 16384
+#define DPL_MAX_NORM_DIM 8192
 /* Channels that share one scale in the 8-bit activation format. */
 #define DPL_GROUP 32
 
