@@ -575,7 +575,14 @@ class Plan:
                               more: bool = False, stream=None) -> None:
         dpl_accumulate_block_norm(self, norms, s, y, dx, ds, dh, dy, first, workspace, more, stream)
 
+    def linear_workspace(self, tokens: int, inputs: int, outputs: int, tensor: Optional[int] = None) -> int:
+        return dpl_linear_workspace(self, tokens, inputs, outputs, tensor)
 
-from .layers import (BlockNorm, dpl_accumulate_block_norm, dpl_accumulate_embed, dpl_block_norm,  # noqa: E402
-                     dpl_block_norm_workspace, dpl_embed, dpl_embed_workspace, dpl_pack_activations,
-                     dpl_unpack_activations)
+    def accumulate_linear(self, tensor: int, dy: Sequence, codes: Sequence, scales: Sequence, first: bool,
+                          workspace=None, transposed: bool = False, more: bool = False, stream=None) -> None:
+        dpl_accumulate_linear(self, tensor, dy, codes, scales, first, workspace, transposed, more, stream)
+
+
+from .layers import (BlockNorm, dpl_accumulate_block_norm, dpl_accumulate_embed,  # noqa: E402
+                     dpl_accumulate_linear, dpl_block_norm, dpl_block_norm_workspace, dpl_embed,
+                     dpl_embed_workspace, dpl_linear_workspace, dpl_pack_activations, dpl_unpack_activations)

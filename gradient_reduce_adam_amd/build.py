@@ -18,7 +18,7 @@ HIP_FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
 
 
 SOURCES = ("kernels.hip", "api.cpp", "checkpoint.cpp", "noalloc.hip", "layers.cpp", "embed.hip",
-           "block_norm.hip", "block_grad.hip", "act8.hip")
+           "block_norm.hip", "block_grad.hip", "act8.hip", "linear.hip")
 
 
 def _run(cmd):

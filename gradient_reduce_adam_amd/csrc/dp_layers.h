@@ -57,4 +57,17 @@ hipError_t launch_pack(dp_dtype dt, int64_t tokens, int64_t dim, const void* x, 
 hipError_t launch_unpack(dp_dtype dt, int64_t tokens, int64_t dim, const void* codes, int64_t ld_codes,
                          const void* scales, int64_t ld_scales, void* x, int64_t ld, bool vec, hipStream_t stream);
 
+// ---- weight gradient of a linear layer (linear.hip) -----------------------------
+struct LinearGrad {
+    dpl_linear_rows rows[DP_MAX_REPLICAS];
+    float* acc[DP_MAX_REPLICAS];
+    int64_t tokens, outputs, inputs, ld_dy, ld_codes, ld_scales;
+    int32_t n;
+    bool transposed, overwrite;
+    bool vec;  // rows of dy and codes are aligned to 16 bytes and made of whole 16-byte pieces
+};
+int64_t linear_jobs(int64_t outputs, int64_t inputs, int64_t tokens, int n);  // workgroups of its launch
+size_t linear_workspace(int64_t outputs, int64_t inputs, int64_t tokens, int n);
+hipError_t launch_linear(dp_dtype dt, const LinearGrad& g, void* workspace, hipStream_t stream);
+
 }  // namespace dpk

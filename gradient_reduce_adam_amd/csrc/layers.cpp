@@ -166,6 +166,22 @@ dp_status check_packed(const char* where, int64_t tokens, int64_t dim, dp_dtype 
     return DP_OK;
 }
 
+// ---- weight gradient of a linear layer -------------------------------------------
+dp_status check_linear(const char* where, const dp_plan* plan, const dpl_linear* d, int64_t tokens) {
+    if (!plan || !d) return fail(DP_ERR_INVALID_ARG, "%s: null argument", where);
+    dp_status s = check_tensor(where, plan, d->tensor);
+    if (s == DP_OK) s = check_tokens(where, tokens);
+    if (s != DP_OK) return s;
+    const int64_t most = int64_t{1} << 24, numel = plan->numel[static_cast<size_t>(d->tensor)];
+    if (d->inputs < 1 || d->outputs < 1 || d->inputs > most || d->outputs > most || d->inputs * d->outputs != numel)
+        return fail(DP_ERR_INVALID_ARG, "%s: tensor %d of %lld elements is no %lld x %lld matrix", where, d->tensor,
+                    ll(numel), ll(d->outputs), ll(d->inputs));
+    if (dpk::linear_jobs(d->outputs, d->inputs, tokens, plan->n) > (int64_t{1} << 22))
+        return fail(DP_ERR_INVALID_ARG, "%s: a %lld x %lld matrix is too large for one call", where, ll(d->outputs),
+                    ll(d->inputs));
+    return DP_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -349,6 +365,56 @@ dp_status dpl_unpack_activations(int64_t tokens, int64_t dim, dp_dtype dtype, co
     const bool vec = vec_rows(x, ld, esize(dtype), 16) && vec_rows(codes, ld_codes, 1, 16);
     return launched(dpk::launch_unpack(dtype, tokens, dim, codes, ld_codes, scales, ld_scales, x, ld, vec, stream),
                     "activation unpacking launch");
+}
+
+dp_status dpl_linear_workspace(const dp_plan* plan, const dpl_linear* linear, int64_t tokens, size_t* bytes) {
+    dp_status s = check_linear("dpl_linear_workspace", plan, linear, tokens);
+    if (s == DP_OK && !bytes) s = fail(DP_ERR_INVALID_ARG, "dpl_linear_workspace: null argument");
+    if (s != DP_OK) return s;
+    *bytes = dpk::linear_workspace(linear->outputs, linear->inputs, tokens, plan->n);
+    return DP_OK;
+}
+
+dp_status dpl_accumulate_linear(dp_plan* plan, const dpl_linear* linear, int64_t tokens, dp_dtype dtype,
+                                const dpl_linear_rows* rows, int64_t ld_codes, int64_t ld_scales, int64_t ld_dy,
+                                int32_t first, int32_t more, void* workspace, size_t workspace_bytes,
+                                hipStream_t stream) {
+    const char* where = "dpl_accumulate_linear";
+    dp_status s = check_linear(where, plan, linear, tokens);
+    if (s != DP_OK) return s;
+    if (dtype != DP_BF16 && dtype != DP_F16) return fail(DP_ERR_INVALID_ARG, "%s: dtype must be DP_BF16 or DP_F16", where);
+    if (!rows) return fail(DP_ERR_INVALID_ARG, "%s: null argument", where);
+    dpk::LinearGrad g{};
+    g.vec = linear->inputs % 16 == 0 && linear->outputs % 8 == 0;
+    for (int32_t r = 0; r < plan->n; ++r) {
+        s = check_rows(where, "codes", rows[r].codes, tokens, linear->inputs, ld_codes, 1);
+        if (s == DP_OK)
+            s = check_rows(where, "scales", rows[r].scales, tokens, (linear->inputs + DPL_GROUP - 1) / DPL_GROUP, ld_scales, 1);
+        if (s == DP_OK) s = check_rows(where, "dy", rows[r].dy, tokens, linear->outputs, ld_dy, 2);
+        if (s != DP_OK) return s;
+        g.vec = g.vec && vec_rows(rows[r].codes, ld_codes, 1, 16) && vec_rows(rows[r].dy, ld_dy, 2, 16);
+        g.rows[r] = rows[r];
+    }
+    s = check_workspace(where, workspace, workspace_bytes,
+                        dpk::linear_workspace(linear->outputs, linear->inputs, tokens, plan->n));
+    if (s != DP_OK) return s;
+    bool overwrite = false;
+    s = dpapi::part_begin(plan, &linear->tensor, 1, first != 0, where, g.acc, &overwrite);
+    if (s == DP_OK) s = check_acc(where, g.acc, plan->n);
+    if (s != DP_OK) return s;
+    g.tokens = tokens;
+    g.outputs = linear->outputs;
+    g.inputs = linear->inputs;
+    g.ld_dy = ld_dy;
+    g.ld_codes = ld_codes;
+    g.ld_scales = ld_scales;
+    g.n = plan->n;
+    g.transposed = linear->transposed != 0;
+    g.overwrite = overwrite;
+    s = launched(dpk::launch_linear(dtype, g, workspace, stream), "linear gradient launch");
+    if (s != DP_OK) return s;
+    dpapi::part_end(plan, &linear->tensor, 1, first != 0, more != 0);
+    return DP_OK;
 }
 
 }  // extern "C"

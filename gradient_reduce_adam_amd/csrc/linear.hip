@@ -1,0 +1,390 @@
+// gfx950 kernel of a linear layer's weight gradient from its 8-bit input:
+// G[o][i] = sum over the tokens t of dy[t][o] x[t][i], added to (or written
+// over) binary32 accumulators.
+//
+// A product on the matrix cores, with the token axis summed: both operands lie
+// with that axis slow, so a tile of 64 tokens by 256 columns of each is staged
+// in LDS as it lies in memory, in 16 bits, and fragments are read with the transposing LDS load,
+// which gives a lane four consecutive tokens of its column.
+//  - x is read as codes and scale bytes, half the bytes of 16 bits, and decoded
+//    on the way to LDS (codes times a power of two are exact in 16 bits: one
+//    conversion instruction for two).
+//  - A workgroup of 8 waves makes a tile of 256 x 256 weights, each wave 128 x
+//    64 as 4 x 2 products of 32 x 32 x 16, in 128 accumulator registers a
+//    lane.  Two LDS buffers (128 KiB): while one is multiplied, the next 64
+//    tokens are written to the other, and those after them are loaded.
+//  - LDS rows are 512 bytes, so four consecutive tokens of one column would
+//    hit the same banks: 64-byte slots are permuted by the token's low two
+//    bits (slot ^ (token & 3)), which spreads every fragment read over all
+//    banks.
+// The matrix cores bound it; the LDS reads (192 KiB a step, against 8.4 MFLOP)
+// come next.
+//
+// Few tiles and many tokens leave CUs idle, so the token axis is then split
+// over several workgroups, whose tiles go to the workspace and are added in
+// order by a second launch.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "dp_device.h"
+#include "dp_layers.h"
+
+namespace dpk {
+namespace {
+
+constexpr int kTileCols = 256;  // columns of either operand per workgroup
+constexpr int kTileTokens = 64;
+constexpr int kThreads = 512;
+constexpr int kTileBytes = kTileTokens * kTileCols * 2;
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+struct LinearArgs {
+    const void* dy[DP_MAX_REPLICAS];
+    const unsigned char* codes[DP_MAX_REPLICAS];
+    const unsigned char* scales[DP_MAX_REPLICAS];
+    float* acc[DP_MAX_REPLICAS];
+    float* part;  // [splits][n][outputs * inputs] with splits > 1
+    int64_t tokens, ld_dy, ld_codes, ld_scales;
+    int64_t outputs, inputs;
+    int32_t n, tiles_o, tiles_i, splits;
+    int64_t split_tokens;  // of one split, a multiple of kTileTokens
+    bool overwrite;
+};
+
+// Byte offset in a tile of column c (a multiple of 8) of token k.
+__device__ __forceinline__ int at(int k, int c) { return k * (2 * kTileCols) + ((2 * c) ^ ((k & 3) << 6)); }
+
+template <dp_dtype DT>
+__device__ __forceinline__ unsigned int decode2(unsigned int codes, float unit, int half) {
+    if constexpr (DT == DP_BF16) {
+        return half ? __builtin_bit_cast(unsigned int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, unit, true))
+                    : __builtin_bit_cast(unsigned int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, unit, false));
+    } else {
+        return half ? __builtin_bit_cast(unsigned int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(codes, unit, true))
+                    : __builtin_bit_cast(unsigned int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(codes, unit, false));
+    }
+}
+
+template <dp_dtype DT>
+__device__ __forceinline__ f32x16 mma(s16x8 a, s16x8 b, f32x16 c) {
+    if constexpr (DT == DP_BF16)
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
+typedef __attribute__((address_space(3))) unsigned char lds_u8;
+
+// Fragments: of 32 columns and 16 tokens lane l gets column l % 32 and tokens
+// 8 (l / 32) + 0 .. 7.  One transposing load takes a 4 x 16 piece through 16 lanes: lane
+// i of them addresses token i / 4, columns 4 (i % 4), and receives column i of
+// all four tokens.  `place` is this lane's offset in a tile for columns from c0
+// (a multiple of 32); tokens from k0 (a multiple of 16) lie k0 rows further.
+__device__ __forceinline__ int place(int c0) {
+    const int l = threadIdx.x & 63, i = l & 15;
+    const int k = 8 * (l >> 5) + (i >> 2), c = c0 + (l & 16) + 4 * (i & 3);
+    return k * (2 * kTileCols) + ((2 * c) ^ ((k & 3) << 6));
+}
+__device__ __forceinline__ s16x8 fragment(const lds_u8* p) {
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * 2 * kTileCols));
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// One workgroup's operands and place.
+struct Job {
+    const unsigned char* dy;
+    const unsigned char* codes;
+    const unsigned char* scales;
+    int64_t o0, i0;  // first output and input of the tile
+};
+
+// ---- staging -------------------------------------------------------------------
+// A thread's share of one tile on its way through registers: dy as 4 pieces of 8
+// elements (piece q * 512 + thread: token piece / 32), x as the codes of 16
+// columns of tokens thread / 16 and thread / 16 + 32, with their scale bytes.
+struct Stage {
+    u32x4 dy[4];
+    u32x4 codes[2];
+    unsigned int unit[2];
+};
+
+// Every token of [t, t + 64) exists.  Columns past the last are read from the
+// last whole piece: their products are not stored.
+__device__ __forceinline__ void load_full(const LinearArgs& a, const Job& j, int64_t t, Stage& s) {
+    int64_t c = j.o0 + ((threadIdx.x & 31) << 3);
+    c = c < a.outputs ? c : a.outputs - 8;
+    const unsigned char* p = j.dy + 2 * ((t + (threadIdx.x >> 5)) * a.ld_dy + c);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) s.dy[q] = gload<u32x4>(p + q * 32 * a.ld_dy, 0);
+    c = j.i0 + ((threadIdx.x & 15) << 4);
+    c = c < a.inputs ? c : a.inputs - 16;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int64_t k = t + (threadIdx.x >> 4) + 32 * h;
+        s.codes[h] = gload<u32x4>(j.codes + k * a.ld_codes + c, 0);
+        s.unit[h] = gload<unsigned char>(j.scales, k * a.ld_scales + c / DPL_GROUP);
+    }
+}
+
+// Tokens [t, end), any alignment, zeros for tokens and columns that do not exist.
+__device__ __forceinline__ void load_checked(const LinearArgs& a, const Job& j, int64_t t, int64_t end, Stage& s) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const int id = q * kThreads + threadIdx.x, k = id >> 5, c = (id & 31) << 3;
+        const int64_t left = a.outputs - (j.o0 + c);
+        const int valid = t + k < end ? left >= 8 ? 8 : left > 0 ? static_cast<int>(left) : 0 : 0;
+        const unsigned short* p = reinterpret_cast<const unsigned short*>(j.dy) + (t + k) * a.ld_dy + j.o0 + c;
+        unsigned int e[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e[i] = i < valid ? gload<unsigned short>(p, i) : 0;
+        s.dy[q] = u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int k = (threadIdx.x >> 4) + 32 * h, c = (threadIdx.x & 15) << 4;
+        const int64_t left = a.inputs - (j.i0 + c);
+        const int valid = t + k < end ? left >= 16 ? 16 : left > 0 ? static_cast<int>(left) : 0 : 0;
+        const unsigned char* p = j.codes + (t + k) * a.ld_codes + j.i0 + c;
+        unsigned int e[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) e[i] = i < valid ? gload<unsigned char>(p, i) : 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s.codes[h][i] = e[4 * i] | e[4 * i + 1] << 8 | e[4 * i + 2] << 16 | e[4 * i + 3] << 24;
+        s.unit[h] = valid ? gload<unsigned char>(j.scales, (t + k) * a.ld_scales + (j.i0 + c) / DPL_GROUP) : 127;
+    }
+}
+
+// Half h of a stage into a pair of tiles (dy, x behind it): `dy`, `x` are this
+// thread's places for token 0 of each.
+template <dp_dtype DT>
+__device__ __forceinline__ void store_half(const Stage& s, int h, lds_u8* dy, lds_u8* x) {
+#pragma unroll
+    for (int q = 2 * h; q < 2 * h + 2; ++q) *(lds_u32x4*)(dy + q * 16 * (2 * kTileCols)) = s.dy[q];
+    const float unit = __builtin_bit_cast(float, s.unit[h] << 23);
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+        *(lds_u32x4*)(x + h * 32 * (2 * kTileCols) + 16 * e) =
+            u32x4{decode2<DT>(s.codes[h][2 * e], unit, 0), decode2<DT>(s.codes[h][2 * e], unit, 1),
+                  decode2<DT>(s.codes[h][2 * e + 1], unit, 0), decode2<DT>(s.codes[h][2 * e + 1], unit, 1)};
+}
+
+// Rows of the result are outputs (columns inputs), or inputs with kSwap; the
+// lanes of a wave run along the columns.  kVec: every row of dy and codes is
+// aligned to 16 bytes and made of whole 16-byte pieces, and all tiles but the
+// first, which takes the odd tokens, are loaded without checks.
+template <dp_dtype DT, bool kSwap, bool kVec>
+__global__ void __launch_bounds__(kThreads) k_linear(LinearArgs a) {
+    __shared__ __align__(1024) unsigned char lds[4 * kTileBytes];  // two turns of a dy and an x tile
+    // tiles in the order of their operands' reuse: neighbouring workgroups of one
+    // XCD (every eighth) take tiles next to each other
+    const int64_t jobs = static_cast<int64_t>(gridDim.x);
+    const int64_t per = jobs / 8, extra = jobs % 8, xcd = blockIdx.x % 8, in = blockIdx.x / 8;
+    int64_t id = xcd * per + (xcd < extra ? xcd : extra) + in;
+    const int tiles = a.tiles_o * a.tiles_i;
+    const int tile = static_cast<int>(id % tiles);
+    id /= tiles;
+    const int r = static_cast<int>(id % a.n), split = static_cast<int>(id / a.n);
+    const int band = tile / (8 * a.tiles_i), rows = a.tiles_o - 8 * band < 8 ? a.tiles_o - 8 * band : 8;
+    const int within = tile - band * 8 * a.tiles_i;
+    Job j;
+    j.dy = static_cast<const unsigned char*>(a.dy[r]);
+    j.codes = a.codes[r];
+    j.scales = a.scales[r];
+    j.o0 = static_cast<int64_t>(8 * band + within % rows) * kTileCols;
+    j.i0 = static_cast<int64_t>(within / rows) * kTileCols;
+    const int64_t t0 = split * a.split_tokens;
+    const int64_t t1 = t0 + a.split_tokens < a.tokens ? t0 + a.split_tokens : a.tokens;
+
+    const int w = threadIdx.x >> 6, l = threadIdx.x & 63;
+    const int wm = (w >> 2) * 128, wn = (w & 3) * 64;  // this wave's part of the tile: rows, columns
+    f32x16 c[4][2];
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) c[m][n][e] = 0.0f;
+
+    // Fragments are read one group of 16 tokens ahead of their products, also
+    // across the barrier: while group 3 of a tile is multiplied, group 0 of the
+    // next one is read.  A tile is loaded into registers one step before it is
+    // written to LDS, and two before it is multiplied.
+    lds_u8* const base = (lds_u8*)lds;
+    int left[4], right[2];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) left[m] = place(wm + 32 * m) + (kSwap ? kTileBytes : 0);
+#pragma unroll
+    for (int n = 0; n < 2; ++n) right[n] = place(wn + 32 * n) + (kSwap ? 0 : kTileBytes);
+    const int put_dy = at(threadIdx.x >> 5, (threadIdx.x & 31) << 3);
+    const int put_x = kTileBytes + at(threadIdx.x >> 4, (threadIdx.x & 15) << 4);
+    s16x8 p[2][4], q[2][2];
+    auto read = [&](int turn, int k, int b) {  // turn: byte offset of the pair of tiles
+        const lds_u8* from = base + turn + k * 16 * (2 * kTileCols);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) p[b][m] = fragment(from + left[m]);
+#pragma unroll
+        for (int n = 0; n < 2; ++n) q[b][n] = fragment(from + right[n]);
+    };
+    auto multiply = [&](int b) {
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+            for (int n = 0; n < 2; ++n) c[m][n] = mma<DT>(p[b][m], q[b][n], c[m][n]);
+    };
+    const int64_t full = t1 > t0 ? (t1 - t0 - 1) / kTileTokens : -1;  // whole tiles behind the first one
+    if (full >= 0) {
+        Stage s;
+        int64_t t = t1 - full * kTileTokens;  // the next tile to load
+        const int64_t last = t1 - kTileTokens;
+        load_checked(a, j, t0, t, s);
+        store_half<DT>(s, 0, base + put_dy, base + put_x);
+        store_half<DT>(s, 1, base + put_dy, base + put_x);
+        auto load = [&]() {  // past the end the last tile again, which is not used
+            if (full == 0) return;
+            if constexpr (kVec) load_full(a, j, t < last ? t : last, s);
+            else load_checked(a, j, t < last ? t : last, t1, s);
+            t += kTileTokens;
+        };
+        load();
+        __syncthreads();
+        int turn = 0;
+        read(turn, 0, 0);
+        for (int64_t i = 0; i <= full; ++i) {
+            const int other = turn ^ (2 * kTileBytes);
+            read(turn, 1, 1);
+            store_half<DT>(s, 0, base + other + put_dy, base + other + put_x);
+            multiply(0);
+            read(turn, 2, 0);
+            store_half<DT>(s, 1, base + other + put_dy, base + other + put_x);
+            multiply(1);
+            read(turn, 3, 1);
+            load();
+            multiply(0);
+            __syncthreads();
+            turn = other;
+            read(turn, 0, 0);
+            multiply(1);
+        }
+    }
+
+    // element e of a 32 x 32 product: row 8 (e / 4) + 4 (l / 32) + e % 4, column l % 32
+    const int64_t row0 = (kSwap ? j.i0 : j.o0) + wm + 4 * (l >> 5), col0 = (kSwap ? j.o0 : j.i0) + wn + (l & 31);
+    const int64_t height = kSwap ? a.inputs : a.outputs, width = kSwap ? a.outputs : a.inputs;
+    const bool over = a.overwrite || a.splits > 1;
+    float* out = a.splits > 1 ? a.part + (static_cast<int64_t>(split) * a.n + r) * height * width : a.acc[r];
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            __builtin_amdgcn_sched_barrier(0);
+            const int64_t col = col0 + 32 * n, row = row0 + 32 * m;
+            float* p = out + row * width + col;
+            if (col >= width) continue;
+            float old[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int d = 8 * (e >> 2) + (e & 3);
+                old[e] = !over && row + d < height ? gload<float>(p + d * width, 0) : 0.0f;
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int d = 8 * (e >> 2) + (e & 3);
+                if (row + d < height) gstore<float>(p + d * width, 0, over ? c[m][n][e] : old[e] + c[m][n][e]);
+            }
+        }
+}
+
+// Adds the splits' tiles of every replica, in order, into the accumulators.
+__global__ void __launch_bounds__(256) k_linear_join(LinearArgs a) {
+    const int64_t size = a.outputs * a.inputs;
+    const int r = blockIdx.y;
+    const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
+    const int64_t left = size - i;
+    const int valid = left >= 4 ? 4 : left > 0 ? static_cast<int>(left) : 0;
+    const bool vec = size % 4 == 0;
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int k = 0; k < a.splits; ++k) {
+        float v[4];
+        load_n<DP_F32, 4>(a.part + (static_cast<int64_t>(k) * a.n + r) * size, i, valid, vec, v);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[e] += v[e];
+    }
+    const bool vec_acc = (reinterpret_cast<uintptr_t>(a.acc[r]) & 15) == 0;
+    if (!a.overwrite) {
+        float v[4];
+        load_n<DP_F32, 4>(a.acc[r], i, valid, vec_acc, v);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[e] = v[e] + s[e];
+    }
+    store_n<DP_F32, 4>(a.acc[r], i, valid, vec_acc, s);
+}
+
+// Workgroups that share the tokens of one tile: as many as fill the chip's
+// 256 CUs, each with at least 512 tokens.
+int splits_of(int64_t outputs, int64_t inputs, int64_t tokens, int n) {
+    const int64_t tiles = ((outputs + kTileCols - 1) / kTileCols) * ((inputs + kTileCols - 1) / kTileCols) * n;
+    const int64_t most = tokens / 512, want = 256 / tiles;
+    const int64_t s = want < most ? want : most;
+    return s < 1 ? 1 : static_cast<int>(s);
+}
+
+}  // namespace
+
+int64_t linear_jobs(int64_t outputs, int64_t inputs, int64_t tokens, int n) {
+    const int64_t tiles = ((outputs + kTileCols - 1) / kTileCols) * ((inputs + kTileCols - 1) / kTileCols) * n;
+    return tiles * splits_of(outputs, inputs, tokens, n);
+}
+
+size_t linear_workspace(int64_t outputs, int64_t inputs, int64_t tokens, int n) {
+    const int64_t s = splits_of(outputs, inputs, tokens, n);
+    return s > 1 ? static_cast<size_t>(4 * s * n) * static_cast<size_t>(outputs * inputs) : 0;
+}
+
+hipError_t launch_linear(dp_dtype dt, const LinearGrad& g, void* workspace, hipStream_t stream) {
+    LinearArgs a{};
+    for (int r = 0; r < g.n; ++r) {
+        a.dy[r] = g.rows[r].dy;
+        a.codes[r] = static_cast<const unsigned char*>(g.rows[r].codes);
+        a.scales[r] = static_cast<const unsigned char*>(g.rows[r].scales);
+        a.acc[r] = g.acc[r];
+    }
+    a.part = static_cast<float*>(workspace);
+    a.tokens = g.tokens;
+    a.ld_dy = g.ld_dy;
+    a.ld_codes = g.ld_codes;
+    a.ld_scales = g.ld_scales;
+    a.outputs = g.outputs;
+    a.inputs = g.inputs;
+    a.n = g.n;
+    a.tiles_o = static_cast<int32_t>((g.outputs + kTileCols - 1) / kTileCols);
+    a.tiles_i = static_cast<int32_t>((g.inputs + kTileCols - 1) / kTileCols);
+    a.splits = splits_of(g.outputs, g.inputs, g.tokens, g.n);
+    a.split_tokens = ((g.tokens + a.splits - 1) / a.splits + kTileTokens - 1) / kTileTokens * kTileTokens;
+    a.overwrite = g.overwrite;
+    const dim3 grid(static_cast<unsigned>(linear_jobs(g.outputs, g.inputs, g.tokens, g.n)));
+#define DP_GO(D, S)                                                                                              \
+    if (dt == D && g.transposed == S) {                                                                         \
+        if (g.vec) hipLaunchKernelGGL((k_linear<D, S, true>), grid, dim3(kThreads), 0, stream, a);              \
+        else hipLaunchKernelGGL((k_linear<D, S, false>), grid, dim3(kThreads), 0, stream, a);                   \
+    }
+    DP_GO(DP_BF16, false)
+    DP_GO(DP_BF16, true)
+    DP_GO(DP_F16, false)
+    DP_GO(DP_F16, true)
+#undef DP_GO
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.splits == 1) return e;
+    const dim3 jgrid(static_cast<unsigned>((g.outputs * g.inputs + 1023) / 1024), static_cast<unsigned>(g.n));
+    hipLaunchKernelGGL(k_linear_join, jgrid, dim3(256), 0, stream, a);
+    return hipGetLastError();
+}
+
+}  // namespace dpk

@@ -23,7 +23,8 @@ DPL_GROUP = 32
 
 # every exported symbol of dplayer.h
 EXPORTS = ("dpl_embed", "dpl_embed_workspace", "dpl_accumulate_embed", "dpl_block_norm", "dpl_block_norm_workspace",
-           "dpl_accumulate_block_norm", "dpl_pack_activations", "dpl_unpack_activations")
+           "dpl_accumulate_block_norm", "dpl_pack_activations", "dpl_unpack_activations",
+           "dpl_linear_workspace", "dpl_accumulate_linear")
 
 
 class Table(ctypes.Structure):
@@ -59,6 +60,15 @@ class BlockNorm:
         return Norms(*at, int(self.centered), dim, self.eps, self.residual_scale)
 
 
+class Linear(ctypes.Structure):
+    _fields_ = [("tensor", ctypes.c_int32), ("transposed", ctypes.c_int32), ("inputs", ctypes.c_int64),
+                ("outputs", ctypes.c_int64)]
+
+
+class LinearRows(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_void_p) for k in ("codes", "scales", "dy")]
+
+
 def _register() -> None:
     vp, i32, i64, sz, c_int = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
     PP, PS = ctypes.POINTER(vp), ctypes.POINTER(sz)
@@ -72,6 +82,9 @@ def _register() -> None:
                                       vp, sz, vp],
         "dpl_pack_activations": [i64, i64, c_int, vp, i64, vp, i64, vp, i64, vp],
         "dpl_unpack_activations": [i64, i64, c_int, vp, i64, vp, i64, vp, i64, vp],
+        "dpl_linear_workspace": [vp, ctypes.POINTER(Linear), i64, PS],
+        "dpl_accumulate_linear": [vp, ctypes.POINTER(Linear), i64, c_int, ctypes.POINTER(LinearRows), i64, i64, i64,
+                                  i32, i32, vp, sz, vp],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -248,3 +261,30 @@ def dpl_unpack_activations(codes, scales, x, stream=None) -> None:
     ld_c, ld_s = _packed(codes, scales, tokens, dim)
     _check(lib.dpl_unpack_activations(tokens, dim, _dtype(x), codes.data_ptr(), ld_c, scales.data_ptr(), ld_s,
                                       x.data_ptr(), ld, _stream(stream)))
+
+
+def dpl_linear_workspace(plan, tokens: int, inputs: int, outputs: int, tensor: Optional[int] = None) -> int:
+    """The bytes for a tensor of inputs x outputs elements (the first such one
+    of the plan unless given)."""
+    if tensor is None:
+        tensor = next((i for i, x in enumerate(plan.numel) if x == inputs * outputs), -1)
+    return _query(lib.dpl_linear_workspace, plan.handle, ctypes.byref(Linear(tensor, 0, inputs, outputs)), tokens)
+
+
+def dpl_accumulate_linear(plan, tensor: int, dy: Sequence, codes: Sequence, scales: Sequence, first: bool,
+                          workspace=None, transposed: bool = False, more: bool = False, stream=None) -> None:
+    """A linear layer's weight gradient from every replica's output gradients
+    dy [tokens, outputs] and packed inputs, into the accumulators of plan tensor
+    ``tensor``: outputs x inputs, or inputs x outputs if ``transposed``."""
+    import torch
+    dy, codes, scales = _replicas(plan, "dy", dy), _replicas(plan, "codes", codes), _replicas(plan, "scales", scales)
+    (tokens, outputs), inputs = dy[0].shape, codes[0].shape[1]
+    ld_dy = _same_stride("dy", [_rows("dy", t, tokens, outputs, dy[0].dtype) for t in dy])
+    ld_c = _same_stride("codes", [_rows("codes", t, tokens, inputs, torch.uint8) for t in codes])
+    ld_s = _same_stride("scales", [_rows("scales", t, tokens, -(-inputs // DPL_GROUP), torch.uint8) for t in scales])
+    rows = (LinearRows * plan.n)(*[LinearRows(codes[r].data_ptr(), scales[r].data_ptr(), dy[r].data_ptr())
+                                   for r in range(plan.n)])
+    addr, nbytes = _workspace(workspace)
+    d = Linear(tensor, int(bool(transposed)), inputs, outputs)
+    _check(lib.dpl_accumulate_linear(plan.handle, ctypes.byref(d), tokens, _dtype(dy[0]), rows, ld_c, ld_s, ld_dy,
+                                     int(bool(first)), int(bool(more)), addr, nbytes, _stream(stream)))
