@@ -12,10 +12,12 @@ a :class:`Plan` (whose methods of the same purpose call these functions).
 from __future__ import annotations
 
 import ctypes
-from dataclasses import dataclass
+from dataclasses import dataclass, field
 from typing import Optional, Sequence
 
-from . import DP_BF16, DP_F16, DP_F32, _check, _stream, lib
+import torch
+
+from . import DP_BF16, DP_F16, DP_F32, _check, lib
 
 DPL_MAX_TOKENS = 1 << 24
 DPL_MAX_NORM_DIM = 8192
@@ -54,10 +56,14 @@ class BlockNorm:
     centered: bool = False
     eps: float = 1e-5
     residual_scale: float = 1.0
+    _refs: dict = field(default_factory=dict, init=False, repr=False, compare=False)  # by the rows' width
 
-    def struct(self, dim: int) -> Norms:
-        at = [-1 if t is None else int(t) for t in (self.post_w, self.post_b, self.gate, self.pre_w, self.pre_b)]
-        return Norms(*at, int(self.centered), dim, self.eps, self.residual_scale)
+    def ref(self, dim: int):
+        """A reference to the ``dpl_norms`` of these norms on rows of dim elements."""
+        if dim not in self._refs:
+            at = [-1 if t is None else int(t) for t in (self.post_w, self.post_b, self.gate, self.pre_w, self.pre_b)]
+            self._refs[dim] = ctypes.byref(Norms(*at, int(self.centered), dim, self.eps, self.residual_scale))
+        return self._refs[dim]
 
 
 class Linear(ctypes.Structure):
@@ -95,32 +101,43 @@ def _register() -> None:
 _register()
 
 
+_DTYPES = {torch.bfloat16: DP_BF16, torch.float16: DP_F16, torch.float32: DP_F32}
+_IDS = (torch.int32, torch.int64)
+# a launch costs the host about 4 us; the stream's handle without a Stream object saves 2 more
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(stream, device: int) -> int:
+    if stream is None:
+        return _raw_stream(device) if _raw_stream else torch.cuda.current_stream(device).cuda_stream
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
 def _dtype(t) -> int:
-    import torch
-    code = {torch.bfloat16: DP_BF16, torch.float16: DP_F16, torch.float32: DP_F32}.get(t.dtype)
+    code = _DTYPES.get(t.dtype)
     if code is None:
         raise ValueError(f"activations are bfloat16, float16 or float32, not {t.dtype}")
     return code
 
 
-def _here(name: str, t) -> None:
-    import torch
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+def _elsewhere(name: str, t, device: int):
+    return ValueError(f"{name} is on {t.device}, the current device is cuda:{device}")
 
 
-def _rows(name: str, t, tokens: Optional[int] = None, dim: Optional[int] = None, dtype=None) -> int:
+def _rows(name: str, t, device: int, tokens: Optional[int] = None, dim: Optional[int] = None, dtype=None) -> int:
     """The row stride of an activation tensor, after checking it."""
-    _here(name, t)
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be [tokens, dim] with contiguous rows, not {tuple(t.shape)} of strides "
+    if t.get_device() != device:
+        raise _elsewhere(name, t, device)
+    shape = t.shape
+    if len(shape) != 2 or (t.stride(1) != 1 and shape[1] > 1):
+        raise ValueError(f"{name} must be [tokens, dim] with contiguous rows, not {tuple(shape)} of strides "
                          f"{t.stride()}")
-    if (tokens is not None and t.shape[0] != tokens) or (dim is not None and t.shape[1] != dim):
-        raise ValueError(f"{name} is {tuple(t.shape)}, expected ({tokens}, {dim})")
+    if (tokens is not None and shape[0] != tokens) or (dim is not None and shape[1] != dim):
+        raise ValueError(f"{name} is {tuple(shape)}, expected ({tokens}, {dim})")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} is {t.dtype}, expected {dtype}")
     # the stride of a single row is never used and may be anything
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return t.stride(0) if shape[0] > 1 else shape[1]
 
 
 def _same_stride(name: str, lds: Sequence[int]) -> int:
@@ -129,11 +146,11 @@ def _same_stride(name: str, lds: Sequence[int]) -> int:
     return lds[0]
 
 
-def _ids(name: str, t, tokens: Optional[int] = None) -> int:
+def _ids(name: str, t, device: int, tokens: Optional[int] = None) -> int:
     """The element size of a token id tensor, after checking it."""
-    import torch
-    _here(name, t)
-    if t.dtype not in (torch.int32, torch.int64) or t.dim() != 1 or not t.is_contiguous():
+    if t.get_device() != device:
+        raise _elsewhere(name, t, device)
+    if t.dtype not in _IDS or t.dim() != 1 or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous 1-D int32 or int64 tensor")
     if tokens is not None and t.shape[0] != tokens:
         raise ValueError(f"{name} holds {t.shape[0]} tokens, expected {tokens}")
@@ -141,7 +158,7 @@ def _ids(name: str, t, tokens: Optional[int] = None) -> int:
 
 
 def _replicas(plan, name: str, xs: Sequence) -> Sequence:
-    xs = list(xs)
+    xs = tuple(xs)
     if len(xs) != plan.n:
         raise ValueError(f"{name}: {len(xs)} tensors for {plan.n} replicas")
     return xs
@@ -151,10 +168,11 @@ def _array(xs: Sequence):
     return (ctypes.c_void_p * len(xs))(*[x.data_ptr() for x in xs])
 
 
-def _workspace(workspace):
+def _workspace(workspace, device: int):
     if workspace is None:
         return None, 0
-    _here("workspace", workspace)
+    if workspace.get_device() != device:
+        raise _elsewhere("the workspace", workspace, device)
     if not workspace.is_contiguous():
         raise ValueError("the workspace must be contiguous")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
@@ -170,11 +188,11 @@ def _query(fn, *args) -> int:
 def dpl_embed(plan, tensor: int, ids, out, scale: float = 1.0, stream=None) -> None:
     """out[t] = scale * W[ids[t]] from plan tensor ``tensor``, rows of
     ``out.shape[1]`` parameters; zeros for an id outside the table."""
-    size = _ids("ids", ids)
-    ld = _rows("out", out, ids.shape[0])
-    table = Table(tensor, size, out.shape[1], scale)
-    _check(lib.dpl_embed(plan.handle, ctypes.byref(table), ids.shape[0], ids.data_ptr(), _dtype(out), out.data_ptr(),
-                         ld, _stream(stream)))
+    dev = torch.cuda.current_device()
+    size, tokens = _ids("ids", ids, dev), ids.shape[0]
+    ld = _rows("out", out, dev, tokens)
+    _check(lib.dpl_embed(plan.handle, ctypes.byref(Table(tensor, size, out.shape[1], scale)), tokens, ids.data_ptr(),
+                         _dtype(out), out.data_ptr(), ld, _stream_of(stream, dev)))
 
 
 def dpl_embed_workspace(plan, tensor: int, dim: int, tokens: int) -> int:
@@ -185,33 +203,35 @@ def dpl_accumulate_embed(plan, tensor: int, ids: Sequence, dy: Sequence, first: 
                          more: bool = False, stream=None) -> None:
     """The lookup's gradient from every replica's token ids and gradient rows,
     into the accumulators of plan tensor ``tensor``."""
+    dev = torch.cuda.current_device()
     ids, dy = _replicas(plan, "ids", ids), _replicas(plan, "dy", dy)
     tokens, dim = dy[0].shape
-    sizes = {_ids("ids", x, tokens) for x in ids}
+    sizes = {_ids("ids", x, dev, tokens) for x in ids}
     if len(sizes) > 1:
         raise ValueError("ids: every replica's must have the same type")
-    ld = _same_stride("dy", [_rows("dy", x, tokens, dim, dy[0].dtype) for x in dy])
+    ld = _same_stride("dy", [_rows("dy", x, dev, tokens, dim, dy[0].dtype) for x in dy])
     table = Table(tensor, sizes.pop(), dim, scale)
-    addr, nbytes = _workspace(workspace)
+    addr, nbytes = _workspace(workspace, dev)
     _check(lib.dpl_accumulate_embed(plan.handle, ctypes.byref(table), tokens, _array(ids), _dtype(dy[0]), _array(dy),
-                                    ld, int(bool(first)), int(bool(more)), addr, nbytes, _stream(stream)))
+                                    ld, bool(first), bool(more), addr, nbytes, _stream_of(stream, dev)))
 
 
 # ---- norms around a block ----------------------------------------------------------
 def dpl_block_norm(plan, norms: BlockNorm, h, y, s, x=None, stream=None) -> None:
     """s = residual_scale * h + gate * N_post(y) and, with a norm before the
     next block, x = N_pre(s)."""
+    dev = torch.cuda.current_device()
     tokens, dim = h.shape
-    lds = [_rows(k, t, tokens, dim, h.dtype) if t is not None else dim
-           for k, t in (("h", h), ("y", y), ("s", s), ("x", x))]
-    d = norms.struct(dim)
-    _check(lib.dpl_block_norm(plan.handle, ctypes.byref(d), tokens, _dtype(h), h.data_ptr(), lds[0], y.data_ptr(),
-                              lds[1], s.data_ptr(), lds[2], x.data_ptr() if x is not None else None, lds[3],
-                              _stream(stream)))
+    dtype = h.dtype
+    ld_h, ld_y = _rows("h", h, dev), _rows("y", y, dev, tokens, dim, dtype)
+    ld_s = _rows("s", s, dev, tokens, dim, dtype)
+    ld_x, addr_x = (dim, None) if x is None else (_rows("x", x, dev, tokens, dim, dtype), x.data_ptr())
+    _check(lib.dpl_block_norm(plan.handle, norms.ref(dim), tokens, _dtype(h), h.data_ptr(), ld_h, y.data_ptr(), ld_y,
+                              s.data_ptr(), ld_s, addr_x, ld_x, _stream_of(stream, dev)))
 
 
 def dpl_block_norm_workspace(plan, norms: BlockNorm, dim: int, tokens: int) -> int:
-    return _query(lib.dpl_block_norm_workspace, plan.handle, ctypes.byref(norms.struct(dim)), tokens)
+    return _query(lib.dpl_block_norm_workspace, plan.handle, norms.ref(dim), tokens)
 
 
 def dpl_accumulate_block_norm(plan, norms: BlockNorm, s: Optional[Sequence], y: Optional[Sequence],
@@ -221,46 +241,44 @@ def dpl_accumulate_block_norm(plan, norms: BlockNorm, s: Optional[Sequence], y: 
     """The backward from every replica's rows: dh, dy, and the gradients of
     the weights and the gate into the accumulators.  None for what is not there
     or not wanted."""
-    given = {k: None if v is None else _replicas(plan, k, v)
-             for k, v in (("s", s), ("y", y), ("dx", dx), ("ds", ds), ("dh", dh), ("dy", dy))}
-    one = next((v[0] for v in given.values() if v is not None), None)
-    if one is None:
+    dev = torch.cuda.current_device()
+    given = [None if v is None else _replicas(plan, k, v)
+             for k, v in (("s", s), ("y", y), ("dx", dx), ("ds", ds), ("dh", dh), ("dy", dy))]
+    there = [v for v in given if v is not None]
+    if not there:
         raise ValueError("no rows are given")
+    one = there[0][0]
     tokens, dim = one.shape
-    ld = _same_stride("rows", [_rows(k, t, tokens, dim, one.dtype) for k, v in given.items() if v is not None
-                               for t in v])
-    rows = (NormRows * plan.n)(*[NormRows(*[v[r].data_ptr() if v is not None else None for v in given.values()])
+    ld = _same_stride("rows", [_rows("rows", t, dev, tokens, dim, one.dtype) for v in there for t in v])
+    rows = (NormRows * plan.n)(*[NormRows(*[None if v is None else v[r].data_ptr() for v in given])
                                  for r in range(plan.n)])
-    addr, nbytes = _workspace(workspace)
-    d = norms.struct(dim)
-    _check(lib.dpl_accumulate_block_norm(plan.handle, ctypes.byref(d), tokens, _dtype(one), rows, ld,
-                                         int(bool(first)), int(bool(more)), addr, nbytes, _stream(stream)))
+    addr, nbytes = _workspace(workspace, dev)
+    _check(lib.dpl_accumulate_block_norm(plan.handle, norms.ref(dim), tokens, _dtype(one), rows, ld, bool(first),
+                                         bool(more), addr, nbytes, _stream_of(stream, dev)))
 
 
 # ---- activations in 8 bits -----------------------------------------------------------
-def _packed(codes, scales, tokens: int, dim: int):
-    import torch
-    return (_rows("codes", codes, tokens, dim, torch.uint8),
-            _rows("scales", scales, tokens, -(-dim // DPL_GROUP), torch.uint8))
-
-
 def dpl_pack_activations(x, codes, scales, stream=None) -> None:
     """x [tokens, dim] as e4m3 bytes, codes [tokens, dim], and a scale byte for
     32 channels, scales [tokens, ceil(dim / 32)]."""
+    dev = torch.cuda.current_device()
+    ld = _rows("x", x, dev)
     tokens, dim = x.shape
-    ld = _rows("x", x)
-    ld_c, ld_s = _packed(codes, scales, tokens, dim)
-    _check(lib.dpl_pack_activations(tokens, dim, _dtype(x), x.data_ptr(), ld, codes.data_ptr(), ld_c,
-                                    scales.data_ptr(), ld_s, _stream(stream)))
+    _check(lib.dpl_pack_activations(tokens, dim, _dtype(x), x.data_ptr(), ld, codes.data_ptr(),
+                                    _rows("codes", codes, dev, tokens, dim, torch.uint8), scales.data_ptr(),
+                                    _rows("scales", scales, dev, tokens, -(-dim // DPL_GROUP), torch.uint8),
+                                    _stream_of(stream, dev)))
 
 
 def dpl_unpack_activations(codes, scales, x, stream=None) -> None:
     """The values that codes and scales stand for, into x."""
+    dev = torch.cuda.current_device()
+    ld = _rows("x", x, dev)
     tokens, dim = x.shape
-    ld = _rows("x", x)
-    ld_c, ld_s = _packed(codes, scales, tokens, dim)
-    _check(lib.dpl_unpack_activations(tokens, dim, _dtype(x), codes.data_ptr(), ld_c, scales.data_ptr(), ld_s,
-                                      x.data_ptr(), ld, _stream(stream)))
+    _check(lib.dpl_unpack_activations(tokens, dim, _dtype(x), codes.data_ptr(),
+                                      _rows("codes", codes, dev, tokens, dim, torch.uint8), scales.data_ptr(),
+                                      _rows("scales", scales, dev, tokens, -(-dim // DPL_GROUP), torch.uint8),
+                                      x.data_ptr(), ld, _stream_of(stream, dev)))
 
 
 def dpl_linear_workspace(plan, tokens: int, inputs: int, outputs: int, tensor: Optional[int] = None) -> int:
@@ -276,15 +294,16 @@ def dpl_accumulate_linear(plan, tensor: int, dy: Sequence, codes: Sequence, scal
     """A linear layer's weight gradient from every replica's output gradients
     dy [tokens, outputs] and packed inputs, into the accumulators of plan tensor
     ``tensor``: outputs x inputs, or inputs x outputs if ``transposed``."""
-    import torch
+    dev = torch.cuda.current_device()
     dy, codes, scales = _replicas(plan, "dy", dy), _replicas(plan, "codes", codes), _replicas(plan, "scales", scales)
     (tokens, outputs), inputs = dy[0].shape, codes[0].shape[1]
-    ld_dy = _same_stride("dy", [_rows("dy", t, tokens, outputs, dy[0].dtype) for t in dy])
-    ld_c = _same_stride("codes", [_rows("codes", t, tokens, inputs, torch.uint8) for t in codes])
-    ld_s = _same_stride("scales", [_rows("scales", t, tokens, -(-inputs // DPL_GROUP), torch.uint8) for t in scales])
-    rows = (LinearRows * plan.n)(*[LinearRows(codes[r].data_ptr(), scales[r].data_ptr(), dy[r].data_ptr())
-                                   for r in range(plan.n)])
-    addr, nbytes = _workspace(workspace)
-    d = Linear(tensor, int(bool(transposed)), inputs, outputs)
-    _check(lib.dpl_accumulate_linear(plan.handle, ctypes.byref(d), tokens, _dtype(dy[0]), rows, ld_c, ld_s, ld_dy,
-                                     int(bool(first)), int(bool(more)), addr, nbytes, _stream(stream)))
+    groups = -(-inputs // DPL_GROUP)
+    ld_dy = _same_stride("dy", [_rows("dy", t, dev, tokens, outputs, dy[0].dtype) for t in dy])
+    ld_c = _same_stride("codes", [_rows("codes", t, dev, tokens, inputs, torch.uint8) for t in codes])
+    ld_s = _same_stride("scales", [_rows("scales", t, dev, tokens, groups, torch.uint8) for t in scales])
+    rows = (LinearRows * plan.n)(*[LinearRows(c.data_ptr(), e.data_ptr(), d.data_ptr())
+                                   for c, e, d in zip(codes, scales, dy)])
+    addr, nbytes = _workspace(workspace, dev)
+    _check(lib.dpl_accumulate_linear(plan.handle, ctypes.byref(Linear(tensor, bool(transposed), inputs, outputs)),
+                                     tokens, _dtype(dy[0]), rows, ld_c, ld_s, ld_dy, bool(first), bool(more), addr,
+                                     nbytes, _stream_of(stream, dev)))
