@@ -42,54 +42,54 @@ struct GradArgs {
 template <bool kCentered>
 constexpr int kSums = kCentered ? 4 : 2;
 
-template <dp_dtype DT, dp_dtype PT, int NT, int NV, bool kCentered, bool kPost>
+template <dp_dtype DT, dp_dtype PT, int NT, int NV, int VW, bool kCentered, bool kPost>
 __global__ void __launch_bounds__(block_of(NT)) k_block_grad(GradArgs a) {
-    constexpr int kRows = block_of(NT) / NT, kStep = 8 * NT, Q = kSums<kCentered>;
+    constexpr int kRows = block_of(NT) / NT, kStep = VW * NT, Q = kSums<kCentered>;
     __shared__ float lds[sum_scratch(NT)];
-    __shared__ float fold[kRows > 1 ? kRows - 1 : 1][kRows > 1 ? NT * 8 * NV : 1];
+    __shared__ float fold[kRows > 1 ? kRows - 1 : 1][kRows > 1 ? NT * VW * NV : 1];
     int turn = 0;
     const dpl_norm_rows p = a.rows[blockIdx.y];
-    const int lane = threadIdx.x % NT, c0 = 8 * lane;
+    const int lane = threadIdx.x % NT, c0 = VW * lane;
     const float dim = static_cast<float>(a.dim), inv = 1.0f / dim;
     const bool has_gate = a.w.gate != nullptr, has_x = p.dx != nullptr, has_ds = p.ds != nullptr;
     const bool has_y = kPost || has_gate;
-    Column<PT, NV> post_w, gate, pre_w;
+    Column<PT, NV, VW> post_w, gate, pre_w;
     if constexpr (kPost) post_w.load(a.w.post_w, c0, kStep, a.dim, a.w.vec);
     if (has_gate) gate.load(a.w.gate, c0, kStep, a.dim, a.w.vec);
     if (has_x) pre_w.load(a.w.pre_w, c0, kStep, a.dim, a.w.vec);
-    float sum[Q][NV][8];
+    float sum[Q][NV][VW];
 #pragma unroll
     for (int q = 0; q < Q; ++q)
 #pragma unroll
         for (int k = 0; k < NV; ++k)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum[q][k][j] = 0.0f;
+            for (int j = 0; j < VW; ++j) sum[q][k][j] = 0.0f;
 
     const int64_t stride = static_cast<int64_t>(gridDim.x) * kRows;
     int64_t base = static_cast<int64_t>(blockIdx.x) * kRows;
     int64_t row = base + threadIdx.x / NT;
-    Raw<DT> ns[NV], ny[NV], nx[NV], nd[NV];
+    Raw<DT, VW> ns[NV], ny[NV], nx[NV], nd[NV];
     auto fetch = [&](int64_t t) {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int c = c0 + k * kStep;
-            const int valid = t < a.tokens ? valid_of(a.dim, c) : 0;
+            const int valid = t < a.tokens ? valid_of<VW>(a.dim, c) : 0;
             const int64_t at = t * a.ld + c;
-            ns[k] = load_raw<DT>(p.s, at, has_x ? valid : 0, a.vec && has_x);
-            nx[k] = load_raw<DT>(p.dx, at, has_x ? valid : 0, a.vec && has_x);
-            ny[k] = load_raw<DT>(p.y, at, has_y ? valid : 0, a.vec && has_y);
-            nd[k] = load_raw<DT>(p.ds, at, has_ds ? valid : 0, a.vec && has_ds);
+            ns[k] = load_raw<DT, VW>(p.s, at, has_x ? valid : 0, a.vec && has_x);
+            nx[k] = load_raw<DT, VW>(p.dx, at, has_x ? valid : 0, a.vec && has_x);
+            ny[k] = load_raw<DT, VW>(p.y, at, has_y ? valid : 0, a.vec && has_y);
+            nd[k] = load_raw<DT, VW>(p.ds, at, has_ds ? valid : 0, a.vec && has_ds);
         }
     };
     fetch(row);
     for (; base < a.tokens; base += stride, row += stride) {
-        float s[NV][8], y[NV][8], e[NV][8], t[NV][8];
+        float s[NV][VW], y[NV][VW], e[NV][VW], t[NV][VW];
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            expand<DT>(ns[k], s[k]);
-            expand<DT>(nx[k], e[k]);
-            expand<DT>(ny[k], y[k]);
-            expand<DT>(nd[k], t[k]);
+            expand<DT, VW>(ns[k], s[k]);
+            expand<DT, VW>(nx[k], e[k]);
+            expand<DT, VW>(ny[k], y[k]);
+            expand<DT, VW>(nd[k], t[k]);
         }
         if (base + stride < a.tokens) fetch(row + stride);
         if constexpr (kCentered) {
@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(block_of(NT)) k_block_grad(GradArgs a) {
 #pragma unroll
             for (int k = 0; k < NV; ++k)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
+                for (int j = 0; j < VW; ++j) {
                     m[0] += s[k][j];
                     m[1] += y[k][j];
                 }
@@ -106,8 +106,8 @@ __global__ void __launch_bounds__(block_of(NT)) k_block_grad(GradArgs a) {
 #pragma unroll
             for (int k = 0; k < NV; ++k)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const bool in = j < valid_of(a.dim, c0 + k * kStep);
+                for (int j = 0; j < VW; ++j) {
+                    const bool in = j < valid_of<VW>(a.dim, c0 + k * kStep);
                     s[k][j] = in ? s[k][j] - mean_s : 0.0f;
                     if constexpr (kPost) y[k][j] = in ? y[k][j] - mean_y : 0.0f;
                 }
@@ -117,10 +117,10 @@ __global__ void __launch_bounds__(block_of(NT)) k_block_grad(GradArgs a) {
         float v[2 + kCentered + kPost] = {};
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            float w[8];
-            expand<PT>(pre_w.q[k], w);
+            float w[VW];
+            expand<PT, VW>(pre_w.q[k], w);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < VW; ++j) {
                 const float f = has_x ? e[k][j] * w[j] : 0.0f;
                 v[0] += s[k][j] * s[k][j];
                 v[1] += f * s[k][j];
@@ -136,10 +136,10 @@ __global__ void __launch_bounds__(block_of(NT)) k_block_grad(GradArgs a) {
         if (has_x) {
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
-                float w[8];
-                expand<PT>(pre_w.q[k], w);
+                float w[VW];
+                expand<PT, VW>(pre_w.q[k], w);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
+                for (int j = 0; j < VW; ++j) {
                     const float n = s[k][j] * r;
                     sum[0][k][j] += e[k][j] * n;
                     if constexpr (kCentered) sum[2][k][j] += e[k][j];
@@ -151,31 +151,31 @@ __global__ void __launch_bounds__(block_of(NT)) k_block_grad(GradArgs a) {
         float g[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            float w[8], f[8];
-            const int c = c0 + k * kStep, valid = row < a.tokens ? valid_of(a.dim, c) : 0;
+            float w[VW], f[VW];
+            const int c = c0 + k * kStep, valid = row < a.tokens ? valid_of<VW>(a.dim, c) : 0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = a.alpha * t[k][j];
-            if (p.dh) store_n<DT, 8>(p.dh, row * a.ld + c, valid, a.vec, f);
+            for (int j = 0; j < VW; ++j) f[j] = a.alpha * t[k][j];
+            if (p.dh) store_n<DT, VW>(p.dh, row * a.ld + c, valid, a.vec, f);
             if constexpr (kCentered) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) sum[3][k][j] += j < valid ? t[k][j] : 0.0f;
+                for (int j = 0; j < VW; ++j) sum[3][k][j] += j < valid ? t[k][j] : 0.0f;
             }
             if (kPost || has_gate) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) sum[1][k][j] += t[k][j] * (kPost ? y[k][j] * ry : y[k][j]);
+                for (int j = 0; j < VW; ++j) sum[1][k][j] += t[k][j] * (kPost ? y[k][j] * ry : y[k][j]);
             }
             if (has_gate) {
-                expand<PT>(gate.q[k], w);
+                expand<PT, VW>(gate.q[k], w);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) t[k][j] *= w[j];
+                for (int j = 0; j < VW; ++j) t[k][j] *= w[j];
             }
             if constexpr (kPost) {
-                expand<PT>(post_w.q[k], w);
+                expand<PT, VW>(post_w.q[k], w);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
+                for (int j = 0; j < VW; ++j) {
                     t[k][j] *= w[j];
                     g[0] += t[k][j] * y[k][j];
-                    g[1] += j < valid_of(a.dim, c) ? t[k][j] : 0.0f;
+                    g[1] += j < valid_of<VW>(a.dim, c) ? t[k][j] : 0.0f;
                 }
             }
         }
@@ -186,12 +186,12 @@ __global__ void __launch_bounds__(block_of(NT)) k_block_grad(GradArgs a) {
 #pragma unroll
             for (int k = 0; k < NV; ++k)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) t[k][j] = ry * (t[k][j] - mean_t - y[k][j] * ry * mean_tn);
+                for (int j = 0; j < VW; ++j) t[k][j] = ry * (t[k][j] - mean_t - y[k][j] * ry * mean_tn);
         }
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int c = c0 + k * kStep, valid = row < a.tokens ? valid_of(a.dim, c) : 0;
-            store_n<DT, 8>(p.dy, row * a.ld + c, valid, a.vec, t[k]);
+            const int c = c0 + k * kStep, valid = row < a.tokens ? valid_of<VW>(a.dim, c) : 0;
+            store_n<DT, VW>(p.dy, row * a.ld + c, valid, a.vec, t[k]);
         }
     }
     // the rows' sums of this workgroup, in row order, then one slot of the workspace
@@ -205,19 +205,19 @@ __global__ void __launch_bounds__(block_of(NT)) k_block_grad(GradArgs a) {
 #pragma unroll
                 for (int k = 0; k < NV; ++k)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) fold[w - 1][(k * 8 + j) * NT + lane] = sum[q][k][j];
+                    for (int j = 0; j < VW; ++j) fold[w - 1][(k * VW + j) * NT + lane] = sum[q][k][j];
             __syncthreads();
             if (w == 0)
                 for (int i = 0; i < kRows - 1; ++i)
 #pragma unroll
                     for (int k = 0; k < NV; ++k)
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) sum[q][k][j] += fold[i][(k * 8 + j) * NT + lane];
+                        for (int j = 0; j < VW; ++j) sum[q][k][j] += fold[i][(k * VW + j) * NT + lane];
         }
         if (threadIdx.x < NT)
 #pragma unroll
             for (int k = 0; k < NV; ++k)
-                store_n<DP_F32, 8>(out + q * a.dim, c0 + k * kStep, valid_of(a.dim, c0 + k * kStep), a.dim % 4 == 0,
+                store_n<DP_F32, VW>(out + q * a.dim, c0 + k * kStep, valid_of<VW>(a.dim, c0 + k * kStep), a.dim % 4 == 0,
                                    sum[q][k]);
     }
 }
@@ -226,7 +226,7 @@ struct JoinArgs {
     const float* part;
     float* acc[5][DP_MAX_REPLICAS];  // post_w, post_b, gate, pre_w, pre_b; null: none
     bool overwrite[5];
-    int32_t dim, groups, sums;
+    int32_t dim, groups;
     Weights w;
 };
 
@@ -239,25 +239,27 @@ __device__ __forceinline__ float weight_at(const void* p, int c, float none) {
 
 // Adds the workgroups' sums of 32 columns of one replica: 16 threads a column
 // each take every 16th group, then their sums are added in order.
-template <dp_dtype PT>
+template <dp_dtype PT, int Q>
 __global__ void __launch_bounds__(kJoinColumns* kJoinLanes) k_block_join(JoinArgs a) {
-    __shared__ float lds[kJoinLanes][kJoinColumns];
+    __shared__ float lds[Q][kJoinLanes][kJoinColumns];
     const int col = threadIdx.x % kJoinColumns, lane = threadIdx.x / kJoinColumns;
     const int c = blockIdx.x * kJoinColumns + col, r = blockIdx.y;
-    const float* part = a.part + static_cast<int64_t>(r) * a.groups * a.sums * a.dim;
-    float total[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int q = 0; q < a.sums; ++q) {
-        float s = 0.0f;
-        if (c < a.dim)
+    const float* part = a.part + static_cast<int64_t>(r) * a.groups * Q * a.dim + c;
+    float s[Q] = {};
+    if (c < a.dim)
 #pragma unroll 4
-            for (int g = lane; g < a.groups; g += kJoinLanes) s += part[(static_cast<int64_t>(g) * a.sums + q) * a.dim + c];
-        __syncthreads();
-        lds[lane][col] = s;
-        __syncthreads();
+        for (int g = lane; g < a.groups; g += kJoinLanes)
 #pragma unroll
-        for (int i = 0; i < kJoinLanes; ++i) total[q] += lds[i][col];
-    }
+            for (int q = 0; q < Q; ++q) s[q] += part[(static_cast<int64_t>(g) * Q + q) * a.dim];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) lds[q][lane][col] = s[q];
+    __syncthreads();
     if (lane != 0 || c >= a.dim) return;
+    float total[4] = {};
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+#pragma unroll
+        for (int i = 0; i < kJoinLanes; ++i) total[q] += lds[q][i][col];
     const float C = total[0], A = total[1], E = total[2], B = total[3];
     const float gate = weight_at<PT>(a.w.gate, c, 1.0f);
     const float grads[5] = {gate * A, gate * B,
@@ -268,26 +270,34 @@ __global__ void __launch_bounds__(kJoinColumns* kJoinLanes) k_block_join(JoinArg
         if (a.acc[i][r]) a.acc[i][r][c] = a.overwrite[i] ? grads[i] : a.acc[i][r][c] + grads[i];
 }
 
+// One wave a row up to 1024 elements needs no barriers.  32768 rows of 768,
+// centred, bf16: 128 threads with 8 elements each take 112 us, one wave with 2 x
+// 8 takes 94 us and with 3 x 4 (every lane busy, 196 registers) 77 us; forcing
+// a third wave a SIMD spills 29 registers and takes 92 to 114 us.
 Shape shape_of(int64_t dim) {
-    if (dim <= 512) return {64, 1};
-    if (dim <= 1024) return {128, 1};
-    if (dim <= 2048) return {256, 1};
-    if (dim <= 4096) return {512, 1};
-    return {512, 2};
+    if (dim <= 512) return {64, 1, 8};
+    if (dim <= 768) return {64, 3, 4};
+    if (dim <= 1024) return {64, 2, 8};
+    if (dim <= 2048) return {256, 1, 8};
+    if (dim <= 4096) return {512, 1, 8};
+    return {512, 2, 8};
 }
 
-#define DP_SHAPES(GO)                  \
-    if (sh.nt == 64) GO(64, 1)         \
-    else if (sh.nt == 128) GO(128, 1)  \
-    else if (sh.nt == 256) GO(256, 1)  \
-    else if (sh.nv == 1) GO(512, 1)    \
-    else GO(512, 2)
+#define DP_SHAPES(GO)                           \
+    if (sh.nt == 64 && sh.nv == 1) GO(64, 1, 8) \
+    else if (sh.vw == 4) GO(64, 3, 4)           \
+    else if (sh.nt == 64) GO(64, 2, 8)          \
+    else if (sh.nt == 256) GO(256, 1, 8)        \
+    else if (sh.nv == 1) GO(512, 1, 8)          \
+    else GO(512, 2, 8)
 
-// Workgroups of one replica's backward: about as many as the chip holds at a
-// time, shared by the replicas, each with rows to walk over.
+// Workgroups of one replica's backward: as many as the chip holds at a time
+// (two of 4 one-wave rows a CU; 1024 threads a CU else), shared by the replicas.
+// Twice as many for the one-wave rows costs 4% of the pass, and the second
+// launch doubles.
 int64_t groups_of(int64_t dim, int64_t tokens, int n) {
     const int nt = shape_of(dim).nt;
-    const int64_t most = (256 * 1024 / block_of(nt) + n - 1) / n, rows = block_of(nt) / nt;
+    const int64_t most = (256 * (nt == 64 ? 512 : 1024) / block_of(nt) + n - 1) / n, rows = block_of(nt) / nt;
     const int64_t want = (tokens + rows - 1) / rows;
     return want < most ? want : most;
 }
@@ -296,8 +306,8 @@ template <dp_dtype DT, dp_dtype PT, bool kCentered, bool kPost>
 void backward(const GradArgs& a, int groups, int n, hipStream_t stream) {
     const Shape sh = shape_of(a.dim);
     const dim3 grid(static_cast<unsigned>(groups), static_cast<unsigned>(n));
-#define GO(T, V) \
-    { hipLaunchKernelGGL((k_block_grad<DT, PT, T, V, kCentered, kPost>), grid, dim3(block_of(T)), 0, stream, a); }
+#define GO(T, V, W) \
+    { hipLaunchKernelGGL((k_block_grad<DT, PT, T, V, W, kCentered, kPost>), grid, dim3(block_of(T)), 0, stream, a); }
     DP_SHAPES(GO)
 #undef GO
 }
@@ -342,11 +352,14 @@ hipError_t launch_block_grad(dp_dtype dt, dp_dtype pdt, const BlockNorm& b, int6
     j.part = a.part;
     j.dim = a.dim;
     j.groups = tokens > 0 ? groups : 0;
-    j.sums = b.centered ? 4 : 2;
     j.w = a.w;
     const dim3 grid(static_cast<unsigned>((b.dim + kJoinColumns - 1) / kJoinColumns), static_cast<unsigned>(n));
-    if (pdt == DP_BF16) hipLaunchKernelGGL((k_block_join<DP_BF16>), grid, dim3(kJoinColumns * kJoinLanes), 0, stream, j);
-    else hipLaunchKernelGGL((k_block_join<DP_F16>), grid, dim3(kJoinColumns * kJoinLanes), 0, stream, j);
+#define GO(P, S) hipLaunchKernelGGL((k_block_join<P, S>), grid, dim3(kJoinColumns * kJoinLanes), 0, stream, j)
+    if (pdt == DP_BF16 && b.centered) GO(DP_BF16, 4);
+    else if (pdt == DP_BF16) GO(DP_BF16, 2);
+    else if (b.centered) GO(DP_F16, 4);
+    else GO(DP_F16, 2);
+#undef GO
     return hipGetLastError();
 }
 

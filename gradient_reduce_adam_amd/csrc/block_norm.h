@@ -10,32 +10,39 @@
 
 namespace dpk {
 
-// Eight elements as they lie in memory.
-template <dp_dtype DT>
+// VW (4 or 8) elements as they lie in memory.
+template <dp_dtype DT, int VW>
 struct Raw {
-    static constexpr int kWords = DT == DP_F32 ? 8 : 4;
+    static constexpr int kWords = VW * (DT == DP_F32 ? 4 : 2) / 4;
     unsigned int w[kWords];
 };
 
-template <dp_dtype DT>
-__device__ __forceinline__ Raw<DT> load_raw(const void* p, int64_t i, int valid, bool vec) {
-    Raw<DT> q;
-    if (vec && valid >= 8) {
-        const u32x4* at = reinterpret_cast<const u32x4*>(static_cast<const char*>(p) + i * (DT == DP_F32 ? 4 : 2));
+template <dp_dtype DT, int VW>
+__device__ __forceinline__ Raw<DT, VW> load_raw(const void* p, int64_t i, int valid, bool vec) {
+    constexpr int kWords = Raw<DT, VW>::kWords;
+    Raw<DT, VW> q;
+    if (vec && valid >= VW) {
+        const char* at = static_cast<const char*>(p) + i * (DT == DP_F32 ? 4 : 2);
+        if constexpr (kWords == 2) {
+            const u32x2 v = gload<u32x2>(at, 0);
+            q.w[0] = v[0];
+            q.w[1] = v[1];
+        } else {
 #pragma unroll
-        for (int k = 0; k < Raw<DT>::kWords / 4; ++k) {
-            const u32x4 v = gload<u32x4>(at, k);
+            for (int k = 0; k < kWords / 4; ++k) {
+                const u32x4 v = gload<u32x4>(at, k);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) q.w[4 * k + j] = v[j];
+                for (int j = 0; j < 4; ++j) q.w[4 * k + j] = v[j];
+            }
         }
         return q;
     }
     if constexpr (DT == DP_F32) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) q.w[j] = j < valid ? gload<unsigned int>(p, i + j) : 0u;
+        for (int j = 0; j < VW; ++j) q.w[j] = j < valid ? gload<unsigned int>(p, i + j) : 0u;
     } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < VW / 2; ++j) {
             const unsigned int lo = 2 * j < valid ? gload<unsigned short>(p, i + 2 * j) : 0u;
             const unsigned int hi = 2 * j + 1 < valid ? gload<unsigned short>(p, i + 2 * j + 1) : 0u;
             q.w[j] = lo | hi << 16;
@@ -44,14 +51,14 @@ __device__ __forceinline__ Raw<DT> load_raw(const void* p, int64_t i, int valid,
     return q;
 }
 
-template <dp_dtype DT>
-__device__ __forceinline__ void expand(const Raw<DT>& q, float* o) {
+template <dp_dtype DT, int VW>
+__device__ __forceinline__ void expand(const Raw<DT, VW>& q, float* o) {
     if constexpr (DT == DP_F32) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = __builtin_bit_cast(float, q.w[j]);
+        for (int j = 0; j < VW; ++j) o[j] = __builtin_bit_cast(float, q.w[j]);
     } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) unpack2<DT>(q.w[j], o + 2 * j);
+        for (int j = 0; j < VW / 2; ++j) unpack2<DT>(q.w[j], o + 2 * j);
     }
 }
 
@@ -66,9 +73,7 @@ constexpr int sum_scratch(int nt) { return nt > 64 ? 2 * 4 * (block_of(nt) / 64)
 template <int NT, int K>
 __device__ __forceinline__ void row_sum(float (&v)[K], float* lds, int& turn) {
 #pragma unroll
-    for (int d = 32; d > 0; d >>= 1)
-#pragma unroll
-        for (int k = 0; k < K; ++k) v[k] += __shfl_xor(v[k], d);
+    for (int k = 0; k < K; ++k) v[k] = wave_sum(v[k]);
     if constexpr (NT > 64) {
         constexpr int kWaves = NT / 64;  // of a row
         float* at = lds + turn * (block_of(NT) / 64) * 4;
@@ -93,25 +98,27 @@ struct Weights {
 };
 
 // The weights of this thread's columns stay packed in registers over all rows.
-template <dp_dtype PT, int NV>
+template <dp_dtype PT, int NV, int VW>
 struct Column {
-    Raw<PT> q[NV];
+    Raw<PT, VW> q[NV];
     __device__ __forceinline__ void load(const void* p, int c0, int step, int dim, bool vec) {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int left = dim - (c0 + k * step);
-            const int valid = !p || left <= 0 ? 0 : left < 8 ? left : 8;
-            q[k] = load_raw<PT>(p, c0 + k * step, valid, vec);
+            const int valid = !p || left <= 0 ? 0 : left < VW ? left : VW;
+            q[k] = load_raw<PT, VW>(p, c0 + k * step, valid, vec);
         }
     }
 };
 
-__device__ __forceinline__ int valid_of(int dim, int c) { return dim - c >= 8 ? 8 : dim - c > 0 ? dim - c : 0; }
+template <int VW>
+__device__ __forceinline__ int valid_of(int dim, int c) {
+    return dim - c >= VW ? VW : dim - c > 0 ? dim - c : 0;
+}
 
-
-// Threads of a row and 8-element vectors of a thread, by the row's width.
+// How a row is held: nt threads with nv vectors of vw elements each.
 struct Shape {
-    int nt, nv;
+    int nt, nv, vw;
 };
 
 inline Weights weights_of(const BlockNorm& b) {

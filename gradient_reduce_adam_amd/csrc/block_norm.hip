@@ -31,15 +31,15 @@ struct NormArgs {
     Weights w;
 };
 
-template <dp_dtype DT, dp_dtype PT, int NT, int NV, bool kCentered, bool kPost>
+template <dp_dtype DT, dp_dtype PT, int NT, int NV, int VW, bool kCentered, bool kPost>
 __global__ void __launch_bounds__(block_of(NT)) k_block_norm(NormArgs a) {
-    constexpr int kRows = block_of(NT) / NT, kStep = 8 * NT;
+    constexpr int kRows = block_of(NT) / NT, kStep = VW * NT;
     __shared__ float lds[sum_scratch(NT)];
     int turn = 0;
-    const int lane = threadIdx.x % NT, c0 = 8 * lane;
+    const int lane = threadIdx.x % NT, c0 = VW * lane;
     const float dim = static_cast<float>(a.dim), inv = 1.0f / dim;
     const bool has_gate = a.w.gate != nullptr, has_x = a.x != nullptr;
-    Column<PT, NV> post_w, post_b, gate, pre_w, pre_b;
+    Column<PT, NV, VW> post_w, post_b, gate, pre_w, pre_b;
     if constexpr (kPost) post_w.load(a.w.post_w, c0, kStep, a.dim, a.w.vec);
     if constexpr (kPost && kCentered) post_b.load(a.w.post_b, c0, kStep, a.dim, a.w.vec);
     if (has_gate) gate.load(a.w.gate, c0, kStep, a.dim, a.w.vec);
@@ -52,23 +52,23 @@ __global__ void __launch_bounds__(block_of(NT)) k_block_norm(NormArgs a) {
     const int64_t stride = static_cast<int64_t>(gridDim.x) * kRows;
     int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / NT;
     int64_t base = static_cast<int64_t>(blockIdx.x) * kRows;
-    Raw<DT> nh[NV], ny[NV];
+    Raw<DT, VW> nh[NV], ny[NV];
     auto fetch = [&](int64_t t) {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int c = c0 + k * kStep;
-            const int valid = t < a.tokens ? valid_of(a.dim, c) : 0;
-            nh[k] = load_raw<DT>(a.h, t * a.ld_h + c, valid, a.vec_h);
-            ny[k] = load_raw<DT>(a.y, t * a.ld_y + c, valid, a.vec_y);
+            const int valid = t < a.tokens ? valid_of<VW>(a.dim, c) : 0;
+            nh[k] = load_raw<DT, VW>(a.h, t * a.ld_h + c, valid, a.vec_h);
+            ny[k] = load_raw<DT, VW>(a.y, t * a.ld_y + c, valid, a.vec_y);
         }
     };
     fetch(row);
     for (; base < a.tokens; base += stride, row += stride) {
-        float h[NV][8], u[NV][8];
+        float h[NV][VW], u[NV][VW];
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            expand<DT>(nh[k], h[k]);
-            expand<DT>(ny[k], u[k]);
+            expand<DT, VW>(nh[k], h[k]);
+            expand<DT, VW>(ny[k], u[k]);
         }
         if (base + stride < a.tokens) fetch(row + stride);
         if constexpr (kPost) {
@@ -77,44 +77,44 @@ __global__ void __launch_bounds__(block_of(NT)) k_block_norm(NormArgs a) {
 #pragma unroll
                 for (int k = 0; k < NV; ++k)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) m[0] += u[k][j];
+                    for (int j = 0; j < VW; ++j) m[0] += u[k][j];
                 row_sum<NT>(m, lds, turn);
                 const float mean = m[0] / dim;
 #pragma unroll
                 for (int k = 0; k < NV; ++k)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        u[k][j] = j < valid_of(a.dim, c0 + k * kStep) ? u[k][j] - mean : 0.0f;
+                    for (int j = 0; j < VW; ++j)
+                        u[k][j] = j < valid_of<VW>(a.dim, c0 + k * kStep) ? u[k][j] - mean : 0.0f;
             }
             float q[1] = {0.0f};
 #pragma unroll
             for (int k = 0; k < NV; ++k)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) q[0] += u[k][j] * u[k][j];
+                for (int j = 0; j < VW; ++j) q[0] += u[k][j] * u[k][j];
             row_sum<NT>(q, lds, turn);
             const float r = 1.0f / sqrtf(q[0] * inv + a.eps);
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
-                float w[8], b[8];
-                expand<PT>(post_w.q[k], w);
-                if constexpr (kCentered) expand<PT>(post_b.q[k], b);
+                float w[VW], b[VW];
+                expand<PT, VW>(post_w.q[k], w);
+                if constexpr (kCentered) expand<PT, VW>(post_b.q[k], b);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) u[k][j] = u[k][j] * r * w[j] + (kCentered ? b[j] : 0.0f);
+                for (int j = 0; j < VW; ++j) u[k][j] = u[k][j] * r * w[j] + (kCentered ? b[j] : 0.0f);
             }
         }
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             if (has_gate) {
-                float w[8];
-                expand<PT>(gate.q[k], w);
+                float w[VW];
+                expand<PT, VW>(gate.q[k], w);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) u[k][j] *= w[j];
+                for (int j = 0; j < VW; ++j) u[k][j] *= w[j];
             }
             const int c = c0 + k * kStep;
-            const int valid = row < a.tokens ? valid_of(a.dim, c) : 0;
+            const int valid = row < a.tokens ? valid_of<VW>(a.dim, c) : 0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) h[k][j] = a.alpha * h[k][j] + u[k][j];
-            store_n<DT, 8>(a.s, row * a.ld_s + c, valid, a.vec_s, h[k]);
+            for (int j = 0; j < VW; ++j) h[k][j] = a.alpha * h[k][j] + u[k][j];
+            store_n<DT, VW>(a.s, row * a.ld_s + c, valid, a.vec_s, h[k]);
         }
         if (!has_x) continue;
         if constexpr (kCentered) {
@@ -122,58 +122,58 @@ __global__ void __launch_bounds__(block_of(NT)) k_block_norm(NormArgs a) {
 #pragma unroll
             for (int k = 0; k < NV; ++k)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) m[0] += h[k][j];
+                for (int j = 0; j < VW; ++j) m[0] += h[k][j];
             row_sum<NT>(m, lds, turn);
             const float mean = m[0] / dim;
 #pragma unroll
             for (int k = 0; k < NV; ++k)
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    h[k][j] = j < valid_of(a.dim, c0 + k * kStep) ? h[k][j] - mean : 0.0f;
+                for (int j = 0; j < VW; ++j)
+                    h[k][j] = j < valid_of<VW>(a.dim, c0 + k * kStep) ? h[k][j] - mean : 0.0f;
         }
         float q[1] = {0.0f};
 #pragma unroll
         for (int k = 0; k < NV; ++k)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) q[0] += h[k][j] * h[k][j];
+            for (int j = 0; j < VW; ++j) q[0] += h[k][j] * h[k][j];
         row_sum<NT>(q, lds, turn);
         const float r = 1.0f / sqrtf(q[0] * inv + a.eps);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            float w[8], b[8];
-            expand<PT>(pre_w.q[k], w);
-            if constexpr (kCentered) expand<PT>(pre_b.q[k], b);
+            float w[VW], b[VW];
+            expand<PT, VW>(pre_w.q[k], w);
+            if constexpr (kCentered) expand<PT, VW>(pre_b.q[k], b);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) h[k][j] = h[k][j] * r * w[j] + (kCentered ? b[j] : 0.0f);
+            for (int j = 0; j < VW; ++j) h[k][j] = h[k][j] * r * w[j] + (kCentered ? b[j] : 0.0f);
             const int c = c0 + k * kStep;
-            const int valid = row < a.tokens ? valid_of(a.dim, c) : 0;
-            store_n<DT, 8>(a.x, row * a.ld_x + c, valid, a.vec_x, h[k]);
+            const int valid = row < a.tokens ? valid_of<VW>(a.dim, c) : 0;
+            store_n<DT, VW>(a.x, row * a.ld_x + c, valid, a.vec_x, h[k]);
         }
     }
 }
 
 Shape shape_of(int64_t dim) {
-    if (dim <= 512) return {64, 1};
-    if (dim <= 1024) return {64, 2};
-    if (dim <= 2048) return {256, 1};
-    if (dim <= 4096) return {256, 2};
-    return {512, 2};
+    if (dim <= 512) return {64, 1, 8};
+    if (dim <= 1024) return {64, 2, 8};
+    if (dim <= 2048) return {256, 1, 8};
+    if (dim <= 4096) return {256, 2, 8};
+    return {512, 2, 8};
 }
 
-#define DP_SHAPES(GO)                               \
-    if (sh.nt == 64 && sh.nv == 1) GO(64, 1)        \
-    else if (sh.nt == 64) GO(64, 2)                 \
-    else if (sh.nt == 256 && sh.nv == 1) GO(256, 1) \
-    else if (sh.nt == 256) GO(256, 2)               \
-    else GO(512, 2)
+#define DP_SHAPES(GO)                                  \
+    if (sh.nt == 64 && sh.nv == 1) GO(64, 1, 8)        \
+    else if (sh.nt == 64) GO(64, 2, 8)                 \
+    else if (sh.nt == 256 && sh.nv == 1) GO(256, 1, 8) \
+    else if (sh.nt == 256) GO(256, 2, 8)               \
+    else GO(512, 2, 8)
 
 template <dp_dtype DT, dp_dtype PT, bool kCentered, bool kPost>
 void forward(const NormArgs& a, hipStream_t stream) {
     const Shape sh = shape_of(a.dim);
     const int64_t rows = block_of(sh.nt) / sh.nt, want = (a.tokens + rows - 1) / rows;
     const dim3 grid(static_cast<unsigned>(want < 4096 ? want : 4096));
-#define GO(T, V) \
-    { hipLaunchKernelGGL((k_block_norm<DT, PT, T, V, kCentered, kPost>), grid, dim3(block_of(T)), 0, stream, a); }
+#define GO(T, V, W) \
+    { hipLaunchKernelGGL((k_block_norm<DT, PT, T, V, W, kCentered, kPost>), grid, dim3(block_of(T)), 0, stream, a); }
     DP_SHAPES(GO)
 #undef GO
 }

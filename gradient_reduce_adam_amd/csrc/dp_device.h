@@ -72,26 +72,48 @@ __device__ __forceinline__ void store1(void* p, int64_t i, float x) {
     }
 }
 
+// The sum of a wave's 64 values, in every lane, in a fixed order: within rows of
+// 16 lanes by shifts of 1, 2, 4 and 8, then over the rows (data-parallel moves
+// folded into the additions; a butterfly through LDS costs ten times as long).
+template <int kCtrl, int kRows>
+__device__ __forceinline__ float moved(float x) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), kCtrl, kRows, 0xf, true));
+}
+__device__ __forceinline__ float wave_sum(float x) {
+    x += moved<0x111, 0xf>(x);
+    x += moved<0x112, 0xf>(x);
+    x += moved<0x114, 0xf>(x);
+    x += moved<0x118, 0xf>(x);
+    x += moved<0x142, 0xa>(x);  // the last lane of rows 0 and 2 into rows 1 and 3
+    x += moved<0x143, 0xc>(x);  // lane 31 into the upper half
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), 63));
+}
+
 // N (4 or 8) consecutive elements from element i of p, of which the first
 // `valid` exist (the others come back as zero, or are not written).  `vec`:
 // the address is a multiple of the vector's bytes (16 at most), so that whole
 // vectors go in one or two accesses.
-template <dp_dtype DT, int N>
+// kOnce: the data is used once, so it need not stay in the caches.
+template <dp_dtype DT, int N, bool kOnce = false>
 __device__ __forceinline__ void load_n(const void* p, int64_t i, int valid, bool vec, float* o) {
+    const auto get = [](const auto* at, int64_t k, auto like) {
+        if constexpr (kOnce) return gload_nt<decltype(like)>(at, k);
+        else return gload<decltype(like)>(at, k);
+    };
     if (vec && valid >= N) {
         if constexpr (DT == DP_F32) {
 #pragma unroll
             for (int k = 0; k < N / 4; ++k) {
-                const f32x4 v = gload<f32x4>(static_cast<const float*>(p) + i, k);
+                const f32x4 v = get(static_cast<const float*>(p) + i, k, f32x4{});
 #pragma unroll
                 for (int j = 0; j < 4; ++j) o[4 * k + j] = v[j];
             }
         } else if constexpr (N == 8) {
-            const u32x4 v = gload<u32x4>(static_cast<const unsigned short*>(p) + i, 0);
+            const u32x4 v = get(static_cast<const unsigned short*>(p) + i, 0, u32x4{});
 #pragma unroll
             for (int j = 0; j < 4; ++j) unpack2<DT>(v[j], o + 2 * j);
         } else {
-            const u32x2 v = gload<u32x2>(static_cast<const unsigned short*>(p) + i, 0);
+            const u32x2 v = get(static_cast<const unsigned short*>(p) + i, 0, u32x2{});
 #pragma unroll
             for (int j = 0; j < 2; ++j) unpack2<DT>(v[j], o + 2 * j);
         }
@@ -100,19 +122,22 @@ __device__ __forceinline__ void load_n(const void* p, int64_t i, int valid, bool
 #pragma unroll
     for (int j = 0; j < N; ++j) o[j] = j < valid ? load1<DT>(p, i + j) : 0.0f;
 }
-template <dp_dtype DT, int N>
+template <dp_dtype DT, int N, bool kOnce = false>
 __device__ __forceinline__ void store_n(void* p, int64_t i, int valid, bool vec, const float* x) {
+    const auto put = [](auto* at, int64_t k, auto v) {
+        if constexpr (kOnce) gstore_nt(at, k, v);
+        else gstore(at, k, v);
+    };
     if (vec && valid >= N) {
         if constexpr (DT == DP_F32) {
 #pragma unroll
             for (int k = 0; k < N / 4; ++k)
-                gstore<f32x4>(static_cast<float*>(p) + i, k, f32x4{x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]});
+                put(static_cast<float*>(p) + i, k, f32x4{x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]});
         } else if constexpr (N == 8) {
-            gstore<u32x4>(static_cast<unsigned short*>(p) + i, 0,
-                          u32x4{pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3]), pack2<DT>(x[4], x[5]),
-                                pack2<DT>(x[6], x[7])});
+            put(static_cast<unsigned short*>(p) + i, 0,
+                u32x4{pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3]), pack2<DT>(x[4], x[5]), pack2<DT>(x[6], x[7])});
         } else {
-            gstore<u32x2>(static_cast<unsigned short*>(p) + i, 0, u32x2{pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3])});
+            put(static_cast<unsigned short*>(p) + i, 0, u32x2{pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3])});
         }
         return;
     }

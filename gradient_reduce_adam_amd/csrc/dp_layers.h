@@ -26,7 +26,8 @@ struct EmbedGrad {
     float scale;
     int32_t n, id_bytes;
     bool overwrite;       // ACC = G, else ACC += G
-    bool vec_dy, vec_acc;
+    bool vec_dy, vec_acc;  // rows of dy and of the accumulators in vectors of 4 elements
+    bool vec_base;         // every accumulator's first row is aligned to 16 bytes
 };
 size_t embed_workspace(int64_t dim, int64_t tokens, int n);
 int64_t embed_waves(const EmbedGrad& a);  // workgroups of its largest launch, for one replica

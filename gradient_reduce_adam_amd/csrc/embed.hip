@@ -15,7 +15,7 @@
 //    position of a pair is the count of smaller digits, plus that of its digit
 //    in earlier spans, plus its rank within the span.  Ranks within a wave come
 //    from ballots (which lanes hold my digit), so equal ids keep their order.
-//    Spans of at most 4096 tokens are sorted in LDS by one workgroup a replica
+//    Lists of at most 16384 tokens are sorted in LDS by one workgroup a replica
 //    in a single launch.
 //  - The sorted list is cut into chunks of 32 pairs.  One wave sums one chunk
 //    over 256 columns (4 a lane), adding rows of dy in list order.  A run that
@@ -25,8 +25,9 @@
 //    batch is thus summed by all waves, and the order depends on nothing but
 //    the list.
 //  - When the gradient overwrites the accumulators, rows without a token have
-//    to become zero: further waves of the same launch find them by a binary
-//    search in the sorted ids and write each element of the table once.
+//    to become zero: further workgroups of the sort's first launch clear the
+//    tables meanwhile, so that the sort, which few CUs work on, costs nothing
+//    beside them.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -42,7 +43,7 @@ __device__ __forceinline__ int64_t load_id(const void* ids, int id_bytes, int64_
     return id_bytes == 8 ? gload<int64_t>(ids, i) : static_cast<int64_t>(gload<int32_t>(ids, i));
 }
 
-template <dp_dtype PT, dp_dtype OT>
+template <dp_dtype PT, dp_dtype OT, bool kOnce>
 __global__ void __launch_bounds__(64) k_embed(const void* table, int64_t rows, int64_t dim, float scale,
                                               const void* ids, int id_bytes, void* out, int64_t ld, bool vec) {
     const int64_t t = blockIdx.x;
@@ -65,16 +66,18 @@ __global__ void __launch_bounds__(64) k_embed(const void* table, int64_t rows, i
         const int valid = left >= 8 ? 8 : left > 0 ? static_cast<int>(left) : 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[k][j] = ok ? v[k][j] * scale : 0.0f;
-        store_n<OT, 8>(out, t * ld + c, valid, vec, v[k]);
+        store_n<OT, 8, kOnce>(out, t * ld + c, valid, vec, v[k]);
     }
 }
 
 // ---- the sort ----------------------------------------------------------------
-constexpr int kSortThreads = 256;
-constexpr int kSortItems = 16;
-constexpr int kTile = kSortThreads * kSortItems;  // pairs one workgroup ranks at a time
+constexpr int kSortThreads = 1024;
+constexpr int kSortWaves = kSortThreads / 64;
+constexpr int kTileItems = 4;                     // pairs per thread that the launches over spans rank at a time
+constexpr int kTile = kSortThreads * kTileItems;
 constexpr int kMaxSpans = 64;
 constexpr int kDigits = 256;
+constexpr int kSmallSort = 16 * kSortThreads;     // longest list sorted by one workgroup
 
 // The list of one replica during the sort, and the digit counts of its spans.
 struct SortBuf {
@@ -85,7 +88,7 @@ struct SortBuf {
 
 struct Ids {
     const void* p[DP_MAX_REPLICAS];
-    int32_t id_bytes;
+    int32_t id_bytes, n;
 };
 
 // The sort key of token t: its id, or `rows` for an id outside the table (they
@@ -97,45 +100,94 @@ __device__ __forceinline__ uint32_t key_of(const void* ids, int id_bytes, int64_
 
 __device__ __forceinline__ int lane_id() { return threadIdx.x & 63; }
 
-// How many lanes below this one hold the same 8-bit digit, and whether this is
-// the last that does (`mask`: the lanes that hold one at all).
+// Of the lanes in `mask`, those that hold the same 8-bit digit as this one: a
+// lane stays where its bit equals mine, mask & ~(lanes with the bit set ^ my bit).
 __device__ __forceinline__ uint64_t same_digit(uint32_t d, uint64_t mask) {
+    uint32_t lo = static_cast<uint32_t>(mask), hi = static_cast<uint32_t>(mask >> 32);
 #pragma unroll
     for (int b = 0; b < 8; ++b) {
-        const bool set = (d >> b) & 1;
-        const uint64_t m = __ballot(set);
-        mask &= set ? m : ~m;
+        const uint32_t mine = static_cast<uint32_t>(static_cast<int32_t>(d << (31 - b)) >> 31);
+        const uint64_t m = __ballot(mine != 0);
+        lo &= ~(static_cast<uint32_t>(m) ^ mine);
+        hi &= ~(static_cast<uint32_t>(m >> 32) ^ mine);
     }
-    return mask;
+    return static_cast<uint64_t>(hi) << 32 | lo;
 }
 
-// Ranks the pairs of one tile by a digit: item k of lane l of wave w is pair
-// (w * kSortItems + k) * 64 + l of the tile, so that waves hold consecutive
-// pairs.  `wave_count` [4][256] is cleared by the caller; afterwards it holds the
-// digits' counts of each wave, and rank[k] the number of earlier pairs of the
-// same wave with the same digit.
-__device__ __forceinline__ void rank_tile(const uint32_t (&key)[kSortItems], int shift, int valid,
-                                          volatile uint32_t (*wave_count)[kDigits],
-                                          uint32_t (&rank)[kSortItems]) {
-    const int w = threadIdx.x >> 6, l = lane_id();
+// The tables of every replica set to zero by further workgroups of the sort's
+// first launch: `elements` floats each, `groups` workgroups a table.
+struct Zeros {
+    float* acc[DP_MAX_REPLICAS];
+    int64_t elements, groups;
+    int32_t n;
+    bool vec;
+};
+constexpr int kZeroQuads = 4;  // 16-byte stores per thread
+constexpr int64_t kZeroSpan = int64_t{4} * kZeroQuads * kSortThreads;
+
+__device__ __forceinline__ void zero_table(const Zeros& z, int64_t group) {
+    float* p = z.acc[group / z.groups];
+    const int64_t i0 = group % z.groups * kZeroSpan, left = z.elements - i0;
+    if (z.vec && left >= kZeroSpan) {
 #pragma unroll
-    for (int k = 0; k < kSortItems; ++k) {
-        const bool in = (w * kSortItems + k) * 64 + l < valid;
+        for (int k = 0; k < kZeroQuads; ++k)
+            gstore<f32x4>(p + i0, k * kSortThreads + threadIdx.x, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+    } else {
+        for (int64_t i = threadIdx.x; i < left && i < kZeroSpan; i += kSortThreads) gstore<float>(p + i0, i, 0.0f);
+    }
+}
+
+// Counts of a tile's digits by wave, and scratch of the scan.
+struct TileCounts {
+    uint32_t wave[kSortWaves][kDigits];
+    uint32_t sum[kDigits / 64];
+};
+
+// Where the pairs of one tile go by a digit.  Item k of lane l of wave w is pair
+// (w * kItems + k) * 64 + l of the tile, so that waves hold consecutive pairs; the
+// first `valid` exist.  A pair goes to first(its digit) + the pairs before it
+// in the tile with the same digit: rank[k] is its rank within the wave, and
+// c.wave holds, afterwards, the place of each wave's first pair of each digit.
+// `place` (of the 256 threads of the first waves, one a digit) maps the
+// tile's count of the digit to the place of its first pair.
+template <int kItems, typename F>
+__device__ __forceinline__ void rank_tile(const uint32_t (&key)[kItems], int shift, int valid, TileCounts& c,
+                                          uint32_t (&rank)[kItems], F&& place) {
+    const int w = threadIdx.x >> 6, l = lane_id();
+    for (int i = threadIdx.x; i < kSortWaves * kDigits; i += kSortThreads) (&c.wave[0][0])[i] = 0;
+    __syncthreads();
+    volatile uint32_t* count = c.wave[w];
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+        const bool in = (w * kItems + k) * 64 + l < valid;
         const uint32_t d = (key[k] >> shift) & (kDigits - 1);
         const uint64_t peers = same_digit(d, __ballot(in));
         if (in) {
-            const int before = __popcll(peers & ((uint64_t{1} << l) - 1));
-            rank[k] = wave_count[w][d] + before;
-            // the last of the peers moves the count on (the wave's lanes have
-            // all read it: they run in step and LDS accesses keep their order)
+            rank[k] = count[d] + __popcll(peers & ((uint64_t{1} << l) - 1));
+            // the last of the peers moves the count on; all of them have read
+            // it (a wave's LDS accesses keep their order)
             __builtin_amdgcn_wave_barrier();
-            if ((peers >> l) == 1) wave_count[w][d] = rank[k] + 1;
+            if ((peers >> l) == 1) count[d] = rank[k] + 1;
         }
         __builtin_amdgcn_wave_barrier();
     }
+    __syncthreads();
+    uint32_t total = 0;
+    if (threadIdx.x < kDigits)
+#pragma unroll
+        for (int k = 0; k < kSortWaves; ++k) total += c.wave[k][threadIdx.x];
+    uint32_t base = place(total);
+    if (threadIdx.x < kDigits)
+#pragma unroll
+        for (int k = 0; k < kSortWaves; ++k) {
+            const uint32_t n = c.wave[k][threadIdx.x];
+            c.wave[k][threadIdx.x] = base;
+            base += n;
+        }
+    __syncthreads();
 }
 
-// Exclusive sums over 256 values, one per thread of the workgroup.
+// Exclusive sums over 256 values, one in each of the first 256 threads.
 __device__ __forceinline__ uint32_t exclusive_scan(uint32_t x, uint32_t* wave_sum) {
     const int l = lane_id(), w = threadIdx.x >> 6;
     uint32_t s = x;
@@ -144,150 +196,133 @@ __device__ __forceinline__ uint32_t exclusive_scan(uint32_t x, uint32_t* wave_su
         const uint32_t up = __shfl_up(s, d);
         if (l >= d) s += up;
     }
-    if (l == 63) wave_sum[w] = s;
+    if (l == 63 && threadIdx.x < kDigits) wave_sum[w] = s;
     __syncthreads();
     uint32_t base = 0;
 #pragma unroll
-    for (int k = 0; k < kSortThreads / 64; ++k) base += k < w ? wave_sum[k] : 0;
+    for (int k = 0; k < kDigits / 64; ++k) base += k < w ? wave_sum[k] : 0;
     __syncthreads();
     return base + s - x;
 }
 
-// The whole sort of a list of at most kTile pairs, in LDS: one workgroup a replica.
-__global__ void __launch_bounds__(kSortThreads) k_sort_small(Ids ids, SortBuf sb, int64_t rows, int64_t tokens,
-                                                             int passes) {
-    __shared__ uint32_t lk[kTile], lp[kTile];
-    __shared__ uint32_t wave_count[kSortThreads / 64][kDigits];
-    __shared__ uint32_t wave_sum[kSortThreads / 64];
+// The whole sort of a list of at most kItems * 1024 pairs, in LDS: one
+// workgroup a replica, and those behind them for the zeros.
+template <int kItems>
+__global__ void __launch_bounds__(kSortThreads) k_sort_small(Ids ids, SortBuf sb, Zeros z, int64_t rows,
+                                                             int64_t tokens, int passes) {
+    __shared__ uint32_t lk[kItems * kSortThreads], lp[kItems * kSortThreads];
+    __shared__ TileCounts c;
+    if (static_cast<int>(blockIdx.x) >= ids.n) {
+        zero_table(z, blockIdx.x - ids.n);
+        return;
+    }
     const int r = blockIdx.x, w = threadIdx.x >> 6, l = lane_id();
     const int valid = static_cast<int>(tokens);
-    uint32_t key[kSortItems], pos[kSortItems], rank[kSortItems];
+    uint32_t key[kItems], pos[kItems], rank[kItems];
 #pragma unroll
-    for (int k = 0; k < kSortItems; ++k) {
-        const int i = (w * kSortItems + k) * 64 + l;
+    for (int k = 0; k < kItems; ++k) {
+        const int i = (w * kItems + k) * 64 + l;
         pos[k] = i;
         key[k] = i < valid ? key_of(ids.p[r], ids.id_bytes, i, rows) : 0;
     }
-    for (int p = 0; p < passes; ++p) {
-        for (int i = threadIdx.x; i < kDigits * (kSortThreads / 64); i += kSortThreads) (&wave_count[0][0])[i] = 0;
-        __syncthreads();
-        rank_tile(key, 8 * p, valid, wave_count, rank);
-        __syncthreads();
-        uint32_t total = 0;
+    for (int p = 0;; ++p) {
+        rank_tile<kItems>(key, 8 * p, valid, c, rank, [&](uint32_t total) { return exclusive_scan(total, c.sum); });
+        const bool last = p + 1 == passes;
 #pragma unroll
-        for (int k = 0; k < kSortThreads / 64; ++k) total += wave_count[k][threadIdx.x];
-        uint32_t base = exclusive_scan(total, wave_sum);
-#pragma unroll
-        for (int k = 0; k < kSortThreads / 64; ++k) {
-            const uint32_t c = wave_count[k][threadIdx.x];
-            wave_count[k][threadIdx.x] = base;
-            base += c;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < kSortItems; ++k) {
-            const int i = (w * kSortItems + k) * 64 + l;
-            if (i < valid) {
-                const uint32_t at = wave_count[w][(key[k] >> (8 * p)) & (kDigits - 1)] + rank[k];
+        for (int k = 0; k < kItems; ++k) {
+            if ((w * kItems + k) * 64 + l >= valid) continue;
+            const uint32_t at = c.wave[w][(key[k] >> (8 * p)) & (kDigits - 1)] + rank[k];
+            if (last) {
+                sb.key[0][r * tokens + at] = key[k];
+                sb.pos[0][r * tokens + at] = pos[k];
+            } else {
                 lk[at] = key[k];
                 lp[at] = pos[k];
             }
         }
+        if (last) break;
         __syncthreads();
 #pragma unroll
-        for (int k = 0; k < kSortItems; ++k) {
-            const int i = (w * kSortItems + k) * 64 + l;
+        for (int k = 0; k < kItems; ++k) {
+            const int i = (w * kItems + k) * 64 + l;
             if (i < valid) {
                 key[k] = lk[i];
                 pos[k] = lp[i];
             }
         }
-        __syncthreads();
-    }
-#pragma unroll
-    for (int k = 0; k < kSortItems; ++k) {
-        const int i = (w * kSortItems + k) * 64 + l;
-        if (i < valid) {
-            sb.key[0][r * tokens + i] = key[k];
-            sb.pos[0][r * tokens + i] = pos[k];
-        }
     }
 }
 
-// Digit counts of each span of each replica (grid: spans x replicas).
-__global__ void __launch_bounds__(kSortThreads) k_sort_count(Ids ids, SortBuf sb, int from, bool first, int64_t rows,
-                                                             int64_t tokens, int64_t span, int shift) {
+// Digit counts of each span of each replica (grid: spans x replicas), and
+// workgroups behind those of the last replica for the zeros.
+__global__ void __launch_bounds__(kSortThreads) k_sort_count(Ids ids, SortBuf sb, Zeros z, int from, bool first,
+                                                             int64_t rows, int64_t tokens, int64_t span, int spans,
+                                                             int shift) {
     __shared__ uint32_t c[kDigits];
-    const int r = blockIdx.y;
-    c[threadIdx.x] = 0;
+    if (static_cast<int>(blockIdx.x) >= spans * ids.n) {
+        zero_table(z, blockIdx.x - spans * ids.n);
+        return;
+    }
+    const int r = blockIdx.x / spans, block = blockIdx.x % spans;
+    if (threadIdx.x < kDigits) c[threadIdx.x] = 0;
     __syncthreads();
-    const int64_t lo = blockIdx.x * span, hi = lo + span < tokens ? lo + span : tokens;
+    const int64_t lo = block * span, hi = lo + span < tokens ? lo + span : tokens;
     for (int64_t i = lo + threadIdx.x; i < hi; i += kSortThreads) {
         const uint32_t k = first ? key_of(ids.p[r], ids.id_bytes, i, rows) : sb.key[from][r * tokens + i];
         atomicAdd(&c[(k >> shift) & (kDigits - 1)], 1u);
     }
     __syncthreads();
-    sb.counts[(r * kMaxSpans + blockIdx.x) * kDigits + threadIdx.x] = c[threadIdx.x];
+    if (threadIdx.x < kDigits) sb.counts[(r * kMaxSpans + block) * kDigits + threadIdx.x] = c[threadIdx.x];
 }
 
 // Places the pairs of each span by a digit.
 __global__ void __launch_bounds__(kSortThreads) k_sort_place(Ids ids, SortBuf sb, int from, bool first, int64_t rows,
                                                              int64_t tokens, int64_t span, int spans, int shift) {
-    __shared__ uint32_t wave_count[kSortThreads / 64][kDigits];
-    __shared__ uint32_t next[kDigits];  // where the span's next pair of each digit goes
-    __shared__ uint32_t wave_sum[kSortThreads / 64];
+    __shared__ TileCounts c;
     const int r = blockIdx.y, w = threadIdx.x >> 6, l = lane_id();
+    uint32_t next = 0;  // of a digit: where the span's next pair goes
     {
         uint32_t total = 0, before = 0;
-        const uint32_t* c = sb.counts + static_cast<int64_t>(r) * kMaxSpans * kDigits + threadIdx.x;
-        for (int s = 0; s < spans; ++s) {
-            const uint32_t x = c[s * kDigits];
-            before += s < static_cast<int>(blockIdx.x) ? x : 0;
-            total += x;
-        }
-        next[threadIdx.x] = exclusive_scan(total, wave_sum) + before;
+        const uint32_t* n = sb.counts + static_cast<int64_t>(r) * kMaxSpans * kDigits + threadIdx.x;
+        if (threadIdx.x < kDigits)
+            for (int s = 0; s < spans; ++s) {
+                const uint32_t x = n[s * kDigits];
+                before += s < static_cast<int>(blockIdx.x) ? x : 0;
+                total += x;
+            }
+        next = exclusive_scan(total, c.sum) + before;
     }
     const int64_t lo = blockIdx.x * span, hi = lo + span < tokens ? lo + span : tokens;
     for (int64_t t0 = lo; t0 < hi; t0 += kTile) {
         const int valid = static_cast<int>(hi - t0 < kTile ? hi - t0 : kTile);
-        uint32_t key[kSortItems], pos[kSortItems], rank[kSortItems];
+        uint32_t key[kTileItems], pos[kTileItems], rank[kTileItems];
 #pragma unroll
-        for (int k = 0; k < kSortItems; ++k) {
-            const int i = (w * kSortItems + k) * 64 + l;
+        for (int k = 0; k < kTileItems; ++k) {
+            const int i = (w * kTileItems + k) * 64 + l;
             key[k] = pos[k] = 0;
             if (i < valid) {
                 key[k] = first ? key_of(ids.p[r], ids.id_bytes, t0 + i, rows) : sb.key[from][r * tokens + t0 + i];
                 pos[k] = first ? static_cast<uint32_t>(t0 + i) : sb.pos[from][r * tokens + t0 + i];
             }
         }
-        for (int i = threadIdx.x; i < kDigits * (kSortThreads / 64); i += kSortThreads) (&wave_count[0][0])[i] = 0;
-        __syncthreads();
-        rank_tile(key, shift, valid, wave_count, rank);
-        __syncthreads();
-        uint32_t base = next[threadIdx.x];
+        rank_tile<kTileItems>(key, shift, valid, c, rank, [&](uint32_t total) {
+            const uint32_t at = next;
+            next += total;
+            return at;
+        });
 #pragma unroll
-        for (int k = 0; k < kSortThreads / 64; ++k) {
-            const uint32_t c = wave_count[k][threadIdx.x];
-            wave_count[k][threadIdx.x] = base;
-            base += c;
-        }
-        next[threadIdx.x] = base;
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < kSortItems; ++k) {
-            const int i = (w * kSortItems + k) * 64 + l;
-            if (i < valid) {
-                const int64_t at = r * tokens + wave_count[w][(key[k] >> shift) & (kDigits - 1)] + rank[k];
-                sb.key[from ^ 1][at] = key[k];
-                sb.pos[from ^ 1][at] = pos[k];
-            }
+        for (int k = 0; k < kTileItems; ++k) {
+            if ((w * kTileItems + k) * 64 + l >= valid) continue;
+            const int64_t at = r * tokens + c.wave[w][(key[k] >> shift) & (kDigits - 1)] + rank[k];
+            sb.key[from ^ 1][at] = key[k];
+            sb.pos[from ^ 1][at] = pos[k];
         }
         __syncthreads();
     }
 }
 
 // ---- the sums ----------------------------------------------------------------
-constexpr int kChunk = 32;      // pairs of the sorted list per wave
+constexpr int kChunk = 16;      // pairs of the sorted list per wave
 constexpr int kColumns = 256;   // columns per wave, 4 a lane
 constexpr int kBatch = 8;       // rows of dy in flight per wave
 
@@ -298,58 +333,33 @@ struct GradArgs {
     const uint32_t* pos;
     float* part;          // [n][chunks][2][dim]: a chunk's first and last run where they cross its ends
     int64_t rows, dim, tokens, ld;
-    int64_t chunks, slices, zero_rows;
+    int64_t chunks, slices;
     float scale;
     bool vec_dy, vec_acc;
 };
 
-// ACC of 4 columns (+)= scale * s.
+// The accumulator of 4 columns of a row, if the gradient is added to it.
 template <bool kOver>
-__device__ __forceinline__ void put(const GradArgs& a, float* acc, int64_t row, int64_t c, int valid, const float* s) {
+__device__ __forceinline__ void fetch(const GradArgs& a, const float* acc, int64_t row, int64_t c, int valid, float* old) {
+    if constexpr (!kOver) load_n<DP_F32, 4>(acc, row * a.dim + c, valid, a.vec_acc, old);
+}
+// ACC = scale * s, or what was fetched of it + scale * s.
+template <bool kOver>
+__device__ __forceinline__ void put(const GradArgs& a, float* acc, int64_t row, int64_t c, int valid, const float* s,
+                                    const float* old) {
     float v[4];
-    const int64_t at = row * a.dim + c;
-    if constexpr (!kOver) load_n<DP_F32, 4>(acc, at, valid, a.vec_acc, v);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = kOver ? a.scale * s[j] : v[j] + a.scale * s[j];
-    store_n<DP_F32, 4>(acc, at, valid, a.vec_acc, v);
+    for (int j = 0; j < 4; ++j) v[j] = kOver ? a.scale * s[j] : old[j] + a.scale * s[j];
+    store_n<DP_F32, 4>(acc, row * a.dim + c, valid, a.vec_acc, v);
 }
 
-// Zeros in the rows [row0, row0 + zero_rows) that no token holds.
-__device__ __forceinline__ void zero_rows(const GradArgs& a, float* acc, const uint32_t* key, int64_t row0) {
-    const int l = lane_id();
-    const int64_t mine = row0 + l;
-    bool absent = false;
-    if (l < a.zero_rows && mine < a.rows) {
-        int64_t lo = 0, hi = a.tokens;  // first pair whose id is not below mine
-        while (lo < hi) {
-            const int64_t mid = (lo + hi) >> 1;
-            if (key[mid] < mine) lo = mid + 1;
-            else hi = mid;
-        }
-        absent = lo == a.tokens || key[lo] != mine;
-    }
-    uint64_t todo = __ballot(absent);
-    const float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    while (todo) {
-        const int64_t row = row0 + __builtin_ctzll(todo);
-        todo &= todo - 1;
-        for (int64_t c = 4 * l; c < a.dim; c += kColumns)
-            store_n<DP_F32, 4>(acc, row * a.dim + c, static_cast<int>(a.dim - c < 4 ? a.dim - c : 4), a.vec_acc, zero);
-    }
-}
-
-// Grid: (chunks * slices + waves of zero_rows rows) x replicas, one wave each.
+// Grid: (chunks * slices) x replicas, one wave each.
 template <dp_dtype DT, bool kOver>
 __global__ void __launch_bounds__(64) k_embed_sum(GradArgs a) {
     const int r = blockIdx.y, l = lane_id();
     const uint32_t* key = a.key + r * a.tokens;
     const uint32_t* pos = a.pos + r * a.tokens;
     float* acc = a.acc[r];
-    const int64_t sums = a.chunks * a.slices;
-    if (static_cast<int64_t>(blockIdx.x) >= sums) {
-        if constexpr (kOver) zero_rows(a, acc, key, (blockIdx.x - sums) * a.zero_rows);
-        return;
-    }
     const int64_t chunk = blockIdx.x / a.slices, c = (blockIdx.x % a.slices) * kColumns + 4 * l;
     const int64_t left = a.dim - c;
     const int valid = left >= 4 ? 4 : left > 0 ? static_cast<int>(left) : 0;
@@ -369,11 +379,13 @@ __global__ void __launch_bounds__(64) k_embed_sum(GradArgs a) {
     const uint32_t before = __builtin_amdgcn_readlane(k, 62), behind = __builtin_amdgcn_readlane(k, 63);
     float* part = a.part + (r * a.chunks + chunk) * 2 * a.dim;
     const bool vec_part = a.dim % 4 == 0;
+    // bit i: pair i is the last of its run in this chunk
+    const uint32_t after = __shfl_down(k, 1);
+    const uint64_t ends = __ballot(l < count && (l == count - 1 || k != after));
     float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    uint32_t run = __builtin_amdgcn_readlane(k, 0);
-    bool head = run == before;  // the current run began in an earlier chunk
+    bool head = __builtin_amdgcn_readlane(k, 0) == before;  // the current run began in an earlier chunk
     for (int b = 0; b < count; b += kBatch) {
-        float v[kBatch][4];
+        float v[kBatch][4], old[kBatch][4];
         uint32_t kk[kBatch];
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
@@ -383,28 +395,24 @@ __global__ void __launch_bounds__(64) k_embed_sum(GradArgs a) {
             // a batch past the chunk's end, or an id outside the table, reads no row
             const bool read = b + j < count && kk[j] < a.rows;
             load_n<DT, 4>(a.dy[r], row * a.ld + c, read ? valid : 0, a.vec_dy, v[j]);
+            fetch<kOver>(a, acc, kk[j], c, read && (ends >> i & 1) ? valid : 0, old[j]);
         }
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
             if (b + j >= count) break;
-            if (kk[j] != run) {
-                if (run < a.rows) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) s[q] += v[j][q];
+            if (ends >> (b + j) & 1) {
+                if (kk[j] < a.rows) {
                     if (head) store_n<DP_F32, 4>(part, c, valid, vec_part, s);
-                    else put<kOver>(a, acc, run, c, valid, s);
+                    else if (b + j == count - 1 && kk[j] == behind) store_n<DP_F32, 4>(part + a.dim, c, valid, vec_part, s);
+                    else put<kOver>(a, acc, kk[j], c, valid, s, old[j]);
                 }
                 head = false;
-                run = kk[j];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) s[q] = 0.0f;
             }
-#pragma unroll
-            for (int q = 0; q < 4; ++q) s[q] += v[j][q];
         }
-    }
-    if (run < a.rows) {
-        if (head) store_n<DP_F32, 4>(part, c, valid, vec_part, s);
-        else if (run == behind) store_n<DP_F32, 4>(part + a.dim, c, valid, vec_part, s);
-        else put<kOver>(a, acc, run, c, valid, s);
     }
 }
 
@@ -432,7 +440,8 @@ __global__ void __launch_bounds__(64) k_embed_join(GradArgs a) {
     const int valid = left >= 4 ? 4 : left > 0 ? static_cast<int>(left) : 0;
     const bool vec_part = a.dim % 4 == 0;
     const float* part = a.part + (r * a.chunks + chunk) * 2 * a.dim;
-    float s[4];
+    float s[4], old[4];
+    fetch<kOver>(a, a.acc[r], run, c, valid, old);
     load_n<DP_F32, 4>(part + a.dim, c, valid, vec_part, s);
     for (int64_t b = 0; b < n; b += kBatch) {
         float v[kBatch][4];
@@ -444,20 +453,13 @@ __global__ void __launch_bounds__(64) k_embed_join(GradArgs a) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) s[q] += v[j][q];
     }
-    put<kOver>(a, a.acc[r], run, c, valid, s);
+    put<kOver>(a, a.acc[r], run, c, valid, s, old);
 }
 
 int64_t round256(int64_t x) { return (x + 255) & ~int64_t{255}; }
 int64_t chunks_of(int64_t tokens) { return (tokens + kChunk - 1) / kChunk; }
 
 int64_t slices_of(int64_t dim) { return (dim + kColumns - 1) / kColumns; }
-
-// Rows of zeros per wave: about 64 KiB to write, a power of two of at most 64 rows.
-int64_t zero_rows_per_wave(int64_t dim) {
-    int64_t z = 64;
-    while (z > 1 && z * dim > 16384) z >>= 1;
-    return z;
-}
 
 int passes_of(int64_t rows) {
     int p = 1;
@@ -472,15 +474,24 @@ hipError_t launch_embed(dp_dtype pdt, dp_dtype odt, const void* table, int64_t r
                         hipStream_t stream) {
     if (tokens == 0) return hipSuccess;
     const dim3 grid(static_cast<unsigned>(tokens), static_cast<unsigned>((dim + kLookupSpan - 1) / kLookupSpan));
-#define DP_GO(P, O)                                                                                              \
-    if (pdt == P && odt == O)                                                                                    \
-    hipLaunchKernelGGL((k_embed<P, O>), grid, dim3(64), 0, stream, table, rows, dim, scale, ids, id_bytes, out, ld, vec)
-    DP_GO(DP_BF16, DP_BF16);
-    DP_GO(DP_BF16, DP_F16);
-    DP_GO(DP_BF16, DP_F32);
-    DP_GO(DP_F16, DP_BF16);
-    DP_GO(DP_F16, DP_F16);
-    DP_GO(DP_F16, DP_F32);
+    // An output beyond the 32 MiB of all L2 caches cannot wait there for its
+    // reader, and stored past them it leaves them to the table's rows: 32768 x
+    // 4096 bf16 takes 58 us instead of 81.  A smaller one stays for its reader.
+    const bool once = tokens * dim * (odt == DP_F32 ? 4 : 2) > (int64_t{32} << 20);
+#define DP_GO2(P, O, S) \
+    hipLaunchKernelGGL((k_embed<P, O, S>), grid, dim3(64), 0, stream, table, rows, dim, scale, ids, id_bytes, out, ld, vec)
+#define DP_GO(P, O)                    \
+    if (pdt == P && odt == O) {        \
+        if (once) DP_GO2(P, O, true);  \
+        else DP_GO2(P, O, false);      \
+    }
+    DP_GO(DP_BF16, DP_BF16)
+    DP_GO(DP_BF16, DP_F16)
+    DP_GO(DP_BF16, DP_F32)
+    DP_GO(DP_F16, DP_BF16)
+    DP_GO(DP_F16, DP_F16)
+    DP_GO(DP_F16, DP_F32)
+#undef DP_GO2
 #undef DP_GO
     return hipGetLastError();
 }
@@ -491,8 +502,7 @@ size_t embed_workspace(int64_t dim, int64_t tokens, int n) {
 }
 
 int64_t embed_waves(const EmbedGrad& a) {
-    const int64_t z = zero_rows_per_wave(a.dim);
-    return chunks_of(a.tokens) * slices_of(a.dim) + (a.overwrite ? (a.rows + z - 1) / z : 0);
+    return chunks_of(a.tokens) * slices_of(a.dim);
 }
 
 hipError_t launch_embed_grad(dp_dtype dt, const EmbedGrad& a, void* workspace, hipStream_t stream) {
@@ -515,17 +525,36 @@ hipError_t launch_embed_grad(dp_dtype dt, const EmbedGrad& a, void* workspace, h
         g.dy[r] = a.dy[r];
         g.acc[r] = a.acc[r];
     }
+    ids.n = a.tokens > 0 ? a.n : 0;
+    Zeros z{};
+    if (a.overwrite) {
+        z.n = a.n;
+        z.elements = a.rows * a.dim;
+        z.vec = a.vec_base;
+        z.groups = (z.elements + kZeroSpan - 1) / kZeroSpan;
+        for (int r = 0; r < a.n; ++r) z.acc[r] = a.acc[r];
+    }
+    const int64_t zeros = z.groups * z.n;
+    if (ids.n + zeros == 0) return hipSuccess;
     const int passes = passes_of(a.rows);
     int from = 0;
-    if (a.tokens > 0 && a.tokens <= kTile) {
-        hipLaunchKernelGGL(k_sort_small, dim3(a.n), dim3(kSortThreads), 0, stream, ids, sb, a.rows, a.tokens, passes);
-    } else if (a.tokens > 0) {
+    if (a.tokens <= kSmallSort) {
+        const dim3 sgrid(static_cast<unsigned>(ids.n + zeros));
+#define DP_GO(K) \
+    hipLaunchKernelGGL((k_sort_small<K>), sgrid, dim3(kSortThreads), 0, stream, ids, sb, z, a.rows, a.tokens, passes)
+        if (a.tokens <= kSortThreads) DP_GO(1);
+        else if (a.tokens <= 4 * kSortThreads) DP_GO(4);
+        else if (a.tokens <= 8 * kSortThreads) DP_GO(8);
+        else DP_GO(16);
+#undef DP_GO
+    } else {
         const int64_t tiles = (a.tokens + kTile - 1) / kTile;
         const int64_t span = (tiles + kMaxSpans - 1) / kMaxSpans * kTile;
         const int spans = static_cast<int>((a.tokens + span - 1) / span);
         for (int p = 0; p < passes; ++p) {
-            hipLaunchKernelGGL(k_sort_count, dim3(spans, a.n), dim3(kSortThreads), 0, stream, ids, sb, from, p == 0,
-                               a.rows, a.tokens, span, 8 * p);
+            const dim3 cgrid(static_cast<unsigned>(spans * a.n + (p == 0 ? zeros : 0)));
+            hipLaunchKernelGGL(k_sort_count, cgrid, dim3(kSortThreads), 0, stream, ids, sb, z, from, p == 0, a.rows,
+                               a.tokens, span, spans, 8 * p);
             hipLaunchKernelGGL(k_sort_place, dim3(spans, a.n), dim3(kSortThreads), 0, stream, ids, sb, from, p == 0,
                                a.rows, a.tokens, span, spans, 8 * p);
             from ^= 1;
@@ -544,10 +573,8 @@ hipError_t launch_embed_grad(dp_dtype dt, const EmbedGrad& a, void* workspace, h
     g.scale = a.scale;
     g.vec_dy = a.vec_dy;
     g.vec_acc = a.vec_acc;
-    g.zero_rows = zero_rows_per_wave(a.dim);
-    const int64_t sums = g.chunks * g.slices, waves = embed_waves(a);
-    if (waves == 0) return hipSuccess;
-    const dim3 grid(static_cast<unsigned>(waves), static_cast<unsigned>(a.n));
+    if (g.chunks == 0) return hipSuccess;
+    const dim3 grid(static_cast<unsigned>(embed_waves(a)), static_cast<unsigned>(a.n));
 #define DP_GO(D)                                                                                   \
     if (dt == D) {                                                                                 \
         if (a.overwrite) hipLaunchKernelGGL((k_embed_sum<D, true>), grid, dim3(64), 0, stream, g); \
@@ -559,9 +586,8 @@ hipError_t launch_embed_grad(dp_dtype dt, const EmbedGrad& a, void* workspace, h
 #undef DP_GO
     e = hipGetLastError();
     if (e != hipSuccess || g.chunks < 2) return e;
-    const dim3 jgrid(static_cast<unsigned>(sums), static_cast<unsigned>(a.n));
-    if (a.overwrite) hipLaunchKernelGGL((k_embed_join<true>), jgrid, dim3(64), 0, stream, g);
-    else hipLaunchKernelGGL((k_embed_join<false>), jgrid, dim3(64), 0, stream, g);
+    if (a.overwrite) hipLaunchKernelGGL((k_embed_join<true>), grid, dim3(64), 0, stream, g);
+    else hipLaunchKernelGGL((k_embed_join<false>), grid, dim3(64), 0, stream, g);
     return hipGetLastError();
 }
 

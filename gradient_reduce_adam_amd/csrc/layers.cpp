@@ -225,7 +225,7 @@ dp_status dpl_accumulate_embed(dp_plan* plan, const dpl_table* table, int64_t to
     if (!dtype_ok(dtype)) return fail(DP_ERR_INVALID_ARG, "%s: unknown dtype %d", where, static_cast<int>(dtype));
     if (!ids || !dy) return fail(DP_ERR_INVALID_ARG, "%s: null argument", where);
     a.n = plan->n;
-    a.vec_dy = a.vec_acc = true;
+    a.vec_dy = true;
     for (int32_t r = 0; r < plan->n; ++r) {
         s = check_ids(where, ids[r], tokens, table->id_bytes);
         if (s == DP_OK) s = check_rows(where, "dy", dy[r], tokens, table->dim, ld, esize(dtype));
@@ -240,7 +240,9 @@ dp_status dpl_accumulate_embed(dp_plan* plan, const dpl_table* table, int64_t to
     s = dpapi::part_begin(plan, &table->tensor, 1, first != 0, where, a.acc, &overwrite);
     if (s == DP_OK) s = check_acc(where, a.acc, plan->n);
     if (s != DP_OK) return s;
-    for (int32_t r = 0; r < plan->n; ++r) a.vec_acc = a.vec_acc && vec_rows(a.acc[r], table->dim, 4, 16);
+    a.vec_base = true;
+    for (int32_t r = 0; r < plan->n; ++r) a.vec_base = a.vec_base && multiple(a.acc[r], 16);
+    a.vec_acc = a.vec_base && table->dim % 4 == 0;
     a.dim = table->dim;
     a.tokens = tokens;
     a.ld = ld;
