@@ -10,58 +10,6 @@
 
 namespace dpk {
 
-// VW (4 or 8) elements as they lie in memory.
-template <dp_dtype DT, int VW>
-struct Raw {
-    static constexpr int kWords = VW * (DT == DP_F32 ? 4 : 2) / 4;
-    unsigned int w[kWords];
-};
-
-template <dp_dtype DT, int VW>
-__device__ __forceinline__ Raw<DT, VW> load_raw(const void* p, int64_t i, int valid, bool vec) {
-    constexpr int kWords = Raw<DT, VW>::kWords;
-    Raw<DT, VW> q;
-    if (vec && valid >= VW) {
-        const char* at = static_cast<const char*>(p) + i * (DT == DP_F32 ? 4 : 2);
-        if constexpr (kWords == 2) {
-            const u32x2 v = gload<u32x2>(at, 0);
-            q.w[0] = v[0];
-            q.w[1] = v[1];
-        } else {
-#pragma unroll
-            for (int k = 0; k < kWords / 4; ++k) {
-                const u32x4 v = gload<u32x4>(at, k);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) q.w[4 * k + j] = v[j];
-            }
-        }
-        return q;
-    }
-    if constexpr (DT == DP_F32) {
-#pragma unroll
-        for (int j = 0; j < VW; ++j) q.w[j] = j < valid ? gload<unsigned int>(p, i + j) : 0u;
-    } else {
-#pragma unroll
-        for (int j = 0; j < VW / 2; ++j) {
-            const unsigned int lo = 2 * j < valid ? gload<unsigned short>(p, i + 2 * j) : 0u;
-            const unsigned int hi = 2 * j + 1 < valid ? gload<unsigned short>(p, i + 2 * j + 1) : 0u;
-            q.w[j] = lo | hi << 16;
-        }
-    }
-    return q;
-}
-
-template <dp_dtype DT, int VW>
-__device__ __forceinline__ void expand(const Raw<DT, VW>& q, float* o) {
-    if constexpr (DT == DP_F32) {
-#pragma unroll
-        for (int j = 0; j < VW; ++j) o[j] = __builtin_bit_cast(float, q.w[j]);
-    } else {
-#pragma unroll
-        for (int j = 0; j < VW / 2; ++j) unpack2<DT>(q.w[j], o + 2 * j);
-    }
-}
-
 // Threads of a workgroup whose rows are held by nt threads each.
 constexpr int block_of(int nt) { return nt < 256 ? 256 : nt; }
 

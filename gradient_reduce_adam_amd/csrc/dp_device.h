@@ -93,27 +93,22 @@ __device__ __forceinline__ float wave_sum(float x) {
 // `valid` exist (the others come back as zero, or are not written).  `vec`:
 // the address is a multiple of the vector's bytes (16 at most), so that whole
 // vectors go in one or two accesses.
-// kOnce: the data is used once, so it need not stay in the caches.
-template <dp_dtype DT, int N, bool kOnce = false>
+template <dp_dtype DT, int N>
 __device__ __forceinline__ void load_n(const void* p, int64_t i, int valid, bool vec, float* o) {
-    const auto get = [](const auto* at, int64_t k, auto like) {
-        if constexpr (kOnce) return gload_nt<decltype(like)>(at, k);
-        else return gload<decltype(like)>(at, k);
-    };
     if (vec && valid >= N) {
         if constexpr (DT == DP_F32) {
 #pragma unroll
             for (int k = 0; k < N / 4; ++k) {
-                const f32x4 v = get(static_cast<const float*>(p) + i, k, f32x4{});
+                const f32x4 v = gload<f32x4>(static_cast<const float*>(p) + i, k);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) o[4 * k + j] = v[j];
             }
         } else if constexpr (N == 8) {
-            const u32x4 v = get(static_cast<const unsigned short*>(p) + i, 0, u32x4{});
+            const u32x4 v = gload<u32x4>(static_cast<const unsigned short*>(p) + i, 0);
 #pragma unroll
             for (int j = 0; j < 4; ++j) unpack2<DT>(v[j], o + 2 * j);
         } else {
-            const u32x2 v = get(static_cast<const unsigned short*>(p) + i, 0, u32x2{});
+            const u32x2 v = gload<u32x2>(static_cast<const unsigned short*>(p) + i, 0);
 #pragma unroll
             for (int j = 0; j < 2; ++j) unpack2<DT>(v[j], o + 2 * j);
         }
@@ -122,6 +117,7 @@ __device__ __forceinline__ void load_n(const void* p, int64_t i, int valid, bool
 #pragma unroll
     for (int j = 0; j < N; ++j) o[j] = j < valid ? load1<DT>(p, i + j) : 0.0f;
 }
+// kOnce: the data is not read again soon, so it need not stay in the caches.
 template <dp_dtype DT, int N, bool kOnce = false>
 __device__ __forceinline__ void store_n(void* p, int64_t i, int valid, bool vec, const float* x) {
     const auto put = [](auto* at, int64_t k, auto v) {
@@ -144,6 +140,58 @@ __device__ __forceinline__ void store_n(void* p, int64_t i, int valid, bool vec,
 #pragma unroll
     for (int j = 0; j < N; ++j)
         if (j < valid) store1<DT>(p, i + j, x[j]);
+}
+
+// VW (4 or 8) elements as they lie in memory.
+template <dp_dtype DT, int VW>
+struct Raw {
+    static constexpr int kWords = VW * (DT == DP_F32 ? 4 : 2) / 4;
+    unsigned int w[kWords];
+};
+
+template <dp_dtype DT, int VW>
+__device__ __forceinline__ Raw<DT, VW> load_raw(const void* p, int64_t i, int valid, bool vec) {
+    constexpr int kWords = Raw<DT, VW>::kWords;
+    Raw<DT, VW> q;
+    if (vec && valid >= VW) {
+        const char* at = static_cast<const char*>(p) + i * (DT == DP_F32 ? 4 : 2);
+        if constexpr (kWords == 2) {
+            const u32x2 v = gload<u32x2>(at, 0);
+            q.w[0] = v[0];
+            q.w[1] = v[1];
+        } else {
+#pragma unroll
+            for (int k = 0; k < kWords / 4; ++k) {
+                const u32x4 v = gload<u32x4>(at, k);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) q.w[4 * k + j] = v[j];
+            }
+        }
+        return q;
+    }
+    if constexpr (DT == DP_F32) {
+#pragma unroll
+        for (int j = 0; j < VW; ++j) q.w[j] = j < valid ? gload<unsigned int>(p, i + j) : 0u;
+    } else {
+#pragma unroll
+        for (int j = 0; j < VW / 2; ++j) {
+            const unsigned int lo = 2 * j < valid ? gload<unsigned short>(p, i + 2 * j) : 0u;
+            const unsigned int hi = 2 * j + 1 < valid ? gload<unsigned short>(p, i + 2 * j + 1) : 0u;
+            q.w[j] = lo | hi << 16;
+        }
+    }
+    return q;
+}
+
+template <dp_dtype DT, int VW>
+__device__ __forceinline__ void expand(const Raw<DT, VW>& q, float* o) {
+    if constexpr (DT == DP_F32) {
+#pragma unroll
+        for (int j = 0; j < VW; ++j) o[j] = __builtin_bit_cast(float, q.w[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < VW / 2; ++j) unpack2<DT>(q.w[j], o + 2 * j);
+    }
 }
 
 }  // namespace dpk

@@ -17,7 +17,7 @@
 //    from ballots (which lanes hold my digit), so equal ids keep their order.
 //    Lists of at most 16384 tokens are sorted in LDS by one workgroup a replica
 //    in a single launch.
-//  - The sorted list is cut into chunks of 32 pairs.  One wave sums one chunk
+//  - The sorted list is cut into chunks of 16 pairs.  One wave sums one chunk
 //    over 256 columns (4 a lane), adding rows of dy in list order.  A run that
 //    lies inside its chunk is finished there; one that crosses a boundary
 //    leaves a partial sum in the workspace, and a second launch adds the
@@ -385,7 +385,8 @@ __global__ void __launch_bounds__(64) k_embed_sum(GradArgs a) {
     float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     bool head = __builtin_amdgcn_readlane(k, 0) == before;  // the current run began in an earlier chunk
     for (int b = 0; b < count; b += kBatch) {
-        float v[kBatch][4], old[kBatch][4];
+        Raw<DT, 4> v[kBatch];
+        float old[kBatch][4];
         uint32_t kk[kBatch];
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
@@ -394,14 +395,16 @@ __global__ void __launch_bounds__(64) k_embed_sum(GradArgs a) {
             const int64_t row = __builtin_amdgcn_readlane(p, i);
             // a batch past the chunk's end, or an id outside the table, reads no row
             const bool read = b + j < count && kk[j] < a.rows;
-            load_n<DT, 4>(a.dy[r], row * a.ld + c, read ? valid : 0, a.vec_dy, v[j]);
+            v[j] = load_raw<DT, 4>(a.dy[r], row * a.ld + c, read ? valid : 0, a.vec_dy);
             fetch<kOver>(a, acc, kk[j], c, read && (ends >> i & 1) ? valid : 0, old[j]);
         }
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
             if (b + j >= count) break;
+            float x[4];
+            expand<DT, 4>(v[j], x);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) s[q] += v[j][q];
+            for (int q = 0; q < 4; ++q) s[q] += x[q];
             if (ends >> (b + j) & 1) {
                 if (kk[j] < a.rows) {
                     if (head) store_n<DP_F32, 4>(part, c, valid, vec_part, s);

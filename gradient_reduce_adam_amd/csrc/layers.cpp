@@ -387,7 +387,8 @@ dp_status dpl_accumulate_linear(dp_plan* plan, const dpl_linear* linear, int64_t
     if (dtype != DP_BF16 && dtype != DP_F16) return fail(DP_ERR_INVALID_ARG, "%s: dtype must be DP_BF16 or DP_F16", where);
     if (!rows) return fail(DP_ERR_INVALID_ARG, "%s: null argument", where);
     dpk::LinearGrad g{};
-    g.vec = linear->inputs % 16 == 0 && linear->outputs % 8 == 0;
+    g.vec = linear->inputs % 16 == 0 && linear->outputs % 8 == 0 && ld_dy < (int64_t{1} << 24) &&
+            ld_codes < (int64_t{1} << 24) && ld_scales < (int64_t{1} << 24);
     for (int32_t r = 0; r < plan->n; ++r) {
         s = check_rows(where, "codes", rows[r].codes, tokens, linear->inputs, ld_codes, 1);
         if (s == DP_OK)

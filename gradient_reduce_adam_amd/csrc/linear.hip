@@ -116,25 +116,37 @@ struct Stage {
     unsigned int unit[2];
 };
 
-// Every token of [t, t + 64) exists.  Columns past the last are read from the
-// last whole piece: their products are not stored.
-__device__ __forceinline__ void load_full(const LinearArgs& a, const Job& j, int64_t t, Stage& s) {
-    int64_t c = j.o0 + ((threadIdx.x & 31) << 3);
-    c = c < a.outputs ? c : a.outputs - 8;
-    const unsigned char* p = j.dy + 2 * ((t + (threadIdx.x >> 5)) * a.ld_dy + c);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) s.dy[q] = gload<u32x4>(p + q * 32 * a.ld_dy, 0);
-    c = j.i0 + ((threadIdx.x & 15) << 4);
-    c = c < a.inputs ? c : a.inputs - 16;
+// Where a thread reads its pieces of a whole tile: offsets from the tile's first
+// token.  Columns past the last are read from the last whole piece: their
+// products are not stored.
+struct Pieces {
+    uint32_t dy, codes, scales;
+};
+
+__device__ __forceinline__ Pieces pieces(const LinearArgs& a, const Job& j, int64_t ld_dy, int64_t ld_codes, int64_t ld_scales) {
+    int64_t o = j.o0 + ((threadIdx.x & 31) << 3), i = j.i0 + ((threadIdx.x & 15) << 4);
+    o = o < a.outputs ? o : a.outputs - 8;
+    i = i < a.inputs ? i : a.inputs - 16;
+    return {static_cast<uint32_t>(2 * ((threadIdx.x >> 5) * ld_dy + o)),
+            static_cast<uint32_t>((threadIdx.x >> 4) * ld_codes + i),
+            static_cast<uint32_t>((threadIdx.x >> 4) * ld_scales + i / DPL_GROUP)};
+}
+
+// The tile whose first token is row 0 of the three addresses.
+__device__ __forceinline__ void load_full(const unsigned char* dy, const unsigned char* codes, const unsigned char* scales,
+                                          int64_t ld_dy, int64_t ld_codes, int64_t ld_scales, const Pieces& p, Stage& s) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const int64_t k = t + (threadIdx.x >> 4) + 32 * h;
-        s.codes[h] = gload<u32x4>(j.codes + k * a.ld_codes + c, 0);
-        s.unit[h] = gload<unsigned char>(j.scales, k * a.ld_scales + c / DPL_GROUP);
+        s.dy[2 * h] = gload<u32x4>(dy + 2 * h * 32 * ld_dy + p.dy, 0);
+        s.dy[2 * h + 1] = gload<u32x4>(dy + (2 * h + 1) * 32 * ld_dy + p.dy, 0);
+        s.codes[h] = gload<u32x4>(codes + h * 32 * ld_codes + p.codes, 0);
+        s.unit[h] = gload<unsigned char>(scales + h * 32 * ld_scales + p.scales, 0);
     }
 }
 
-// Tokens [t, end), any alignment, zeros for tokens and columns that do not exist.
+// Tokens [t, end) of a tile, with zeros for tokens and columns that do not exist;
+// in whole pieces with kVec, else element by element.
+template <bool kVec>
 __device__ __forceinline__ void load_checked(const LinearArgs& a, const Job& j, int64_t t, int64_t end, Stage& s) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -142,10 +154,14 @@ __device__ __forceinline__ void load_checked(const LinearArgs& a, const Job& j, 
         const int64_t left = a.outputs - (j.o0 + c);
         const int valid = t + k < end ? left >= 8 ? 8 : left > 0 ? static_cast<int>(left) : 0 : 0;
         const unsigned short* p = reinterpret_cast<const unsigned short*>(j.dy) + (t + k) * a.ld_dy + j.o0 + c;
-        unsigned int e[8];
+        if constexpr (kVec) {
+            s.dy[q] = valid ? gload<u32x4>(p, 0) : u32x4{0, 0, 0, 0};
+        } else {
+            unsigned int e[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) e[i] = i < valid ? gload<unsigned short>(p, i) : 0;
-        s.dy[q] = u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
+            for (int i = 0; i < 8; ++i) e[i] = i < valid ? gload<unsigned short>(p, i) : 0;
+            s.dy[q] = u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
+        }
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -153,11 +169,16 @@ __device__ __forceinline__ void load_checked(const LinearArgs& a, const Job& j, 
         const int64_t left = a.inputs - (j.i0 + c);
         const int valid = t + k < end ? left >= 16 ? 16 : left > 0 ? static_cast<int>(left) : 0 : 0;
         const unsigned char* p = j.codes + (t + k) * a.ld_codes + j.i0 + c;
-        unsigned int e[16];
+        if constexpr (kVec) {
+            s.codes[h] = valid ? gload<u32x4>(p, 0) : u32x4{0, 0, 0, 0};
+        } else {
+            unsigned int e[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) e[i] = i < valid ? gload<unsigned char>(p, i) : 0;
+            for (int i = 0; i < 16; ++i) e[i] = i < valid ? gload<unsigned char>(p, i) : 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s.codes[h][i] = e[4 * i] | e[4 * i + 1] << 8 | e[4 * i + 2] << 16 | e[4 * i + 3] << 24;
+            for (int i = 0; i < 4; ++i)
+                s.codes[h][i] = e[4 * i] | e[4 * i + 1] << 8 | e[4 * i + 2] << 16 | e[4 * i + 3] << 24;
+        }
         s.unit[h] = valid ? gload<unsigned char>(j.scales, (t + k) * a.ld_scales + (j.i0 + c) / DPL_GROUP) : 127;
     }
 }
@@ -174,6 +195,24 @@ __device__ __forceinline__ void store_half(const Stage& s, int h, lds_u8* dy, ld
         *(lds_u32x4*)(x + h * 32 * (2 * kTileCols) + 16 * e) =
             u32x4{decode2<DT>(s.codes[h][2 * e], unit, 0), decode2<DT>(s.codes[h][2 * e], unit, 1),
                   decode2<DT>(s.codes[h][2 * e + 1], unit, 0), decode2<DT>(s.codes[h][2 * e + 1], unit, 1)};
+}
+
+// The order of a group of eight products and what goes on beside them: the
+// twelve fragment loads for the next group behind the first products, then with
+// kKind >= 1 four LDS writes, and with kKind 2 the eight global loads.  Left
+// alone, the compiler gathers the loads right before their results are needed
+// and the matrix cores wait.
+template <int kKind>
+__device__ __forceinline__ void spread() {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        if (kKind == 0 && i < 6) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+        if (kKind >= 1 && i < 4) __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);
+        if (kKind >= 1 && i >= 4) __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
+        if (kKind == 2 && i >= 4) __builtin_amdgcn_sched_group_barrier(0x020, 2, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
 }
 
 // Rows of the result are outputs (columns inputs), or inputs with kSwap; the
@@ -243,14 +282,21 @@ __global__ void __launch_bounds__(kThreads) k_linear(LinearArgs a) {
     if (full >= 0) {
         Stage s;
         int64_t t = t1 - full * kTileTokens;  // the next tile to load
-        const int64_t last = t1 - kTileTokens;
-        load_checked(a, j, t0, t, s);
+        load_checked<kVec>(a, j, t0, t, s);
         store_half<DT>(s, 0, base + put_dy, base + put_x);
         store_half<DT>(s, 1, base + put_dy, base + put_x);
-        auto load = [&]() {  // past the end the last tile again, which is not used
-            if (full == 0) return;
-            if constexpr (kVec) load_full(a, j, t < last ? t : last, s);
-            else load_checked(a, j, t < last ? t : last, t1, s);
+        // Past the end the last tile is loaded again, and not used; without a
+        // whole tile that is the first token, at a stride of 0.
+        const int64_t last = full > 0 ? t1 - kTileTokens : t0;
+        const int64_t ld_dy = full > 0 ? a.ld_dy : 0, ld_codes = full > 0 ? a.ld_codes : 0;
+        const int64_t ld_scales = full > 0 ? a.ld_scales : 0;
+        const Pieces at_row = pieces(a, j, ld_dy, ld_codes, ld_scales);
+        auto load = [&]() {
+            const int64_t from = t < last ? t : last;
+            if constexpr (kVec)
+                load_full(j.dy + 2 * from * a.ld_dy, j.codes + from * a.ld_codes, j.scales + from * a.ld_scales, ld_dy,
+                          ld_codes, ld_scales, at_row, s);
+            else load_checked<false>(a, j, from, t1, s);
             t += kTileTokens;
         };
         load();
@@ -260,18 +306,23 @@ __global__ void __launch_bounds__(kThreads) k_linear(LinearArgs a) {
         for (int64_t i = 0; i <= full; ++i) {
             const int other = turn ^ (2 * kTileBytes);
             read(turn, 1, 1);
-            store_half<DT>(s, 0, base + other + put_dy, base + other + put_x);
             multiply(0);
+            spread<0>();
             read(turn, 2, 0);
-            store_half<DT>(s, 1, base + other + put_dy, base + other + put_x);
+            store_half<DT>(s, 0, base + other + put_dy, base + other + put_x);
             multiply(1);
+            spread<1>();
             read(turn, 3, 1);
+            store_half<DT>(s, 1, base + other + put_dy, base + other + put_x);
             load();
             multiply(0);
+            spread<2>();
             __syncthreads();
+            __builtin_amdgcn_sched_barrier(0);
             turn = other;
             read(turn, 0, 0);
             multiply(1);
+            spread<0>();
         }
     }
 
@@ -280,26 +331,32 @@ __global__ void __launch_bounds__(kThreads) k_linear(LinearArgs a) {
     const int64_t height = kSwap ? a.inputs : a.outputs, width = kSwap ? a.outputs : a.inputs;
     const bool over = a.overwrite || a.splits > 1;
     float* out = a.splits > 1 ? a.part + (static_cast<int64_t>(split) * a.n + r) * height * width : a.acc[r];
+    // products 2 m + n, each as 16 rows of 32 columns twice; the accumulators of the
+    // next two are on their way while one is stored
+    auto row_of = [&](int k, int e) { return row0 + 32 * (k >> 1) + 8 * (e >> 2) + (e & 3); };
+    auto there = [&](int k, int e) { return row_of(k, e) < height && col0 + 32 * (k & 1) < width; };
+    float old[3][16];
+    auto fetch = [&](int k) {
+        const float* p = out + row_of(k, 0) * width + col0 + 32 * (k & 1);
 #pragma unroll
-    for (int m = 0; m < 4; ++m)
+        for (int e = 0; e < 16; ++e)
+            if (there(k, e)) old[k % 3][e] = gload<float>(p + (8 * (e >> 2) + (e & 3)) * width, 0);
+    };
+    if (!over) {
+        fetch(0);
+        fetch(1);
+    }
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            __builtin_amdgcn_sched_barrier(0);
-            const int64_t col = col0 + 32 * n, row = row0 + 32 * m;
-            float* p = out + row * width + col;
-            if (col >= width) continue;
-            float old[16];
+    for (int k = 0; k < 8; ++k) {
+        __builtin_amdgcn_sched_barrier(0);
+        if (!over && k + 2 < 8) fetch(k + 2);
+        float* p = out + row_of(k, 0) * width + col0 + 32 * (k & 1);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const int d = 8 * (e >> 2) + (e & 3);
-                old[e] = !over && row + d < height ? gload<float>(p + d * width, 0) : 0.0f;
-            }
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const int d = 8 * (e >> 2) + (e & 3);
-                if (row + d < height) gstore<float>(p + d * width, 0, over ? c[m][n][e] : old[e] + c[m][n][e]);
-            }
-        }
+        for (int e = 0; e < 16; ++e)
+            if (there(k, e))
+                gstore<float>(p + (8 * (e >> 2) + (e & 3)) * width, 0,
+                              over ? c[k >> 1][k & 1][e] : old[k % 3][e] + c[k >> 1][k & 1][e]);
+    }
 }
 
 // Adds the splits' tiles of every replica, in order, into the accumulators.
