@@ -30,7 +30,8 @@ struct EmbedGrad {
     bool vec_base;         // every accumulator's first row is aligned to 16 bytes
 };
 size_t embed_workspace(int64_t dim, int64_t tokens, int n);
-int64_t embed_waves(const EmbedGrad& a);  // workgroups of its largest launch, for one replica
+int64_t embed_waves(const EmbedGrad& a);   // one-wave workgroups of the sums, for one replica
+int64_t embed_groups(const EmbedGrad& a);  // workgroups of the first launch: the sort's and the zeros'
 hipError_t launch_embed_grad(dp_dtype dt, const EmbedGrad& a, void* workspace, hipStream_t stream);
 
 // ---- norms around a block (block_norm.hip) -----------------------------------

@@ -508,6 +508,10 @@ int64_t embed_waves(const EmbedGrad& a) {
     return chunks_of(a.tokens) * slices_of(a.dim);
 }
 
+int64_t embed_groups(const EmbedGrad& a) {
+    return a.n * (kMaxSpans + (a.overwrite ? (a.rows * a.dim + kZeroSpan - 1) / kZeroSpan : 0));
+}
+
 hipError_t launch_embed_grad(dp_dtype dt, const EmbedGrad& a, void* workspace, hipStream_t stream) {
     Ids ids{};
     GradArgs g{};

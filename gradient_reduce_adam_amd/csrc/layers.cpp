@@ -15,7 +15,9 @@ using dpapi::hip_fail;
 
 namespace {
 
-constexpr int64_t kMaxWaves = (int64_t{1} << 26) - 1;  // one-wave workgroups of one dispatch
+// one dispatch has fewer than 2^32 threads: workgroups of one wave, and of 1024 threads
+constexpr int64_t kMaxWaves = (int64_t{1} << 26) - 1;
+constexpr int64_t kMaxGroups = (int64_t{1} << 22) - 1;
 
 int64_t esize(dp_dtype d) { return d == DP_F32 ? 4 : 2; }
 bool dtype_ok(dp_dtype d) { return d == DP_F32 || d == DP_F16 || d == DP_BF16; }
@@ -161,7 +163,7 @@ dp_status check_packed(const char* where, int64_t tokens, int64_t dim, dp_dtype 
     s = check_rows(where, "codes", codes, tokens, dim, ld_codes, 1);
     if (s == DP_OK) s = check_rows(where, "scales", scales, tokens, (dim + DPL_GROUP - 1) / DPL_GROUP, ld_scales, 1);
     if (s != DP_OK) return s;
-    if ((dim + DPL_GROUP - 1) / DPL_GROUP * tokens > (int64_t{1} << 31))
+    if ((dim + DPL_GROUP - 1) / DPL_GROUP * tokens > (int64_t{1} << 30))
         return fail(DP_ERR_INVALID_ARG, "%s: %lld rows of %lld elements are too many for one call", where, ll(tokens), ll(dim));
     return DP_OK;
 }
@@ -176,7 +178,7 @@ dp_status check_linear(const char* where, const dp_plan* plan, const dpl_linear*
     if (d->inputs < 1 || d->outputs < 1 || d->inputs > most || d->outputs > most || d->inputs * d->outputs != numel)
         return fail(DP_ERR_INVALID_ARG, "%s: tensor %d of %lld elements is no %lld x %lld matrix", where, d->tensor,
                     ll(numel), ll(d->outputs), ll(d->inputs));
-    if (dpk::linear_jobs(d->outputs, d->inputs, tokens, plan->n) > (int64_t{1} << 22))
+    if (dpk::linear_jobs(d->outputs, d->inputs, tokens, plan->n) > kMaxGroups)
         return fail(DP_ERR_INVALID_ARG, "%s: a %lld x %lld matrix is too large for one call", where, ll(d->outputs),
                     ll(d->inputs));
     return DP_OK;
@@ -249,8 +251,9 @@ dp_status dpl_accumulate_embed(dp_plan* plan, const dpl_table* table, int64_t to
     a.scale = static_cast<float>(table->scale);
     a.id_bytes = table->id_bytes;
     a.overwrite = overwrite;
-    if (dpk::embed_waves(a) > kMaxWaves)
-        return fail(DP_ERR_INVALID_ARG, "%s: %lld tokens of %lld elements are too many for one call", where, ll(tokens), ll(a.dim));
+    if (dpk::embed_waves(a) > kMaxWaves || dpk::embed_groups(a) > kMaxGroups)
+        return fail(DP_ERR_INVALID_ARG, "%s: %lld tokens of %lld elements and %lld rows are too many for one call", where,
+                    ll(tokens), ll(a.dim), ll(a.rows));
     s = launched(dpk::launch_embed_grad(dtype, a, workspace, stream), "embedding gradient launch");
     if (s != DP_OK) return s;
     dpapi::part_end(plan, &table->tensor, 1, first != 0, more != 0);
@@ -332,11 +335,11 @@ dp_status dpl_accumulate_block_norm(dp_plan* plan, const dpl_norms* norms, int64
             return fail(DP_ERR_INVALID_ARG, "%s: outputs overlap each other, s or y", where);
     }
     s = check_workspace(where, workspace, workspace_bytes, dpk::block_norm_workspace(n.b.dim, tokens, plan->n, n.b.centered));
-    if (s == DP_OK) s = norm_weights(where, plan, &n);
     if (s != DP_OK) return s;
     float* acc[5 * DP_MAX_REPLICAS];
     bool overwrite[5];
     s = dpapi::part_begin(plan, n.tensors, n.count, first != 0, where, acc, overwrite);
+    if (s == DP_OK) s = norm_weights(where, plan, &n);
     if (s == DP_OK) s = check_acc(where, acc, n.count * plan->n);
     if (s != DP_OK) return s;
     s = launched(dpk::launch_block_grad(dtype, plan->pdt, n.b, tokens, plan->n, rows, ld, vec, acc, n.at, overwrite,

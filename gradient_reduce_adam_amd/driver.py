@@ -21,7 +21,12 @@ once.  ``step_overlapped`` issues the same step bucket by bucket
 (``dp_accumulate_reduce_range``, or ``dp_reduce_adam_range`` and
 ``dp_reduce_adam_finish`` for the single pass, and with ``micro_buckets`` also
 ``dp_accumulate_all_range`` for the earlier micro-steps), on a second stream
-as the producer writes each bucket; again the same bits.
+as the producer writes each bucket; again the same bits.  ``step_layers`` takes
+a backward pass that writes its gradients into the accumulators itself, with
+the layer operators (``accumulate_embed``, ``accumulate_block_norm``,
+``accumulate_linear`` of :class:`Plan`) and ``accumulate_all_range`` for the
+tensors whose gradients are dense buffers; the replicas are then averaged from
+the accumulators.
 
 HBM layout (flat parameter space of P elements, tensors in list order; see
 ``layout`` for where the arrays sit relative to each other):
@@ -48,6 +53,10 @@ GradProducer = Callable[[int, int, int, float], int]
 # producer(step, micro, lo, hi, stream): writes every replica's gradient of
 # elements [lo, hi) for that micro-step into its flat gradient buffer, on stream
 RangeProducer = Callable[[int, int, int, int, int], None]
+
+# backward(step, micro, first, loss_scale): runs every replica's backward pass of
+# that micro-step and accumulates every tensor's gradient
+LayerBackward = Callable[[int, int, bool, float], None]
 
 
 def backward_buckets(numel: Sequence[int], bucket_bytes: int, elem_bytes: int = 2,
@@ -275,13 +284,14 @@ class DPStep:
         if self.n > 1:
             pl.reduce_replicas("acc", stream=st)
 
-    def finish(self) -> None:
-        """Statistics, scalars and the update on every shard range."""
+    def finish(self, scan: bool = False) -> None:
+        """Statistics, scalars and the update on every shard range.  scan: g_bar
+        has no statistics yet."""
         pl, st = self.plan, self.stream.cuda_stream
         if self.single_pass:
             pl.reduce_adam_step(self.lr, self.eps, self.weight_decay, stream=st)
             return
-        pl.grad_stats(scan=False, max_norm=self.max_norm, stream=st)
+        pl.grad_stats(scan=scan, max_norm=self.max_norm, stream=st)
         if self.offload == "staged":
             self.staged_update()
             return
@@ -338,6 +348,43 @@ class DPStep:
             self.scale = s["scale"]
             return s
         return None
+
+    def issue_layers(self, backward: LayerBackward, step: int) -> None:
+        """One whole step whose micro-steps' gradients are written into the
+        accumulators by ``backward(step, k, first, scale)``: for every replica
+        it runs the backward pass of micro-step k on this step's stream, under
+        the loss scale, and issues the ``accumulate_*`` calls (with that first
+        flag) that together cover every tensor.  No host synchronisation: the
+        form a graph can capture, once one step has run."""
+        if self.partials or self.single_pass:
+            raise ValueError("layer operators write accumulators: no incoming partials, and the two-pass update")
+        for k in range(1, self.a + 1):
+            backward(step, k, k == 1, self.scale)
+        if self.n > 1:
+            self.plan.reduce_replicas("acc", stream=self.stream.cuda_stream)
+        self.finish(scan=self.n == 1)  # with one replica g_bar is its accumulator
+
+    def step_layers(self, backward: LayerBackward, sync_scale: bool = True) -> Optional[dict]:
+        """``issue_layers`` as one step."""
+        self.steps_done += 1
+        self.issue_layers(backward, self.steps_done)
+        if sync_scale:
+            s = self.read_state()
+            self.scale = s["scale"]
+            return s
+        return None
+
+    def capture_layers(self, backward: LayerBackward) -> "StepGraph":
+        """Captures ``issue_layers`` (with the loss scale of now) into a HIP
+        graph on this step's stream, which must not be the null stream.  The
+        buffers that backward works on have to stay where they are while the
+        graph may replay, as do the workspaces of its calls."""
+        if self.stream.cuda_stream == 0:
+            raise ValueError("capture needs a non-default stream: pass stream=torch.cuda.Stream()")
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=self.stream):
+            self.issue_layers(backward, self.steps_done + 1)
+        return StepGraph(g, self.stream)
 
     def step_overlapped(self, grad_slots: Sequence[int], produce: RangeProducer, buckets: Sequence[Tuple[int, int]],
                         reduce_stream: Optional[torch.cuda.Stream] = None, sync_scale: bool = True,

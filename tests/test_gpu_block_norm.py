@@ -47,6 +47,7 @@ class Setup:
         self.plan = dp.Plan(self.numel, n, pdt, pdt)
         P = sum(self.numel)
         self.flat = (torch.randn(P, generator=g) * 0.3 + 1.0).to(DT[pdt]).cuda()
+        self.none = torch.zeros(P, dtype=DT[pdt], device="cuda")
         self.acc = [torch.full((P,), 2.5 + r, device="cuda") for r in range(n)]
         starts = [0] + [off + D * i for i in range(len(names) + 1)]
         self.plan.bind("param", self.flat)
@@ -55,7 +56,7 @@ class Setup:
                 self.plan.bind_tensors("acc", [a[i:] for i in starts], r)
             else:
                 self.plan.bind("acc", a, r)
-            self.plan.bind("grad", torch.zeros(P, dtype=DT[pdt], device="cuda"), r)
+            self.plan.bind("grad", self.none, r)
         self.norms = BlockNorm(centered=centered, eps=EPS, residual_scale=alpha,
                                **{k: i + 1 for i, k in enumerate(names)})
         self.w = {k: self.flat[off + D * i:off + D * (i + 1)].double() for i, k in enumerate(names)}
@@ -316,3 +317,26 @@ def test_captured_and_replayed():
         s.rest(True)
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, (dh[0], dy[0], h, x, s.acc[0][s.off:-5])))
+
+
+@pytest.mark.parametrize("T,D", [(5000, 512), (4500, 768), (2500, 2048), (1500, 4096), (1300, 4104)])
+def test_a_row_does_not_depend_on_the_others(T, D):
+    """Workgroups that walk over many rows give each the bits it has in a call of a few rows."""
+    g = torch.Generator().manual_seed(8)
+    for centered in (False, True):
+        s = Setup(D, 1, kinds(centered, True, True, True), "bf16", "bf16", g, centered, 0.5)
+        S, Y, dx, ds = many_rows(T, D, "bf16", g, 1)
+        ws = s.scratch(T)
+        dh, dy, out, x = (torch.zeros_like(S[0]) for _ in range(4))
+        s.plan.block_norm(s.norms, S[0], Y[0], out, x)
+        s.plan.accumulate_block_norm(s.norms, S, Y, dx, ds, [dh], [dy], first=True, workspace=ws)
+        s.rest(True)
+        for lo in (0, 300, T - 7):
+            part = slice(lo, lo + 7)
+            dh2, dy2, out2, x2 = (torch.zeros_like(S[0][part]) for _ in range(4))
+            s.plan.block_norm(s.norms, S[0][part], Y[0][part], out2, x2)
+            s.plan.accumulate_block_norm(s.norms, *([t[0][part]] for t in (S, Y, dx, ds)), [dh2], [dy2], first=True,
+                                         workspace=ws)
+            s.rest(True)
+            for a, b in ((dh, dh2), (dy, dy2), (out, out2), (x, x2)):
+                assert torch.equal(a[part], b)

@@ -30,7 +30,8 @@ def ids_of(kind, T, V, g, dtype=torch.int64):
     elif kind == "reverse":
         x = torch.arange(T - 1, -1, -1) % V
     elif kind == "wild":  # ids far outside the table, and its first and last row
-        x = torch.tensor([0, V - 1, V, -1, -2 ** 31, 2 ** 31 - 1])[torch.randint(0, 6, (T,), generator=g)]
+        far = [2 ** 32, -2 ** 40, 2 ** 62] if dtype == torch.int64 else [-2 ** 30, 2 ** 30, 2 ** 31 - 2]
+        x = torch.tensor([0, V - 1, V, -1, -2 ** 31, 2 ** 31 - 1] + far)[torch.randint(0, 9, (T,), generator=g)]
     else:  # frequencies that fall with the id, and padding
         u = torch.rand(T, generator=g, dtype=torch.float64)
         x = ((V + 1.0) ** u - 1.0).floor().long().clamp(0, V - 1)
@@ -72,13 +73,14 @@ class Setup:
         self.numel = (off, V * D, 7)
         self.plan = dp.Plan(self.numel, n, dtype, dtype)
         P = sum(self.numel)
+        self.none = torch.zeros(P, dtype=DT[dtype], device="cuda")
         self.acc = [torch.full((P,), 3.25 + r, device="cuda") for r in range(n)]
         for r, a in enumerate(self.acc):
             if tensors:
                 self.plan.bind_tensors("acc", [a[0:], a[off:], a[off + V * D:]], r)
             else:
                 self.plan.bind("acc", a, r)
-            self.plan.bind("grad", torch.zeros(P, dtype=DT[dtype], device="cuda"), r)
+            self.plan.bind("grad", self.none, r)
 
     def table(self, r):
         return self.acc[r][self.off:self.off + self.V * self.D].view(self.V, self.D)

@@ -61,13 +61,14 @@ class Setup:
         self.numel = (off, I * O, 9)
         self.plan = dp.Plan(self.numel, n, dtype, dtype)
         P = sum(self.numel)
+        self.none = torch.zeros(P, dtype=DT[dtype], device="cuda")
         self.acc = [torch.full((P,), 1.5 + r, device="cuda") for r in range(n)]
         for r, a in enumerate(self.acc):
             if tensors:
                 self.plan.bind_tensors("acc", [a, a[off:], a[off + I * O:]], r)
             else:
                 self.plan.bind("acc", a, r)
-            self.plan.bind("grad", torch.zeros(P, dtype=DT[dtype], device="cuda"), r)
+            self.plan.bind("grad", self.none, r)
 
     def matrix(self, r, transposed):
         shape = (self.I, self.O) if transposed else (self.O, self.I)
