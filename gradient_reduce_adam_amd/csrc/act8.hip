@@ -30,7 +30,6 @@ struct PackArgs {
     unsigned char* codes;
     unsigned char* scales;
     int64_t tokens, dim, ld, ld_codes, ld_scales;
-    bool vec;
 };
 
 // The row and first column of this thread's span.  Spans are numbered along
@@ -54,8 +53,8 @@ __global__ void __launch_bounds__(kThreads) k_pack(PackArgs a) {
     const int64_t left = in ? a.dim - c : 0;
     const int valid = left >= kSpan ? kSpan : left > 0 ? static_cast<int>(left) : 0;
     float v[kSpan];
-    load_n<DT, 8>(a.in, row * a.ld + c, valid, a.vec, v);
-    load_n<DT, 8>(a.in, row * a.ld + c + 8, valid - 8, a.vec, v + 8);
+    load_n<DT, 8>(a.in, row * a.ld + c, valid, v);
+    load_n<DT, 8>(a.in, row * a.ld + c + 8, valid - 8, v + 8);
     float top = 0.0f;
 #pragma unroll
     for (int j = 0; j < kSpan; ++j) {
@@ -87,8 +86,8 @@ __global__ void __launch_bounds__(kThreads) k_pack(PackArgs a) {
     }
     if (!in) return;
     unsigned char* out = a.codes + row * a.ld_codes + c;
-    if (a.vec && valid == kSpan) {
-        gstore<u32x4>(out, 0, q);
+    if (valid == kSpan) {
+        gstore<u32x4, 1>(out, 0, q);
     } else {
 #pragma unroll
         for (int j = 0; j < kSpan; ++j)
@@ -107,8 +106,8 @@ __global__ void __launch_bounds__(kThreads) k_unpack(PackArgs a) {
     if (valid == 0) return;
     const unsigned char* in = a.codes_in + row * a.ld_codes + c;
     u32x4 q{0, 0, 0, 0};
-    if (a.vec && valid == kSpan) {
-        q = gload<u32x4>(in, 0);
+    if (valid == kSpan) {
+        q = gload<u32x4, 1>(in, 0);
     } else {
 #pragma unroll
         for (int j = 0; j < kSpan; ++j)
@@ -126,8 +125,8 @@ __global__ void __launch_bounds__(kThreads) k_unpack(PackArgs a) {
         v[4 * k + 2] = hi[0] * unit;
         v[4 * k + 3] = hi[1] * unit;
     }
-    store_n<DT, 8>(a.out, row * a.ld + c, valid, a.vec, v);
-    store_n<DT, 8>(a.out, row * a.ld + c + 8, valid - 8, a.vec, v + 8);
+    store_n<DT, 8>(a.out, row * a.ld + c, valid, v);
+    store_n<DT, 8>(a.out, row * a.ld + c + 8, valid - 8, v + 8);
 }
 
 dim3 grid_of(int64_t tokens, int64_t dim) {
@@ -138,7 +137,7 @@ dim3 grid_of(int64_t tokens, int64_t dim) {
 }  // namespace
 
 hipError_t launch_pack(dp_dtype dt, int64_t tokens, int64_t dim, const void* x, int64_t ld, void* codes,
-                       int64_t ld_codes, void* scales, int64_t ld_scales, bool vec, hipStream_t stream) {
+                       int64_t ld_codes, void* scales, int64_t ld_scales, hipStream_t stream) {
     if (tokens == 0) return hipSuccess;
     PackArgs a{};
     a.in = x;
@@ -149,7 +148,6 @@ hipError_t launch_pack(dp_dtype dt, int64_t tokens, int64_t dim, const void* x, 
     a.ld = ld;
     a.ld_codes = ld_codes;
     a.ld_scales = ld_scales;
-    a.vec = vec;
     const dim3 grid = grid_of(tokens, dim);
     if (dt == DP_F32) hipLaunchKernelGGL((k_pack<DP_F32>), grid, dim3(kThreads), 0, stream, a);
     if (dt == DP_F16) hipLaunchKernelGGL((k_pack<DP_F16>), grid, dim3(kThreads), 0, stream, a);
@@ -158,7 +156,7 @@ hipError_t launch_pack(dp_dtype dt, int64_t tokens, int64_t dim, const void* x, 
 }
 
 hipError_t launch_unpack(dp_dtype dt, int64_t tokens, int64_t dim, const void* codes, int64_t ld_codes,
-                         const void* scales, int64_t ld_scales, void* x, int64_t ld, bool vec, hipStream_t stream) {
+                         const void* scales, int64_t ld_scales, void* x, int64_t ld, hipStream_t stream) {
     if (tokens == 0) return hipSuccess;
     PackArgs a{};
     a.codes_in = static_cast<const unsigned char*>(codes);
@@ -169,7 +167,6 @@ hipError_t launch_unpack(dp_dtype dt, int64_t tokens, int64_t dim, const void* c
     a.ld = ld;
     a.ld_codes = ld_codes;
     a.ld_scales = ld_scales;
-    a.vec = vec;
     const dim3 grid = grid_of(tokens, dim);
     if (dt == DP_F32) hipLaunchKernelGGL((k_unpack<DP_F32>), grid, dim3(kThreads), 0, stream, a);
     if (dt == DP_F16) hipLaunchKernelGGL((k_unpack<DP_F16>), grid, dim3(kThreads), 0, stream, a);

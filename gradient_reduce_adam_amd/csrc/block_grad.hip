@@ -33,7 +33,6 @@ struct GradArgs {
     int64_t tokens, ld;
     int32_t dim;
     float eps, alpha;
-    bool vec;
     Weights w;
 };
 
@@ -54,9 +53,9 @@ __global__ void __launch_bounds__(block_of(NT)) k_block_grad(GradArgs a) {
     const bool has_gate = a.w.gate != nullptr, has_x = p.dx != nullptr, has_ds = p.ds != nullptr;
     const bool has_y = kPost || has_gate;
     Column<PT, NV, VW> post_w, gate, pre_w;
-    if constexpr (kPost) post_w.load(a.w.post_w, c0, kStep, a.dim, a.w.vec);
-    if (has_gate) gate.load(a.w.gate, c0, kStep, a.dim, a.w.vec);
-    if (has_x) pre_w.load(a.w.pre_w, c0, kStep, a.dim, a.w.vec);
+    if constexpr (kPost) post_w.load(a.w.post_w, c0, kStep, a.dim);
+    if (has_gate) gate.load(a.w.gate, c0, kStep, a.dim);
+    if (has_x) pre_w.load(a.w.pre_w, c0, kStep, a.dim);
     float sum[Q][NV][VW];
 #pragma unroll
     for (int q = 0; q < Q; ++q)
@@ -75,10 +74,10 @@ __global__ void __launch_bounds__(block_of(NT)) k_block_grad(GradArgs a) {
             const int c = c0 + k * kStep;
             const int valid = t < a.tokens ? valid_of<VW>(a.dim, c) : 0;
             const int64_t at = t * a.ld + c;
-            ns[k] = load_raw<DT, VW>(p.s, at, has_x ? valid : 0, a.vec && has_x);
-            nx[k] = load_raw<DT, VW>(p.dx, at, has_x ? valid : 0, a.vec && has_x);
-            ny[k] = load_raw<DT, VW>(p.y, at, has_y ? valid : 0, a.vec && has_y);
-            nd[k] = load_raw<DT, VW>(p.ds, at, has_ds ? valid : 0, a.vec && has_ds);
+            ns[k] = load_raw<DT, VW>(p.s, at, has_x ? valid : 0, a.dim >= VW);
+            nx[k] = load_raw<DT, VW>(p.dx, at, has_x ? valid : 0, a.dim >= VW);
+            ny[k] = load_raw<DT, VW>(p.y, at, has_y ? valid : 0, a.dim >= VW);
+            nd[k] = load_raw<DT, VW>(p.ds, at, has_ds ? valid : 0, a.dim >= VW);
         }
     };
     fetch(row);
@@ -86,6 +85,11 @@ __global__ void __launch_bounds__(block_of(NT)) k_block_grad(GradArgs a) {
         float s[NV][VW], y[NV][VW], e[NV][VW], t[NV][VW];
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
+            const int valid = row < a.tokens ? valid_of<VW>(a.dim, c0 + k * kStep) : 0;
+            settle<DT, VW>(ns[k], valid, a.dim >= VW);
+            settle<DT, VW>(nx[k], valid, a.dim >= VW);
+            settle<DT, VW>(ny[k], valid, a.dim >= VW);
+            settle<DT, VW>(nd[k], valid, a.dim >= VW);
             expand<DT, VW>(ns[k], s[k]);
             expand<DT, VW>(nx[k], e[k]);
             expand<DT, VW>(ny[k], y[k]);
@@ -155,7 +159,7 @@ __global__ void __launch_bounds__(block_of(NT)) k_block_grad(GradArgs a) {
             const int c = c0 + k * kStep, valid = row < a.tokens ? valid_of<VW>(a.dim, c) : 0;
 #pragma unroll
             for (int j = 0; j < VW; ++j) f[j] = a.alpha * t[k][j];
-            if (p.dh) store_n<DT, VW>(p.dh, row * a.ld + c, valid, a.vec, f);
+            if (p.dh) store_n<DT, VW>(p.dh, row * a.ld + c, valid, f);
             if constexpr (kCentered) {
 #pragma unroll
                 for (int j = 0; j < VW; ++j) sum[3][k][j] += j < valid ? t[k][j] : 0.0f;
@@ -191,7 +195,7 @@ __global__ void __launch_bounds__(block_of(NT)) k_block_grad(GradArgs a) {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int c = c0 + k * kStep, valid = row < a.tokens ? valid_of<VW>(a.dim, c) : 0;
-            store_n<DT, VW>(p.dy, row * a.ld + c, valid, a.vec, t[k]);
+            store_n<DT, VW>(p.dy, row * a.ld + c, valid, t[k]);
         }
     }
     // the rows' sums of this workgroup, in row order, then one slot of the workspace
@@ -217,8 +221,7 @@ __global__ void __launch_bounds__(block_of(NT)) k_block_grad(GradArgs a) {
         if (threadIdx.x < NT)
 #pragma unroll
             for (int k = 0; k < NV; ++k)
-                store_n<DP_F32, VW>(out + q * a.dim, c0 + k * kStep, valid_of<VW>(a.dim, c0 + k * kStep), a.dim % 4 == 0,
-                                   sum[q][k]);
+                store_n<DP_F32, VW>(out + q * a.dim, c0 + k * kStep, valid_of<VW>(a.dim, c0 + k * kStep), sum[q][k]);
     }
 }
 
@@ -319,7 +322,7 @@ size_t block_norm_workspace(int64_t dim, int64_t tokens, int n, bool centered) {
 }
 
 hipError_t launch_block_grad(dp_dtype dt, dp_dtype pdt, const BlockNorm& b, int64_t tokens, int n,
-                             const dpl_norm_rows* rows, int64_t ld, bool vec, float* const* acc, const int* at,
+                             const dpl_norm_rows* rows, int64_t ld, float* const* acc, const int* at,
                              const bool* overwrite, void* workspace, hipStream_t stream) {
     GradArgs a{};
     for (int r = 0; r < n; ++r) a.rows[r] = rows[r];
@@ -329,7 +332,6 @@ hipError_t launch_block_grad(dp_dtype dt, dp_dtype pdt, const BlockNorm& b, int6
     a.dim = static_cast<int32_t>(b.dim);
     a.eps = b.eps;
     a.alpha = b.alpha;
-    a.vec = vec;
     a.w = weights_of(b);
     const bool post = b.weight[0] != nullptr;
     const int groups = static_cast<int>(groups_of(b.dim, tokens, n));

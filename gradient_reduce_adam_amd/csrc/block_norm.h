@@ -42,19 +42,19 @@ __device__ __forceinline__ void row_sum(float (&v)[K], float* lds, int& turn) {
 
 struct Weights {
     const void *post_w, *post_b, *gate, *pre_w, *pre_b;  // null: none
-    bool vec;
 };
 
 // The weights of this thread's columns stay packed in registers over all rows.
 template <dp_dtype PT, int NV, int VW>
 struct Column {
     Raw<PT, VW> q[NV];
-    __device__ __forceinline__ void load(const void* p, int c0, int step, int dim, bool vec) {
+    __device__ __forceinline__ void load(const void* p, int c0, int step, int dim) {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int left = dim - (c0 + k * step);
             const int valid = !p || left <= 0 ? 0 : left < VW ? left : VW;
-            q[k] = load_raw<PT, VW>(p, c0 + k * step, valid, vec);
+            q[k] = load_raw<PT, VW>(p, c0 + k * step, valid, dim >= VW);
+            settle<PT, VW>(q[k], valid, dim >= VW);
         }
     }
 };
@@ -76,7 +76,6 @@ inline Weights weights_of(const BlockNorm& b) {
     w.gate = b.weight[2];
     w.pre_w = b.weight[3];
     w.pre_b = b.weight[4];
-    w.vec = b.vec_w;
     return w;
 }
 

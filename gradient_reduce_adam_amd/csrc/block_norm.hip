@@ -27,7 +27,6 @@ struct NormArgs {
     int64_t tokens;
     int32_t dim;
     float eps, alpha;
-    bool vec_h, vec_y, vec_s, vec_x;
     Weights w;
 };
 
@@ -40,12 +39,12 @@ __global__ void __launch_bounds__(block_of(NT)) k_block_norm(NormArgs a) {
     const float dim = static_cast<float>(a.dim), inv = 1.0f / dim;
     const bool has_gate = a.w.gate != nullptr, has_x = a.x != nullptr;
     Column<PT, NV, VW> post_w, post_b, gate, pre_w, pre_b;
-    if constexpr (kPost) post_w.load(a.w.post_w, c0, kStep, a.dim, a.w.vec);
-    if constexpr (kPost && kCentered) post_b.load(a.w.post_b, c0, kStep, a.dim, a.w.vec);
-    if (has_gate) gate.load(a.w.gate, c0, kStep, a.dim, a.w.vec);
+    if constexpr (kPost) post_w.load(a.w.post_w, c0, kStep, a.dim);
+    if constexpr (kPost && kCentered) post_b.load(a.w.post_b, c0, kStep, a.dim);
+    if (has_gate) gate.load(a.w.gate, c0, kStep, a.dim);
     if (has_x) {
-        pre_w.load(a.w.pre_w, c0, kStep, a.dim, a.w.vec);
-        if constexpr (kCentered) pre_b.load(a.w.pre_b, c0, kStep, a.dim, a.w.vec);
+        pre_w.load(a.w.pre_w, c0, kStep, a.dim);
+        if constexpr (kCentered) pre_b.load(a.w.pre_b, c0, kStep, a.dim);
     }
     // a workgroup's rows: in every turn all its rows run (the last turn's
     // beyond the end are computed on zeros and not stored), so that barriers meet
@@ -58,8 +57,8 @@ __global__ void __launch_bounds__(block_of(NT)) k_block_norm(NormArgs a) {
         for (int k = 0; k < NV; ++k) {
             const int c = c0 + k * kStep;
             const int valid = t < a.tokens ? valid_of<VW>(a.dim, c) : 0;
-            nh[k] = load_raw<DT, VW>(a.h, t * a.ld_h + c, valid, a.vec_h);
-            ny[k] = load_raw<DT, VW>(a.y, t * a.ld_y + c, valid, a.vec_y);
+            nh[k] = load_raw<DT, VW>(a.h, t * a.ld_h + c, valid, a.dim >= VW);
+            ny[k] = load_raw<DT, VW>(a.y, t * a.ld_y + c, valid, a.dim >= VW);
         }
     };
     fetch(row);
@@ -67,6 +66,9 @@ __global__ void __launch_bounds__(block_of(NT)) k_block_norm(NormArgs a) {
         float h[NV][VW], u[NV][VW];
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
+            const int valid = row < a.tokens ? valid_of<VW>(a.dim, c0 + k * kStep) : 0;
+            settle<DT, VW>(nh[k], valid, a.dim >= VW);
+            settle<DT, VW>(ny[k], valid, a.dim >= VW);
             expand<DT, VW>(nh[k], h[k]);
             expand<DT, VW>(ny[k], u[k]);
         }
@@ -114,7 +116,7 @@ __global__ void __launch_bounds__(block_of(NT)) k_block_norm(NormArgs a) {
             const int valid = row < a.tokens ? valid_of<VW>(a.dim, c) : 0;
 #pragma unroll
             for (int j = 0; j < VW; ++j) h[k][j] = a.alpha * h[k][j] + u[k][j];
-            store_n<DT, VW>(a.s, row * a.ld_s + c, valid, a.vec_s, h[k]);
+            store_n<DT, VW>(a.s, row * a.ld_s + c, valid, h[k]);
         }
         if (!has_x) continue;
         if constexpr (kCentered) {
@@ -147,7 +149,7 @@ __global__ void __launch_bounds__(block_of(NT)) k_block_norm(NormArgs a) {
             for (int j = 0; j < VW; ++j) h[k][j] = h[k][j] * r * w[j] + (kCentered ? b[j] : 0.0f);
             const int c = c0 + k * kStep;
             const int valid = row < a.tokens ? valid_of<VW>(a.dim, c) : 0;
-            store_n<DT, VW>(a.x, row * a.ld_x + c, valid, a.vec_x, h[k]);
+            store_n<DT, VW>(a.x, row * a.ld_x + c, valid, h[k]);
         }
     }
 }
@@ -182,10 +184,10 @@ void forward(const NormArgs& a, hipStream_t stream) {
 
 hipError_t launch_block_norm(dp_dtype dt, dp_dtype pdt, const BlockNorm& b, int64_t tokens, const void* h,
                              int64_t ld_h, const void* y, int64_t ld_y, void* s, int64_t ld_s, void* x, int64_t ld_x,
-                             const bool* vec, hipStream_t stream) {
+                             hipStream_t stream) {
     if (tokens == 0) return hipSuccess;
     NormArgs a{h,    y,    s,     x, ld_h, ld_y, ld_s, ld_x, tokens, static_cast<int32_t>(b.dim), b.eps, b.alpha,
-               vec[0], vec[1], vec[2], vec[3], weights_of(b)};
+               weights_of(b)};
     const bool post = b.weight[0] != nullptr;
 #define GO(D, P, C, O) forward<D, P, C, O>(a, stream)
     DP_KINDS(GO);

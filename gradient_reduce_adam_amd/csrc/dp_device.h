@@ -18,21 +18,24 @@ typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 
-template <typename V>
+// Global memory in units of V at the alignment A: vectors may lie at any
+// element (unaligned access is on for compute, so a vector at 2-byte alignment is
+// still one instruction).
+template <typename V, int A>
+struct Loose {
+    typedef V type __attribute__((aligned(A)));
+};
+template <typename V, int A = sizeof(V)>
 __device__ __forceinline__ V gload(const void* p, int64_t i) {
-    return ((const DP_GLOBAL V*)p)[i];
+    return ((const DP_GLOBAL typename Loose<V, A>::type*)p)[i];
 }
-template <typename V>
+template <typename V, int A = sizeof(V)>
 __device__ __forceinline__ void gstore(void* p, int64_t i, V x) {
-    ((DP_GLOBAL V*)p)[i] = x;
+    ((DP_GLOBAL typename Loose<V, A>::type*)p)[i] = x;
 }
-template <typename V>
-__device__ __forceinline__ V gload_nt(const void* p, int64_t i) {
-    return __builtin_nontemporal_load(((const DP_GLOBAL V*)p) + i);
-}
-template <typename V>
+template <typename V, int A = sizeof(V)>
 __device__ __forceinline__ void gstore_nt(void* p, int64_t i, V x) {
-    __builtin_nontemporal_store(x, ((DP_GLOBAL V*)p) + i);
+    __builtin_nontemporal_store(x, ((DP_GLOBAL typename Loose<V, A>::type*)p) + i);
 }
 
 // Two binary32 values as two 16-bit elements in one word and back (to nearest
@@ -90,25 +93,24 @@ __device__ __forceinline__ float wave_sum(float x) {
 }
 
 // N (4 or 8) consecutive elements from element i of p, of which the first
-// `valid` exist (the others come back as zero, or are not written).  `vec`:
-// the address is a multiple of the vector's bytes (16 at most), so that whole
-// vectors go in one or two accesses.
+// `valid` exist (the others come back as zero, or are not written); a whole
+// vector goes in one or two accesses.
 template <dp_dtype DT, int N>
-__device__ __forceinline__ void load_n(const void* p, int64_t i, int valid, bool vec, float* o) {
-    if (vec && valid >= N) {
+__device__ __forceinline__ void load_n(const void* p, int64_t i, int valid, float* o) {
+    if (valid >= N) {
         if constexpr (DT == DP_F32) {
 #pragma unroll
             for (int k = 0; k < N / 4; ++k) {
-                const f32x4 v = gload<f32x4>(static_cast<const float*>(p) + i, k);
+                const f32x4 v = gload<f32x4, 4>(static_cast<const float*>(p) + i, k);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) o[4 * k + j] = v[j];
             }
         } else if constexpr (N == 8) {
-            const u32x4 v = gload<u32x4>(static_cast<const unsigned short*>(p) + i, 0);
+            const u32x4 v = gload<u32x4, 2>(static_cast<const unsigned short*>(p) + i, 0);
 #pragma unroll
             for (int j = 0; j < 4; ++j) unpack2<DT>(v[j], o + 2 * j);
         } else {
-            const u32x2 v = gload<u32x2>(static_cast<const unsigned short*>(p) + i, 0);
+            const u32x2 v = gload<u32x2, 2>(static_cast<const unsigned short*>(p) + i, 0);
 #pragma unroll
             for (int j = 0; j < 2; ++j) unpack2<DT>(v[j], o + 2 * j);
         }
@@ -119,12 +121,13 @@ __device__ __forceinline__ void load_n(const void* p, int64_t i, int valid, bool
 }
 // kOnce: the data is not read again soon, so it need not stay in the caches.
 template <dp_dtype DT, int N, bool kOnce = false>
-__device__ __forceinline__ void store_n(void* p, int64_t i, int valid, bool vec, const float* x) {
+__device__ __forceinline__ void store_n(void* p, int64_t i, int valid, const float* x) {
     const auto put = [](auto* at, int64_t k, auto v) {
-        if constexpr (kOnce) gstore_nt(at, k, v);
-        else gstore(at, k, v);
+        constexpr int kAlign = sizeof(*at);
+        if constexpr (kOnce) gstore_nt<decltype(v), kAlign>(at, k, v);
+        else gstore<decltype(v), kAlign>(at, k, v);
     };
-    if (vec && valid >= N) {
+    if (valid >= N) {
         if constexpr (DT == DP_F32) {
 #pragma unroll
             for (int k = 0; k < N / 4; ++k)
@@ -149,27 +152,34 @@ struct Raw {
     unsigned int w[kWords];
 };
 
+// A lane's piece of a row, loaded ahead of its use: elements i .. i + VW - 1 of p,
+// of which the first `valid` belong to the row.  A piece that the row's end cuts
+// short is loaded whole from VW - valid elements earlier (`whole`: the row has
+// that many), and `settle` moves its elements into place when they are used, so
+// that no lane waits for its loads where they are issued.
 template <dp_dtype DT, int VW>
-__device__ __forceinline__ Raw<DT, VW> load_raw(const void* p, int64_t i, int valid, bool vec) {
+__device__ __forceinline__ Raw<DT, VW> load_raw(const void* p, int64_t i, int valid, bool whole) {
     constexpr int kWords = Raw<DT, VW>::kWords;
+    constexpr int kSize = DT == DP_F32 ? 4 : 2;
     Raw<DT, VW> q;
-    if (vec && valid >= VW) {
-        const char* at = static_cast<const char*>(p) + i * (DT == DP_F32 ? 4 : 2);
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) q.w[k] = 0;
+    if (valid <= 0) return q;
+    if (whole) {
+        const char* at = static_cast<const char*>(p) + (i - (VW - valid)) * kSize;
         if constexpr (kWords == 2) {
-            const u32x2 v = gload<u32x2>(at, 0);
+            const u32x2 v = gload<u32x2, kSize>(at, 0);
             q.w[0] = v[0];
             q.w[1] = v[1];
         } else {
 #pragma unroll
             for (int k = 0; k < kWords / 4; ++k) {
-                const u32x4 v = gload<u32x4>(at, k);
+                const u32x4 v = gload<u32x4, kSize>(at, k);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) q.w[4 * k + j] = v[j];
             }
         }
-        return q;
-    }
-    if constexpr (DT == DP_F32) {
+    } else if constexpr (DT == DP_F32) {
 #pragma unroll
         for (int j = 0; j < VW; ++j) q.w[j] = j < valid ? gload<unsigned int>(p, i + j) : 0u;
     } else {
@@ -181,6 +191,20 @@ __device__ __forceinline__ Raw<DT, VW> load_raw(const void* p, int64_t i, int va
         }
     }
     return q;
+}
+template <dp_dtype DT, int VW>
+__device__ __forceinline__ void settle(Raw<DT, VW>& q, int valid, bool whole) {
+    if (!whole || valid <= 0 || valid >= VW) return;
+    constexpr int kWords = Raw<DT, VW>::kWords;
+#pragma unroll
+    for (int s = 0; s < VW - 1; ++s) {
+        if (s >= VW - valid) break;  // one element down, VW - valid times
+#pragma unroll
+        for (int k = 0; k < kWords; ++k) {
+            const unsigned int up = k + 1 < kWords ? q.w[k + 1] : 0u;
+            q.w[k] = DT == DP_F32 ? up : __builtin_amdgcn_alignbit(up, q.w[k], 16);
+        }
+    }
 }
 
 template <dp_dtype DT, int VW>

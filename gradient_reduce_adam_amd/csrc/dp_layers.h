@@ -12,10 +12,8 @@
 namespace dpk {
 
 // ---- embedding (embed.hip) -------------------------------------------------
-// `vec` flags say that rows can be moved in whole vectors: base addresses and
-// row strides are multiples of what one lane moves.
 hipError_t launch_embed(dp_dtype pdt, dp_dtype odt, const void* table, int64_t rows, int64_t dim, float scale,
-                        int64_t tokens, const void* ids, int id_bytes, void* out, int64_t ld, bool vec,
+                        int64_t tokens, const void* ids, int id_bytes, void* out, int64_t ld,
                         hipStream_t stream);
 
 struct EmbedGrad {
@@ -25,9 +23,7 @@ struct EmbedGrad {
     int64_t rows, dim, tokens, ld;
     float scale;
     int32_t n, id_bytes;
-    bool overwrite;       // ACC = G, else ACC += G
-    bool vec_dy, vec_acc;  // rows of dy and of the accumulators in vectors of 4 elements
-    bool vec_base;         // every accumulator's first row is aligned to 16 bytes
+    bool overwrite;  // ACC = G, else ACC += G
 };
 size_t embed_workspace(int64_t dim, int64_t tokens, int n);
 int64_t embed_waves(const EmbedGrad& a);   // one-wave workgroups of the sums, for one replica
@@ -40,24 +36,22 @@ struct BlockNorm {
     int64_t dim;
     float eps, alpha;
     bool centered;
-    bool vec_w;  // every weight can be read 16 bytes at a time
 };
-// vec: of h, y, s, x.
 hipError_t launch_block_norm(dp_dtype dt, dp_dtype pdt, const BlockNorm& b, int64_t tokens, const void* h,
                              int64_t ld_h, const void* y, int64_t ld_y, void* s, int64_t ld_s, void* x, int64_t ld_x,
-                             const bool* vec, hipStream_t stream);
+                             hipStream_t stream);
 size_t block_norm_workspace(int64_t dim, int64_t tokens, int n, bool centered);
 // at[i]: which accumulator (acc[at * n + r], overwrite[at]) takes the gradient
 // of weight i, -1 for none.
 hipError_t launch_block_grad(dp_dtype dt, dp_dtype pdt, const BlockNorm& b, int64_t tokens, int n,
-                             const dpl_norm_rows* rows, int64_t ld, bool vec, float* const* acc, const int* at,
+                             const dpl_norm_rows* rows, int64_t ld, float* const* acc, const int* at,
                              const bool* overwrite, void* workspace, hipStream_t stream);
 
 // ---- activations in 8 bits (act8.hip) ------------------------------------------
 hipError_t launch_pack(dp_dtype dt, int64_t tokens, int64_t dim, const void* x, int64_t ld, void* codes,
-                       int64_t ld_codes, void* scales, int64_t ld_scales, bool vec, hipStream_t stream);
+                       int64_t ld_codes, void* scales, int64_t ld_scales, hipStream_t stream);
 hipError_t launch_unpack(dp_dtype dt, int64_t tokens, int64_t dim, const void* codes, int64_t ld_codes,
-                         const void* scales, int64_t ld_scales, void* x, int64_t ld, bool vec, hipStream_t stream);
+                         const void* scales, int64_t ld_scales, void* x, int64_t ld, hipStream_t stream);
 
 // ---- weight gradient of a linear layer (linear.hip) -----------------------------
 struct LinearGrad {
@@ -66,7 +60,7 @@ struct LinearGrad {
     int64_t tokens, outputs, inputs, ld_dy, ld_codes, ld_scales;
     int32_t n;
     bool transposed, overwrite;
-    bool vec;  // rows of dy and codes are aligned to 16 bytes and made of whole 16-byte pieces
+    bool pieces;  // rows of at least one 16-byte piece, tiles within 32-bit offsets
 };
 int64_t linear_jobs(int64_t outputs, int64_t inputs, int64_t tokens, int n);  // workgroups of its launch
 size_t linear_workspace(int64_t outputs, int64_t inputs, int64_t tokens, int n);

@@ -45,7 +45,7 @@ __device__ __forceinline__ int64_t load_id(const void* ids, int id_bytes, int64_
 
 template <dp_dtype PT, dp_dtype OT, bool kOnce>
 __global__ void __launch_bounds__(64) k_embed(const void* table, int64_t rows, int64_t dim, float scale,
-                                              const void* ids, int id_bytes, void* out, int64_t ld, bool vec) {
+                                              const void* ids, int id_bytes, void* out, int64_t ld) {
     const int64_t t = blockIdx.x;
     const int64_t id = load_id(ids, id_bytes, t);
     const bool ok = id >= 0 && id < rows;
@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(64) k_embed(const void* table, int64_t rows, i
         const int64_t c = c0 + k * 512;
         const int64_t left = dim - c;
         const int valid = left >= 8 ? 8 : left > 0 ? static_cast<int>(left) : 0;
-        load_n<PT, 8>(table, src + c, valid, vec, v[k]);
+        load_n<PT, 8>(table, src + c, valid, v[k]);
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(64) k_embed(const void* table, int64_t rows, i
         const int valid = left >= 8 ? 8 : left > 0 ? static_cast<int>(left) : 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[k][j] = ok ? v[k][j] * scale : 0.0f;
-        store_n<OT, 8, kOnce>(out, t * ld + c, valid, vec, v[k]);
+        store_n<OT, 8, kOnce>(out, t * ld + c, valid, v[k]);
     }
 }
 
@@ -120,7 +120,6 @@ struct Zeros {
     float* acc[DP_MAX_REPLICAS];
     int64_t elements, groups;
     int32_t n;
-    bool vec;
 };
 constexpr int kZeroQuads = 4;  // 16-byte stores per thread
 constexpr int64_t kZeroSpan = int64_t{4} * kZeroQuads * kSortThreads;
@@ -128,10 +127,10 @@ constexpr int64_t kZeroSpan = int64_t{4} * kZeroQuads * kSortThreads;
 __device__ __forceinline__ void zero_table(const Zeros& z, int64_t group) {
     float* p = z.acc[group / z.groups];
     const int64_t i0 = group % z.groups * kZeroSpan, left = z.elements - i0;
-    if (z.vec && left >= kZeroSpan) {
+    if (left >= kZeroSpan) {
 #pragma unroll
         for (int k = 0; k < kZeroQuads; ++k)
-            gstore<f32x4>(p + i0, k * kSortThreads + threadIdx.x, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+            gstore<f32x4, 4>(p + i0, k * kSortThreads + threadIdx.x, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
     } else {
         for (int64_t i = threadIdx.x; i < left && i < kZeroSpan; i += kSortThreads) gstore<float>(p + i0, i, 0.0f);
     }
@@ -335,22 +334,23 @@ struct GradArgs {
     int64_t rows, dim, tokens, ld;
     int64_t chunks, slices;
     float scale;
-    bool vec_dy, vec_acc;
 };
 
 // The accumulator of 4 columns of a row, if the gradient is added to it.
 template <bool kOver>
-__device__ __forceinline__ void fetch(const GradArgs& a, const float* acc, int64_t row, int64_t c, int valid, float* old) {
-    if constexpr (!kOver) load_n<DP_F32, 4>(acc, row * a.dim + c, valid, a.vec_acc, old);
+__device__ __forceinline__ Raw<DP_F32, 4> fetch(const GradArgs& a, const float* acc, int64_t row, int64_t c, int valid) {
+    return load_raw<DP_F32, 4>(acc, row * a.dim + c, kOver ? 0 : valid, a.dim >= 4);
 }
 // ACC = scale * s, or what was fetched of it + scale * s.
 template <bool kOver>
 __device__ __forceinline__ void put(const GradArgs& a, float* acc, int64_t row, int64_t c, int valid, const float* s,
-                                    const float* old) {
+                                    Raw<DP_F32, 4> old) {
     float v[4];
+    settle<DP_F32, 4>(old, valid, a.dim >= 4);
+    expand<DP_F32, 4>(old, v);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = kOver ? a.scale * s[j] : old[j] + a.scale * s[j];
-    store_n<DP_F32, 4>(acc, row * a.dim + c, valid, a.vec_acc, v);
+    for (int j = 0; j < 4; ++j) v[j] = kOver ? a.scale * s[j] : v[j] + a.scale * s[j];
+    store_n<DP_F32, 4>(acc, row * a.dim + c, valid, v);
 }
 
 // Grid: (chunks * slices) x replicas, one wave each.
@@ -378,7 +378,6 @@ __global__ void __launch_bounds__(64) k_embed_sum(GradArgs a) {
     }
     const uint32_t before = __builtin_amdgcn_readlane(k, 62), behind = __builtin_amdgcn_readlane(k, 63);
     float* part = a.part + (r * a.chunks + chunk) * 2 * a.dim;
-    const bool vec_part = a.dim % 4 == 0;
     // bit i: pair i is the last of its run in this chunk
     const uint32_t after = __shfl_down(k, 1);
     const uint64_t ends = __ballot(l < count && (l == count - 1 || k != after));
@@ -386,7 +385,7 @@ __global__ void __launch_bounds__(64) k_embed_sum(GradArgs a) {
     bool head = __builtin_amdgcn_readlane(k, 0) == before;  // the current run began in an earlier chunk
     for (int b = 0; b < count; b += kBatch) {
         Raw<DT, 4> v[kBatch];
-        float old[kBatch][4];
+        Raw<DP_F32, 4> old[kBatch];
         uint32_t kk[kBatch];
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
@@ -395,20 +394,21 @@ __global__ void __launch_bounds__(64) k_embed_sum(GradArgs a) {
             const int64_t row = __builtin_amdgcn_readlane(p, i);
             // a batch past the chunk's end, or an id outside the table, reads no row
             const bool read = b + j < count && kk[j] < a.rows;
-            v[j] = load_raw<DT, 4>(a.dy[r], row * a.ld + c, read ? valid : 0, a.vec_dy);
-            fetch<kOver>(a, acc, kk[j], c, read && (ends >> i & 1) ? valid : 0, old[j]);
+            v[j] = load_raw<DT, 4>(a.dy[r], row * a.ld + c, read ? valid : 0, a.dim >= 4);
+            old[j] = fetch<kOver>(a, acc, kk[j], c, read && (ends >> i & 1) ? valid : 0);
         }
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
             if (b + j >= count) break;
             float x[4];
+            settle<DT, 4>(v[j], kk[j] < a.rows ? valid : 0, a.dim >= 4);
             expand<DT, 4>(v[j], x);
 #pragma unroll
             for (int q = 0; q < 4; ++q) s[q] += x[q];
             if (ends >> (b + j) & 1) {
                 if (kk[j] < a.rows) {
-                    if (head) store_n<DP_F32, 4>(part, c, valid, vec_part, s);
-                    else if (b + j == count - 1 && kk[j] == behind) store_n<DP_F32, 4>(part + a.dim, c, valid, vec_part, s);
+                    if (head) store_n<DP_F32, 4>(part, c, valid, s);
+                    else if (b + j == count - 1 && kk[j] == behind) store_n<DP_F32, 4>(part + a.dim, c, valid, s);
                     else put<kOver>(a, acc, kk[j], c, valid, s, old[j]);
                 }
                 head = false;
@@ -441,16 +441,15 @@ __global__ void __launch_bounds__(64) k_embed_join(GradArgs a) {
     }
     const int64_t left = a.dim - c;
     const int valid = left >= 4 ? 4 : left > 0 ? static_cast<int>(left) : 0;
-    const bool vec_part = a.dim % 4 == 0;
     const float* part = a.part + (r * a.chunks + chunk) * 2 * a.dim;
-    float s[4], old[4];
-    fetch<kOver>(a, a.acc[r], run, c, valid, old);
-    load_n<DP_F32, 4>(part + a.dim, c, valid, vec_part, s);
+    float s[4];
+    const Raw<DP_F32, 4> old = fetch<kOver>(a, a.acc[r], run, c, valid);
+    load_n<DP_F32, 4>(part + a.dim, c, valid, s);
     for (int64_t b = 0; b < n; b += kBatch) {
         float v[kBatch][4];
 #pragma unroll
         for (int j = 0; j < kBatch; ++j)
-            load_n<DP_F32, 4>(part + (b + j + 1) * 2 * a.dim, c, b + j < n ? valid : 0, vec_part, v[j]);
+            load_n<DP_F32, 4>(part + (b + j + 1) * 2 * a.dim, c, b + j < n ? valid : 0, v[j]);
 #pragma unroll
         for (int j = 0; j < kBatch; ++j)
 #pragma unroll
@@ -473,8 +472,7 @@ int passes_of(int64_t rows) {
 }  // namespace
 
 hipError_t launch_embed(dp_dtype pdt, dp_dtype odt, const void* table, int64_t rows, int64_t dim, float scale,
-                        int64_t tokens, const void* ids, int id_bytes, void* out, int64_t ld, bool vec,
-                        hipStream_t stream) {
+                        int64_t tokens, const void* ids, int id_bytes, void* out, int64_t ld, hipStream_t stream) {
     if (tokens == 0) return hipSuccess;
     const dim3 grid(static_cast<unsigned>(tokens), static_cast<unsigned>((dim + kLookupSpan - 1) / kLookupSpan));
     // An output beyond the 32 MiB of all L2 caches cannot wait there for its
@@ -482,7 +480,7 @@ hipError_t launch_embed(dp_dtype pdt, dp_dtype odt, const void* table, int64_t r
     // 4096 bf16 takes 58 us instead of 81.  A smaller one stays for its reader.
     const bool once = tokens * dim * (odt == DP_F32 ? 4 : 2) > (int64_t{32} << 20);
 #define DP_GO2(P, O, S) \
-    hipLaunchKernelGGL((k_embed<P, O, S>), grid, dim3(64), 0, stream, table, rows, dim, scale, ids, id_bytes, out, ld, vec)
+    hipLaunchKernelGGL((k_embed<P, O, S>), grid, dim3(64), 0, stream, table, rows, dim, scale, ids, id_bytes, out, ld)
 #define DP_GO(P, O)                    \
     if (pdt == P && odt == O) {        \
         if (once) DP_GO2(P, O, true);  \
@@ -537,7 +535,6 @@ hipError_t launch_embed_grad(dp_dtype dt, const EmbedGrad& a, void* workspace, h
     if (a.overwrite) {
         z.n = a.n;
         z.elements = a.rows * a.dim;
-        z.vec = a.vec_base;
         z.groups = (z.elements + kZeroSpan - 1) / kZeroSpan;
         for (int r = 0; r < a.n; ++r) z.acc[r] = a.acc[r];
     }
@@ -578,8 +575,6 @@ hipError_t launch_embed_grad(dp_dtype dt, const EmbedGrad& a, void* workspace, h
     g.chunks = chunks_of(a.tokens);
     g.slices = slices_of(a.dim);
     g.scale = a.scale;
-    g.vec_dy = a.vec_dy;
-    g.vec_acc = a.vec_acc;
     if (g.chunks == 0) return hipSuccess;
     const dim3 grid(static_cast<unsigned>(embed_waves(a)), static_cast<unsigned>(a.n));
 #define DP_GO(D)                                                                                   \

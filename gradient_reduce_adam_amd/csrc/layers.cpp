@@ -27,11 +27,6 @@ dp_status launched(hipError_t e, const char* what) { return e == hipSuccess ? DP
 
 bool multiple(const void* p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(bytes) == 0; }
 
-// Rows that can be moved `bytes` at a time.
-bool vec_rows(const void* p, int64_t ld, int64_t elem, int64_t bytes) {
-    return multiple(p, bytes) && ld * elem % bytes == 0;
-}
-
 dp_status check_rows(const char* where, const char* what, const void* p, int64_t tokens, int64_t dim, int64_t ld,
                      int64_t elem) {
     if (tokens > 0 && !p) return fail(DP_ERR_INVALID_ARG, "%s: %s is null", where, what);
@@ -133,14 +128,12 @@ dp_status check_norms(const char* where, const dp_plan* plan, const dpl_norms* d
 
 // The weights' addresses, once everything else is checked.
 dp_status norm_weights(const char* where, dp_plan* plan, Norms* n) {
-    n->b.vec_w = true;
     if (n->count == 0) return dpapi::ensure_device(plan);
     for (int i = 0; i < 5; ++i) {
         if (n->at[i] < 0) continue;
         dp_status s = dpapi::param_of(plan, n->tensors[n->at[i]], &n->b.weight[i]);
         if (s != DP_OK) return s;
         if (!multiple(n->b.weight[i], 2)) return fail(DP_ERR_INVALID_ARG, "%s: a weight is not aligned to its elements", where);
-        n->b.vec_w = n->b.vec_w && multiple(n->b.weight[i], 16);
     }
     return DP_OK;
 }
@@ -200,9 +193,9 @@ dp_status dpl_embed(dp_plan* plan, const dpl_table* table, int64_t tokens, const
     const void* w = nullptr;
     if (s == DP_OK) s = dpapi::param_of(plan, table->tensor, &w);
     if (s != DP_OK) return s;
-    const bool vec = vec_rows(w, table->dim, 2, 16) && vec_rows(out, ld, esize(dtype), 16);
+    if (!multiple(w, 2)) return fail(DP_ERR_INVALID_ARG, "%s: the table is not aligned to its elements", where);
     return launched(dpk::launch_embed(plan->pdt, dtype, w, rows, table->dim, static_cast<float>(table->scale), tokens,
-                                      ids, table->id_bytes, out, ld, vec, stream),
+                                      ids, table->id_bytes, out, ld, stream),
                     "embedding launch");
 }
 
@@ -227,14 +220,12 @@ dp_status dpl_accumulate_embed(dp_plan* plan, const dpl_table* table, int64_t to
     if (!dtype_ok(dtype)) return fail(DP_ERR_INVALID_ARG, "%s: unknown dtype %d", where, static_cast<int>(dtype));
     if (!ids || !dy) return fail(DP_ERR_INVALID_ARG, "%s: null argument", where);
     a.n = plan->n;
-    a.vec_dy = true;
     for (int32_t r = 0; r < plan->n; ++r) {
         s = check_ids(where, ids[r], tokens, table->id_bytes);
         if (s == DP_OK) s = check_rows(where, "dy", dy[r], tokens, table->dim, ld, esize(dtype));
         if (s != DP_OK) return s;
         a.ids[r] = ids[r];
         a.dy[r] = dy[r];
-        a.vec_dy = a.vec_dy && vec_rows(dy[r], ld, esize(dtype), 4 * esize(dtype));
     }
     s = check_workspace(where, workspace, workspace_bytes, dpk::embed_workspace(table->dim, tokens, plan->n));
     if (s != DP_OK) return s;
@@ -242,9 +233,6 @@ dp_status dpl_accumulate_embed(dp_plan* plan, const dpl_table* table, int64_t to
     s = dpapi::part_begin(plan, &table->tensor, 1, first != 0, where, a.acc, &overwrite);
     if (s == DP_OK) s = check_acc(where, a.acc, plan->n);
     if (s != DP_OK) return s;
-    a.vec_base = true;
-    for (int32_t r = 0; r < plan->n; ++r) a.vec_base = a.vec_base && multiple(a.acc[r], 16);
-    a.vec_acc = a.vec_base && table->dim % 4 == 0;
     a.dim = table->dim;
     a.tokens = tokens;
     a.ld = ld;
@@ -283,10 +271,8 @@ dp_status dpl_block_norm(dp_plan* plan, const dpl_norms* norms, int64_t tokens, 
         return fail(DP_ERR_INVALID_ARG, "%s: x must not overlap another tensor", where);
     s = norm_weights(where, plan, &n);
     if (s != DP_OK) return s;
-    const bool vec[4] = {vec_rows(h, ld_h, e, 16), vec_rows(y, ld_y, e, 16), vec_rows(s_out, ld_s, e, 16),
-                         vec_rows(x, ld_x, e, 16)};
     return launched(dpk::launch_block_norm(dtype, plan->pdt, n.b, tokens, h, ld_h, y, ld_y, s_out, ld_s,
-                                           has_x ? x : nullptr, ld_x, vec, stream),
+                                           has_x ? x : nullptr, ld_x, stream),
                     "block norm launch");
 }
 
@@ -313,7 +299,6 @@ dp_status dpl_accumulate_block_norm(dp_plan* plan, const dpl_norms* norms, int64
     if (n.count == 0) return fail(DP_ERR_INVALID_ARG, "%s: no norm and no gate", where);
     const int64_t e = esize(dtype);
     const bool has_x = n.at[3] >= 0, has_y = n.at[0] >= 0 || n.at[2] >= 0;
-    bool vec = ld * e % 16 == 0;
     for (int32_t r = 0; r < plan->n; ++r) {
         const dpl_norm_rows& p = rows[r];
         const void* all[6] = {p.s, p.y, p.dx, p.ds, p.dh, p.dy};
@@ -324,7 +309,6 @@ dp_status dpl_accumulate_block_norm(dp_plan* plan, const dpl_norms* norms, int64
                 return fail(DP_ERR_INVALID_ARG, "%s: %s is null for some replicas only", where, names[i]);
             s = check_rows(where, names[i], all[i], 0, n.b.dim, ld, e);
             if (s != DP_OK) return s;
-            vec = vec && multiple(all[i], 16);
         }
         if (tokens > 0 && !p.dx != !has_x)
             return fail(DP_ERR_INVALID_ARG, "%s: dx is given exactly with a norm before the next block", where);
@@ -342,7 +326,7 @@ dp_status dpl_accumulate_block_norm(dp_plan* plan, const dpl_norms* norms, int64
     if (s == DP_OK) s = norm_weights(where, plan, &n);
     if (s == DP_OK) s = check_acc(where, acc, n.count * plan->n);
     if (s != DP_OK) return s;
-    s = launched(dpk::launch_block_grad(dtype, plan->pdt, n.b, tokens, plan->n, rows, ld, vec, acc, n.at, overwrite,
+    s = launched(dpk::launch_block_grad(dtype, plan->pdt, n.b, tokens, plan->n, rows, ld, acc, n.at, overwrite,
                                         workspace, stream),
                  "block norm gradient launch");
     if (s != DP_OK) return s;
@@ -356,8 +340,7 @@ dp_status dpl_pack_activations(int64_t tokens, int64_t dim, dp_dtype dtype, cons
     dp_status s = check_packed(where, tokens, dim, dtype, codes, ld_codes, scales, ld_scales);
     if (s == DP_OK) s = check_rows(where, "x", x, tokens, dim, ld, esize(dtype));
     if (s != DP_OK) return s;
-    const bool vec = vec_rows(x, ld, esize(dtype), 16) && vec_rows(codes, ld_codes, 1, 16);
-    return launched(dpk::launch_pack(dtype, tokens, dim, x, ld, codes, ld_codes, scales, ld_scales, vec, stream),
+    return launched(dpk::launch_pack(dtype, tokens, dim, x, ld, codes, ld_codes, scales, ld_scales, stream),
                     "activation packing launch");
 }
 
@@ -367,8 +350,7 @@ dp_status dpl_unpack_activations(int64_t tokens, int64_t dim, dp_dtype dtype, co
     dp_status s = check_packed(where, tokens, dim, dtype, codes, ld_codes, scales, ld_scales);
     if (s == DP_OK) s = check_rows(where, "x", x, tokens, dim, ld, esize(dtype));
     if (s != DP_OK) return s;
-    const bool vec = vec_rows(x, ld, esize(dtype), 16) && vec_rows(codes, ld_codes, 1, 16);
-    return launched(dpk::launch_unpack(dtype, tokens, dim, codes, ld_codes, scales, ld_scales, x, ld, vec, stream),
+    return launched(dpk::launch_unpack(dtype, tokens, dim, codes, ld_codes, scales, ld_scales, x, ld, stream),
                     "activation unpacking launch");
 }
 
@@ -390,15 +372,14 @@ dp_status dpl_accumulate_linear(dp_plan* plan, const dpl_linear* linear, int64_t
     if (dtype != DP_BF16 && dtype != DP_F16) return fail(DP_ERR_INVALID_ARG, "%s: dtype must be DP_BF16 or DP_F16", where);
     if (!rows) return fail(DP_ERR_INVALID_ARG, "%s: null argument", where);
     dpk::LinearGrad g{};
-    g.vec = linear->inputs % 16 == 0 && linear->outputs % 8 == 0 && ld_dy < (int64_t{1} << 24) &&
-            ld_codes < (int64_t{1} << 24) && ld_scales < (int64_t{1} << 24);
+    g.pieces = linear->inputs >= 16 && linear->outputs >= 8 && ld_dy < (int64_t{1} << 24) &&
+               ld_codes < (int64_t{1} << 24) && ld_scales < (int64_t{1} << 24);
     for (int32_t r = 0; r < plan->n; ++r) {
         s = check_rows(where, "codes", rows[r].codes, tokens, linear->inputs, ld_codes, 1);
         if (s == DP_OK)
             s = check_rows(where, "scales", rows[r].scales, tokens, (linear->inputs + DPL_GROUP - 1) / DPL_GROUP, ld_scales, 1);
         if (s == DP_OK) s = check_rows(where, "dy", rows[r].dy, tokens, linear->outputs, ld_dy, 2);
         if (s != DP_OK) return s;
-        g.vec = g.vec && vec_rows(rows[r].codes, ld_codes, 1, 16) && vec_rows(rows[r].dy, ld_dy, 2, 16);
         g.rows[r] = rows[r];
     }
     s = check_workspace(where, workspace, workspace_bytes,

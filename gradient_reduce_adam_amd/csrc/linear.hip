@@ -117,16 +117,20 @@ struct Stage {
 };
 
 // Where a thread reads its pieces of a whole tile: offsets from the tile's first
-// token.  Columns past the last are read from the last whole piece: their
-// products are not stored.
+// token.  A piece that starts before the last column is read whole, into the
+// next token's row where the columns end within it (every whole tile has a
+// token behind it); one that starts behind it is read from the last eight or
+// sixteen columns.  The products of columns that do not exist are not stored.
 struct Pieces {
     uint32_t dy, codes, scales;
 };
 
-__device__ __forceinline__ Pieces pieces(const LinearArgs& a, const Job& j, int64_t ld_dy, int64_t ld_codes, int64_t ld_scales) {
+__device__ __forceinline__ Pieces pieces(const LinearArgs& a, const Job& j, bool whole, int64_t ld_dy, int64_t ld_codes,
+                                         int64_t ld_scales) {
     int64_t o = j.o0 + ((threadIdx.x & 31) << 3), i = j.i0 + ((threadIdx.x & 15) << 4);
-    o = o < a.outputs ? o : a.outputs - 8;
-    i = i < a.inputs ? i : a.inputs - 16;
+    // without a whole tile nothing is used, and no piece may pass the row's end
+    o = o < (whole ? a.outputs : a.outputs - 7) ? o : a.outputs - 8;
+    i = i < (whole ? a.inputs : a.inputs - 15) ? i : a.inputs - 16;
     return {static_cast<uint32_t>(2 * ((threadIdx.x >> 5) * ld_dy + o)),
             static_cast<uint32_t>((threadIdx.x >> 4) * ld_codes + i),
             static_cast<uint32_t>((threadIdx.x >> 4) * ld_scales + i / DPL_GROUP)};
@@ -137,16 +141,15 @@ __device__ __forceinline__ void load_full(const unsigned char* dy, const unsigne
                                           int64_t ld_dy, int64_t ld_codes, int64_t ld_scales, const Pieces& p, Stage& s) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        s.dy[2 * h] = gload<u32x4>(dy + 2 * h * 32 * ld_dy + p.dy, 0);
-        s.dy[2 * h + 1] = gload<u32x4>(dy + (2 * h + 1) * 32 * ld_dy + p.dy, 0);
-        s.codes[h] = gload<u32x4>(codes + h * 32 * ld_codes + p.codes, 0);
+        s.dy[2 * h] = gload<u32x4, 2>(dy + 2 * h * 32 * ld_dy + p.dy, 0);
+        s.dy[2 * h + 1] = gload<u32x4, 2>(dy + (2 * h + 1) * 32 * ld_dy + p.dy, 0);
+        s.codes[h] = gload<u32x4, 1>(codes + h * 32 * ld_codes + p.codes, 0);
         s.unit[h] = gload<unsigned char>(scales + h * 32 * ld_scales + p.scales, 0);
     }
 }
 
-// Tokens [t, end) of a tile, with zeros for tokens and columns that do not exist;
-// in whole pieces with kVec, else element by element.
-template <bool kVec>
+// Tokens [t, end) of a tile, with zeros for tokens and columns that do not exist,
+// which are not read.
 __device__ __forceinline__ void load_checked(const LinearArgs& a, const Job& j, int64_t t, int64_t end, Stage& s) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -154,8 +157,8 @@ __device__ __forceinline__ void load_checked(const LinearArgs& a, const Job& j, 
         const int64_t left = a.outputs - (j.o0 + c);
         const int valid = t + k < end ? left >= 8 ? 8 : left > 0 ? static_cast<int>(left) : 0 : 0;
         const unsigned short* p = reinterpret_cast<const unsigned short*>(j.dy) + (t + k) * a.ld_dy + j.o0 + c;
-        if constexpr (kVec) {
-            s.dy[q] = valid ? gload<u32x4>(p, 0) : u32x4{0, 0, 0, 0};
+        if (valid == 8) {
+            s.dy[q] = gload<u32x4, 2>(p, 0);
         } else {
             unsigned int e[8];
 #pragma unroll
@@ -169,8 +172,8 @@ __device__ __forceinline__ void load_checked(const LinearArgs& a, const Job& j, 
         const int64_t left = a.inputs - (j.i0 + c);
         const int valid = t + k < end ? left >= 16 ? 16 : left > 0 ? static_cast<int>(left) : 0 : 0;
         const unsigned char* p = j.codes + (t + k) * a.ld_codes + j.i0 + c;
-        if constexpr (kVec) {
-            s.codes[h] = valid ? gload<u32x4>(p, 0) : u32x4{0, 0, 0, 0};
+        if (valid == 16) {
+            s.codes[h] = gload<u32x4, 1>(p, 0);
         } else {
             unsigned int e[16];
 #pragma unroll
@@ -216,10 +219,10 @@ __device__ __forceinline__ void spread() {
 }
 
 // Rows of the result are outputs (columns inputs), or inputs with kSwap; the
-// lanes of a wave run along the columns.  kVec: every row of dy and codes is
-// aligned to 16 bytes and made of whole 16-byte pieces, and all tiles but the
-// first, which takes the odd tokens, are loaded without checks.
-template <dp_dtype DT, bool kSwap, bool kVec>
+// lanes of a wave run along the columns.  The last 1 to 64 tokens are loaded
+// with checks and multiplied first, then the whole tiles before them; without
+// kPieces (fewer than 8 outputs or 16 inputs) those are loaded with checks too.
+template <dp_dtype DT, bool kSwap, bool kPieces>
 __global__ void __launch_bounds__(kThreads) k_linear(LinearArgs a) {
     __shared__ __align__(1024) unsigned char lds[4 * kTileBytes];  // two turns of a dy and an x tile
     // tiles in the order of their operands' reuse: neighbouring workgroups of one
@@ -278,25 +281,25 @@ __global__ void __launch_bounds__(kThreads) k_linear(LinearArgs a) {
 #pragma unroll
             for (int n = 0; n < 2; ++n) c[m][n] = mma<DT>(p[b][m], q[b][n], c[m][n]);
     };
-    const int64_t full = t1 > t0 ? (t1 - t0 - 1) / kTileTokens : -1;  // whole tiles behind the first one
+    const int64_t full = t1 > t0 ? (t1 - t0 - 1) / kTileTokens : -1;  // whole tiles before the last tokens
     if (full >= 0) {
         Stage s;
-        int64_t t = t1 - full * kTileTokens;  // the next tile to load
-        load_checked<kVec>(a, j, t0, t, s);
+        load_checked(a, j, t0 + full * kTileTokens, t1, s);
         store_half<DT>(s, 0, base + put_dy, base + put_x);
         store_half<DT>(s, 1, base + put_dy, base + put_x);
-        // Past the end the last tile is loaded again, and not used; without a
-        // whole tile that is the first token, at a stride of 0.
-        const int64_t last = full > 0 ? t1 - kTileTokens : t0;
+        // Past the end the last whole tile is loaded again, and not used; without
+        // a whole tile that is the first token, at a stride of 0.
+        int64_t t = t0;  // the next tile to load
+        const int64_t last = full > 0 ? t0 + (full - 1) * kTileTokens : t0;
         const int64_t ld_dy = full > 0 ? a.ld_dy : 0, ld_codes = full > 0 ? a.ld_codes : 0;
         const int64_t ld_scales = full > 0 ? a.ld_scales : 0;
-        const Pieces at_row = pieces(a, j, ld_dy, ld_codes, ld_scales);
+        const Pieces at_row = pieces(a, j, full > 0, ld_dy, ld_codes, ld_scales);
         auto load = [&]() {
             const int64_t from = t < last ? t : last;
-            if constexpr (kVec)
+            if constexpr (kPieces)
                 load_full(j.dy + 2 * from * a.ld_dy, j.codes + from * a.ld_codes, j.scales + from * a.ld_scales, ld_dy,
                           ld_codes, ld_scales, at_row, s);
-            else load_checked<false>(a, j, from, t1, s);
+            else load_checked(a, j, from, from + kTileTokens < t1 ? from + kTileTokens : t1, s);
             t += kTileTokens;
         };
         load();
@@ -366,22 +369,20 @@ __global__ void __launch_bounds__(256) k_linear_join(LinearArgs a) {
     const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
     const int64_t left = size - i;
     const int valid = left >= 4 ? 4 : left > 0 ? static_cast<int>(left) : 0;
-    const bool vec = size % 4 == 0;
     float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     for (int k = 0; k < a.splits; ++k) {
         float v[4];
-        load_n<DP_F32, 4>(a.part + (static_cast<int64_t>(k) * a.n + r) * size, i, valid, vec, v);
+        load_n<DP_F32, 4>(a.part + (static_cast<int64_t>(k) * a.n + r) * size, i, valid, v);
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[e] += v[e];
     }
-    const bool vec_acc = (reinterpret_cast<uintptr_t>(a.acc[r]) & 15) == 0;
     if (!a.overwrite) {
         float v[4];
-        load_n<DP_F32, 4>(a.acc[r], i, valid, vec_acc, v);
+        load_n<DP_F32, 4>(a.acc[r], i, valid, v);
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[e] = v[e] + s[e];
     }
-    store_n<DP_F32, 4>(a.acc[r], i, valid, vec_acc, s);
+    store_n<DP_F32, 4>(a.acc[r], i, valid, s);
 }
 
 // Workgroups that share the tokens of one tile: as many as fill the chip's
@@ -429,7 +430,7 @@ hipError_t launch_linear(dp_dtype dt, const LinearGrad& g, void* workspace, hipS
     const dim3 grid(static_cast<unsigned>(linear_jobs(g.outputs, g.inputs, g.tokens, g.n)));
 #define DP_GO(D, S)                                                                                              \
     if (dt == D && g.transposed == S) {                                                                         \
-        if (g.vec) hipLaunchKernelGGL((k_linear<D, S, true>), grid, dim3(kThreads), 0, stream, a);              \
+        if (g.pieces) hipLaunchKernelGGL((k_linear<D, S, true>), grid, dim3(kThreads), 0, stream, a);              \
         else hipLaunchKernelGGL((k_linear<D, S, false>), grid, dim3(kThreads), 0, stream, a);                   \
     }
     DP_GO(DP_BF16, false)

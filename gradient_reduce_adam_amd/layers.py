@@ -140,6 +140,15 @@ def _rows(name: str, t, device: int, tokens: Optional[int] = None, dim: Optional
     return t.stride(0) if shape[0] > 1 else shape[1]
 
 
+def _like(name: str, t, device: int, shape, dtype) -> int:
+    """_rows of a tensor whose shape is known: the common case in four look-ups."""
+    if t.shape == shape and t.dtype is dtype and t.get_device() == device:
+        ld, one = t.stride()
+        if one == 1 and shape[0] > 1:
+            return ld
+    return _rows(name, t, device, shape[0], shape[1], dtype)
+
+
 def _same_stride(name: str, lds: Sequence[int]) -> int:
     if len(set(lds)) > 1:
         raise ValueError(f"{name}: every tensor must have the same row stride, got {sorted(set(lds))}")
@@ -209,7 +218,7 @@ def dpl_accumulate_embed(plan, tensor: int, ids: Sequence, dy: Sequence, first: 
     sizes = {_ids("ids", x, dev, tokens) for x in ids}
     if len(sizes) > 1:
         raise ValueError("ids: every replica's must have the same type")
-    ld = _same_stride("dy", [_rows("dy", x, dev, tokens, dim, dy[0].dtype) for x in dy])
+    ld = _same_stride("dy", [_like("dy", x, dev, dy[0].shape, dy[0].dtype) for x in dy])
     table = Table(tensor, sizes.pop(), dim, scale)
     addr, nbytes = _workspace(workspace, dev)
     _check(lib.dpl_accumulate_embed(plan.handle, ctypes.byref(table), tokens, _array(ids), _dtype(dy[0]), _array(dy),
@@ -221,11 +230,9 @@ def dpl_block_norm(plan, norms: BlockNorm, h, y, s, x=None, stream=None) -> None
     """s = residual_scale * h + gate * N_post(y) and, with a norm before the
     next block, x = N_pre(s)."""
     dev = torch.cuda.current_device()
-    tokens, dim = h.shape
-    dtype = h.dtype
-    ld_h, ld_y = _rows("h", h, dev), _rows("y", y, dev, tokens, dim, dtype)
-    ld_s = _rows("s", s, dev, tokens, dim, dtype)
-    ld_x, addr_x = (dim, None) if x is None else (_rows("x", x, dev, tokens, dim, dtype), x.data_ptr())
+    (tokens, dim), dtype = h.shape, h.dtype
+    ld_h, ld_y, ld_s = _rows("h", h, dev), _like("y", y, dev, h.shape, dtype), _like("s", s, dev, h.shape, dtype)
+    ld_x, addr_x = (dim, None) if x is None else (_like("x", x, dev, h.shape, dtype), x.data_ptr())
     _check(lib.dpl_block_norm(plan.handle, norms.ref(dim), tokens, _dtype(h), h.data_ptr(), ld_h, y.data_ptr(), ld_y,
                               s.data_ptr(), ld_s, addr_x, ld_x, _stream_of(stream, dev)))
 
@@ -248,8 +255,8 @@ def dpl_accumulate_block_norm(plan, norms: BlockNorm, s: Optional[Sequence], y: 
     if not there:
         raise ValueError("no rows are given")
     one = there[0][0]
-    tokens, dim = one.shape
-    ld = _same_stride("rows", [_rows("rows", t, dev, tokens, dim, one.dtype) for v in there for t in v])
+    tokens, dim = shape = one.shape
+    ld = _same_stride("rows", [_like("rows", t, dev, shape, one.dtype) for v in there for t in v])
     rows = (NormRows * plan.n)(*[NormRows(*[None if v is None else v[r].data_ptr() for v in given])
                                  for r in range(plan.n)])
     addr, nbytes = _workspace(workspace, dev)
@@ -265,8 +272,8 @@ def dpl_pack_activations(x, codes, scales, stream=None) -> None:
     ld = _rows("x", x, dev)
     tokens, dim = x.shape
     _check(lib.dpl_pack_activations(tokens, dim, _dtype(x), x.data_ptr(), ld, codes.data_ptr(),
-                                    _rows("codes", codes, dev, tokens, dim, torch.uint8), scales.data_ptr(),
-                                    _rows("scales", scales, dev, tokens, -(-dim // DPL_GROUP), torch.uint8),
+                                    _like("codes", codes, dev, x.shape, torch.uint8), scales.data_ptr(),
+                                    _like("scales", scales, dev, (tokens, -(-dim // DPL_GROUP)), torch.uint8),
                                     _stream_of(stream, dev)))
 
 
@@ -276,8 +283,8 @@ def dpl_unpack_activations(codes, scales, x, stream=None) -> None:
     ld = _rows("x", x, dev)
     tokens, dim = x.shape
     _check(lib.dpl_unpack_activations(tokens, dim, _dtype(x), codes.data_ptr(),
-                                      _rows("codes", codes, dev, tokens, dim, torch.uint8), scales.data_ptr(),
-                                      _rows("scales", scales, dev, tokens, -(-dim // DPL_GROUP), torch.uint8),
+                                      _like("codes", codes, dev, x.shape, torch.uint8), scales.data_ptr(),
+                                      _like("scales", scales, dev, (tokens, -(-dim // DPL_GROUP)), torch.uint8),
                                       x.data_ptr(), ld, _stream_of(stream, dev)))
 
 
@@ -298,9 +305,9 @@ def dpl_accumulate_linear(plan, tensor: int, dy: Sequence, codes: Sequence, scal
     dy, codes, scales = _replicas(plan, "dy", dy), _replicas(plan, "codes", codes), _replicas(plan, "scales", scales)
     (tokens, outputs), inputs = dy[0].shape, codes[0].shape[1]
     groups = -(-inputs // DPL_GROUP)
-    ld_dy = _same_stride("dy", [_rows("dy", t, dev, tokens, outputs, dy[0].dtype) for t in dy])
-    ld_c = _same_stride("codes", [_rows("codes", t, dev, tokens, inputs, torch.uint8) for t in codes])
-    ld_s = _same_stride("scales", [_rows("scales", t, dev, tokens, groups, torch.uint8) for t in scales])
+    ld_dy = _same_stride("dy", [_like("dy", t, dev, dy[0].shape, dy[0].dtype) for t in dy])
+    ld_c = _same_stride("codes", [_like("codes", t, dev, (tokens, inputs), torch.uint8) for t in codes])
+    ld_s = _same_stride("scales", [_like("scales", t, dev, (tokens, groups), torch.uint8) for t in scales])
     rows = (LinearRows * plan.n)(*[LinearRows(c.data_ptr(), e.data_ptr(), d.data_ptr())
                                    for c, e, d in zip(codes, scales, dy)])
     addr, nbytes = _workspace(workspace, dev)

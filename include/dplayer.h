@@ -37,9 +37,8 @@
  *
  * Rows.  An activation tensor is `tokens` rows of `dim` elements of a dtype
  * (DP_F32, DP_F16, DP_BF16); consecutive rows are `ld` elements apart (ld >=
- * dim; elements between the rows are neither read nor written).  Any size,
- * stride and element-aligned address works; addresses and strides that are
- * multiples of 16 bytes are read and written 16 bytes at a time.
+ * dim; elements between the rows are never written and never change a result).
+ * Any size, stride and element-aligned address works.
  */
 #ifndef DPLAYER_H
 #define DPLAYER_H
