@@ -26,7 +26,7 @@ struct EmbedGrad {
     bool overwrite;  // ACC = G, else ACC += G
 };
 size_t embed_workspace(int64_t dim, int64_t tokens, int n);
-int64_t embed_waves(const EmbedGrad& a);   // one-wave workgroups of the sums, for one replica
+int64_t embed_waves(const EmbedGrad& a);   // workgroups of the sums, of four waves, for one replica
 int64_t embed_groups(const EmbedGrad& a);  // workgroups of the first launch: the sort's and the zeros'
 hipError_t launch_embed_grad(dp_dtype dt, const EmbedGrad& a, void* workspace, hipStream_t stream);
 

@@ -17,13 +17,14 @@
 //    from ballots (which lanes hold my digit), so equal ids keep their order.
 //    Lists of at most 16384 tokens are sorted in LDS by one workgroup a replica
 //    in a single launch.
-//  - The sorted list is cut into chunks of 16 pairs.  One wave sums one chunk
-//    over 256 columns (4 a lane), adding rows of dy in list order.  A run that
-//    lies inside its chunk is finished there; one that crosses a boundary
-//    leaves a partial sum in the workspace, and a second launch adds the
-//    partials of each such run in chunk order.  A token that fills the whole
-//    batch is thus summed by all waves, and the order depends on nothing but
-//    the list.
+//  - The sorted list is cut into chunks of 64 pairs, 16 for each wave of a
+//    workgroup.  A wave sums its pairs over 256 columns (4 a lane), adding rows of
+//    dy in list order.  A run inside its 16 pairs is finished there; parts of
+//    longer ones are added through LDS in order; and one that crosses a
+//    chunk's end leaves a partial sum in the workspace, and a second launch
+//    adds the partials of each such run in chunk order.  A token that fills the
+//    whole batch is thus summed by all waves, and the order depends on nothing
+//    but the list.
 //  - When the gradient overwrites the accumulators, rows without a token have
 //    to become zero: further workgroups of the sort's first launch clear the
 //    tables meanwhile, so that the sort, which few CUs work on, costs nothing
@@ -321,9 +322,11 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_place(Ids ids, SortBuf sb
 }
 
 // ---- the sums ----------------------------------------------------------------
-constexpr int kChunk = 16;      // pairs of the sorted list per wave
-constexpr int kColumns = 256;   // columns per wave, 4 a lane
-constexpr int kBatch = 8;       // rows of dy in flight per wave
+constexpr int kSpan = 16;            // pairs of the sorted list per wave
+constexpr int kSpans = 4;            // waves of a workgroup
+constexpr int kChunk = kSpan * kSpans;
+constexpr int kColumns = 256;        // columns per wave, 4 a lane
+constexpr int kBatch = 8;            // rows in flight per wave
 
 struct GradArgs {
     const void* dy[DP_MAX_REPLICAS];
@@ -343,7 +346,7 @@ __device__ __forceinline__ Raw<DP_F32, 4> fetch(const GradArgs& a, const float* 
 }
 // ACC = scale * s, or what was fetched of it + scale * s.
 template <bool kOver>
-__device__ __forceinline__ void put(const GradArgs& a, float* acc, int64_t row, int64_t c, int valid, const float* s,
+__device__ __forceinline__ void put(const GradArgs& a, float* acc, int64_t row, int64_t c, int valid, f32x4 s,
                                     Raw<DP_F32, 4> old) {
     float v[4];
     settle<DP_F32, 4>(old, valid, a.dim >= 4);
@@ -353,36 +356,41 @@ __device__ __forceinline__ void put(const GradArgs& a, float* acc, int64_t row, 
     store_n<DP_F32, 4>(acc, row * a.dim + c, valid, v);
 }
 
-// Grid: (chunks * slices) x replicas, one wave each.
+// Grid: (chunks * slices) x replicas.  The four waves of a workgroup take 16 pairs
+// each of one chunk, over the same columns.
 template <dp_dtype DT, bool kOver>
-__global__ void __launch_bounds__(64) k_embed_sum(GradArgs a) {
-    const int r = blockIdx.y, l = lane_id();
+__global__ void __launch_bounds__(64 * kSpans) k_embed_sum(GradArgs a) {
+    __shared__ f32x4 heads[kSpans][64];  // sums of the waves' first runs, where they began in an earlier span
+    __shared__ bool through[kSpans];     // such a run fills the span and goes on
+    const int r = blockIdx.y, l = lane_id(), w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t* key = a.key + r * a.tokens;
     const uint32_t* pos = a.pos + r * a.tokens;
     float* acc = a.acc[r];
     const int64_t chunk = blockIdx.x / a.slices, c = (blockIdx.x % a.slices) * kColumns + 4 * l;
-    const int64_t left = a.dim - c;
-    const int valid = left >= 4 ? 4 : left > 0 ? static_cast<int>(left) : 0;
-    const int64_t i0 = chunk * kChunk;
-    const int count = static_cast<int>(a.tokens - i0 < kChunk ? a.tokens - i0 : kChunk);
-    // lane i < count: pair i; lane 62: the id before the chunk, lane 63: the one behind it
+    const int64_t width = a.dim - c;
+    const int valid = width >= 4 ? 4 : width > 0 ? static_cast<int>(width) : 0;
+    const int64_t i0 = chunk * kChunk + w * kSpan, left = a.tokens - i0;
+    const int count = left >= kSpan ? kSpan : left > 0 ? static_cast<int>(left) : 0;
+    // lane i < count: pair i; lane 62: the id before the span, lane 63: the one behind it
     const uint32_t none = 0xffffffffu;
     uint32_t k = none, p = 0;
     if (l < count) {
         k = key[i0 + l];
         p = pos[i0 + l];
-    } else if (l == 62 && i0 > 0) {
+    } else if (l == 62 && count > 0 && i0 > 0) {
         k = key[i0 - 1];
-    } else if (l == 63 && i0 + count < a.tokens) {
+    } else if (l == 63 && count > 0 && i0 + count < a.tokens) {
         k = key[i0 + count];
     }
     const uint32_t before = __builtin_amdgcn_readlane(k, 62), behind = __builtin_amdgcn_readlane(k, 63);
-    float* part = a.part + (r * a.chunks + chunk) * 2 * a.dim;
-    // bit i: pair i is the last of its run in this chunk
+    // bit i: pair i is the last of its run in this span
     const uint32_t after = __shfl_down(k, 1);
     const uint64_t ends = __ballot(l < count && (l == count - 1 || k != after));
-    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    bool head = __builtin_amdgcn_readlane(k, 0) == before;  // the current run began in an earlier chunk
+    const uint32_t first = __builtin_amdgcn_readlane(k, 0), last = __builtin_amdgcn_readlane(k, count > 0 ? count - 1 : 0);
+    const bool head = count > 0 && first == before && first < a.rows;  // the first run began earlier
+    const bool open = count > 0 && last == behind && last < a.rows;    // the last run goes on
+    f32x4 s{0.0f, 0.0f, 0.0f, 0.0f};
+    bool at_head = head;
     for (int b = 0; b < count; b += kBatch) {
         Raw<DT, 4> v[kBatch];
         Raw<DP_F32, 4> old[kBatch];
@@ -392,10 +400,12 @@ __global__ void __launch_bounds__(64) k_embed_sum(GradArgs a) {
             const int i = b + j < count ? b + j : count - 1;
             kk[j] = __builtin_amdgcn_readlane(k, i);
             const int64_t row = __builtin_amdgcn_readlane(p, i);
-            // a batch past the chunk's end, or an id outside the table, reads no row
+            // a batch past the span's end, or an id outside the table, reads no row
             const bool read = b + j < count && kk[j] < a.rows;
             v[j] = load_raw<DT, 4>(a.dy[r], row * a.ld + c, read ? valid : 0, a.dim >= 4);
-            old[j] = fetch<kOver>(a, acc, kk[j], c, read && (ends >> i & 1) ? valid : 0);
+            // runs that lie inside the span are finished here
+            const bool whole = (ends >> i & 1) && !(head && kk[j] == first) && !(open && kk[j] == last);
+            old[j] = fetch<kOver>(a, acc, kk[j], c, read && whole ? valid : 0);
         }
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
@@ -405,22 +415,39 @@ __global__ void __launch_bounds__(64) k_embed_sum(GradArgs a) {
             expand<DT, 4>(v[j], x);
 #pragma unroll
             for (int q = 0; q < 4; ++q) s[q] += x[q];
-            if (ends >> (b + j) & 1) {
-                if (kk[j] < a.rows) {
-                    if (head) store_n<DP_F32, 4>(part, c, valid, s);
-                    else if (b + j == count - 1 && kk[j] == behind) store_n<DP_F32, 4>(part + a.dim, c, valid, s);
-                    else put<kOver>(a, acc, kk[j], c, valid, s, old[j]);
-                }
-                head = false;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) s[q] = 0.0f;
-            }
+            if (!(ends >> (b + j) & 1)) continue;
+            if (at_head) heads[w][l] = s;
+            else if (b + j == count - 1 && open) break;  // s stays: the sum of the open run
+            else if (kk[j] < a.rows) put<kOver>(a, acc, kk[j], c, valid, s, old[j]);
+            at_head = false;
+            s = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         }
+    }
+    if (l == 0) through[w] = head && open && first == last;
+    __syncthreads();
+    // Runs over several spans: the wave where such a run begins adds the
+    // following waves' parts in order; so does the first wave with a run that began
+    // in an earlier chunk.
+    const bool inner = head && w == 0, outer = open && !(head && first == last);
+    float* part = a.part + (r * a.chunks + chunk) * 2 * a.dim;
+    if (inner) {
+        f32x4 t = heads[0][l];
+        for (int v = 0; v + 1 < kSpans && through[v]; ++v) t += heads[v + 1][l];
+        store_n<DP_F32, 4>(part, c, valid, reinterpret_cast<const float*>(&t));
+    }
+    if (outer) {
+        bool on = true;
+        for (int v = w + 1; v < kSpans && on; ++v) {
+            s += heads[v][l];
+            on = through[v];
+        }
+        if (on) store_n<DP_F32, 4>(part + a.dim, c, valid, reinterpret_cast<const float*>(&s));
+        else put<kOver>(a, acc, last, c, valid, s, fetch<kOver>(a, acc, last, c, valid));
     }
 }
 
 // Finishes the runs that cross a chunk's end: the wave of the chunk where such
-// a run begins adds its partials in chunk order (grid as the sums of k_embed_sum).
+// a run begins adds its partials in chunk order (one wave per chunk and slice).
 template <bool kOver>
 __global__ void __launch_bounds__(64) k_embed_join(GradArgs a) {
     const int r = blockIdx.y, l = lane_id();
@@ -442,14 +469,13 @@ __global__ void __launch_bounds__(64) k_embed_join(GradArgs a) {
     const int64_t left = a.dim - c;
     const int valid = left >= 4 ? 4 : left > 0 ? static_cast<int>(left) : 0;
     const float* part = a.part + (r * a.chunks + chunk) * 2 * a.dim;
-    float s[4];
+    f32x4 s;
     const Raw<DP_F32, 4> old = fetch<kOver>(a, a.acc[r], run, c, valid);
-    load_n<DP_F32, 4>(part + a.dim, c, valid, s);
+    load_n<DP_F32, 4>(part + a.dim, c, valid, reinterpret_cast<float*>(&s));
     for (int64_t b = 0; b < n; b += kBatch) {
         float v[kBatch][4];
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j)
-            load_n<DP_F32, 4>(part + (b + j + 1) * 2 * a.dim, c, b + j < n ? valid : 0, v[j]);
+        for (int j = 0; j < kBatch; ++j) load_n<DP_F32, 4>(part + (b + j + 1) * 2 * a.dim, c, b + j < n ? valid : 0, v[j]);
 #pragma unroll
         for (int j = 0; j < kBatch; ++j)
 #pragma unroll
@@ -579,8 +605,8 @@ hipError_t launch_embed_grad(dp_dtype dt, const EmbedGrad& a, void* workspace, h
     const dim3 grid(static_cast<unsigned>(embed_waves(a)), static_cast<unsigned>(a.n));
 #define DP_GO(D)                                                                                   \
     if (dt == D) {                                                                                 \
-        if (a.overwrite) hipLaunchKernelGGL((k_embed_sum<D, true>), grid, dim3(64), 0, stream, g); \
-        else hipLaunchKernelGGL((k_embed_sum<D, false>), grid, dim3(64), 0, stream, g);            \
+        if (a.overwrite) hipLaunchKernelGGL((k_embed_sum<D, true>), grid, dim3(64 * kSpans), 0, stream, g); \
+        else hipLaunchKernelGGL((k_embed_sum<D, false>), grid, dim3(64 * kSpans), 0, stream, g);            \
     }
     DP_GO(DP_F32)
     DP_GO(DP_F16)

@@ -239,7 +239,7 @@ dp_status dpl_accumulate_embed(dp_plan* plan, const dpl_table* table, int64_t to
     a.scale = static_cast<float>(table->scale);
     a.id_bytes = table->id_bytes;
     a.overwrite = overwrite;
-    if (dpk::embed_waves(a) > kMaxWaves || dpk::embed_groups(a) > kMaxGroups)
+    if (dpk::embed_waves(a) > kMaxWaves / 4 || dpk::embed_groups(a) > kMaxGroups)
         return fail(DP_ERR_INVALID_ARG, "%s: %lld tokens of %lld elements and %lld rows are too many for one call", where,
                     ll(tokens), ll(a.dim), ll(a.rows));
     s = launched(dpk::launch_embed_grad(dtype, a, workspace, stream), "embedding gradient launch");

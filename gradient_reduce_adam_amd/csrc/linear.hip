@@ -26,6 +26,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "dp_device.h"
 #include "dp_layers.h"
 
@@ -245,7 +247,7 @@ __global__ void __launch_bounds__(kThreads) k_linear(LinearArgs a) {
     const int64_t t0 = split * a.split_tokens;
     const int64_t t1 = t0 + a.split_tokens < a.tokens ? t0 + a.split_tokens : a.tokens;
 
-    const int w = threadIdx.x >> 6, l = threadIdx.x & 63;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63;
     const int wm = (w >> 2) * 128, wn = (w & 3) * 64;  // this wave's part of the tile: rows, columns
     f32x16 c[4][2];
 #pragma unroll
@@ -329,37 +331,46 @@ __global__ void __launch_bounds__(kThreads) k_linear(LinearArgs a) {
         }
     }
 
-    // element e of a 32 x 32 product: row 8 (e / 4) + 4 (l / 32) + e % 4, column l % 32
-    const int64_t row0 = (kSwap ? j.i0 : j.o0) + wm + 4 * (l >> 5), col0 = (kSwap ? j.o0 : j.i0) + wn + (l & 31);
+    // Element e of a 32 x 32 product: row 8 (e / 4) + 4 (l / 32) + e % 4, column l % 32.
+    // Products 2 m + n in turn, each as 16 rows of 32 columns twice, from a
+    // uniform address and a lane's offset; the accumulators of the next two are
+    // on their way while one is stored.
+    const int64_t row0 = (kSwap ? j.i0 : j.o0) + wm, col0 = (kSwap ? j.o0 : j.i0) + wn;
     const int64_t height = kSwap ? a.inputs : a.outputs, width = kSwap ? a.outputs : a.inputs;
     const bool over = a.overwrite || a.splits > 1;
     float* out = a.splits > 1 ? a.part + (static_cast<int64_t>(split) * a.n + r) * height * width : a.acc[r];
-    // products 2 m + n, each as 16 rows of 32 columns twice; the accumulators of the
-    // next two are on their way while one is stored
-    auto row_of = [&](int k, int e) { return row0 + 32 * (k >> 1) + 8 * (e >> 2) + (e & 3); };
-    auto there = [&](int k, int e) { return row_of(k, e) < height && col0 + 32 * (k & 1) < width; };
-    float old[3][16];
-    auto fetch = [&](int k) {
-        const float* p = out + row_of(k, 0) * width + col0 + 32 * (k & 1);
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-            if (there(k, e)) old[k % 3][e] = gload<float>(p + (8 * (e >> 2) + (e & 3)) * width, 0);
+    char* corner = reinterpret_cast<char*>(out + row0 * width + col0);
+    const uint32_t lane = static_cast<uint32_t>(4 * ((l >> 5) * 4 * width + (l & 31)));
+    const int64_t rows_left = height - row0 - 4 * (l >> 5), cols_left = width - col0 - (l & 31);
+    auto place_of = [&](int k, int e) {
+        return corner + 4 * ((32 * (k >> 1) + 8 * (e >> 2) + (e & 3)) * width + 32 * (k & 1)) + lane;
     };
-    if (!over) {
-        fetch(0);
-        fetch(1);
-    }
+    auto there = [&](int k, int e) {
+        return 32 * (k >> 1) + 8 * (e >> 2) + (e & 3) < rows_left && 32 * (k & 1) < cols_left;
+    };
+    auto finish = [&](auto inside) {  // inside: all of the wave's 128 x 64 elements exist
+        float old[3][16];
+        auto fetch = [&](int k) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        __builtin_amdgcn_sched_barrier(0);
-        if (!over && k + 2 < 8) fetch(k + 2);
-        float* p = out + row_of(k, 0) * width + col0 + 32 * (k & 1);
+            for (int e = 0; e < 16; ++e)
+                if (inside || there(k, e)) old[k % 3][e] = gload<float>(place_of(k, e), 0);
+        };
+        if (!over) {
+            fetch(0);
+            fetch(1);
+        }
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-            if (there(k, e))
-                gstore<float>(p + (8 * (e >> 2) + (e & 3)) * width, 0,
-                              over ? c[k >> 1][k & 1][e] : old[k % 3][e] + c[k >> 1][k & 1][e]);
-    }
+        for (int k = 0; k < 8; ++k) {
+            __builtin_amdgcn_sched_barrier(0);
+            if (!over && k + 2 < 8) fetch(k + 2);
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                if (inside || there(k, e))
+                    gstore<float>(place_of(k, e), 0, over ? c[k >> 1][k & 1][e] : old[k % 3][e] + c[k >> 1][k & 1][e]);
+        }
+    };
+    if (row0 + 128 <= height && col0 + 64 <= width) finish(std::true_type{});
+    else finish(std::false_type{});
 }
 
 // Adds the splits' tiles of every replica, in order, into the accumulators.
@@ -370,11 +381,16 @@ __global__ void __launch_bounds__(256) k_linear_join(LinearArgs a) {
     const int64_t left = size - i;
     const int valid = left >= 4 ? 4 : left > 0 ? static_cast<int>(left) : 0;
     float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int k = 0; k < a.splits; ++k) {
-        float v[4];
-        load_n<DP_F32, 4>(a.part + (static_cast<int64_t>(k) * a.n + r) * size, i, valid, v);
+    constexpr int kBatch = 8;  // partial sums on their way together
+    for (int k0 = 0; k0 < a.splits; k0 += kBatch) {
+        float v[kBatch][4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[e] += v[e];
+        for (int k = 0; k < kBatch; ++k)
+            load_n<DP_F32, 4>(a.part + (static_cast<int64_t>(k0 + k) * a.n + r) * size, i, k0 + k < a.splits ? valid : 0, v[k]);
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[e] += v[k][e];
     }
     if (!a.overwrite) {
         float v[4];
@@ -385,20 +401,35 @@ __global__ void __launch_bounds__(256) k_linear_join(LinearArgs a) {
     store_n<DP_F32, 4>(a.acc[r], i, valid, s);
 }
 
-// Workgroups that share the tokens of one tile: as many as fill the chip's
-// 256 CUs, each with at least 512 tokens.
+int64_t tiles_of(int64_t outputs, int64_t inputs, int n) {
+    return ((outputs + kTileCols - 1) / kTileCols) * ((inputs + kTileCols - 1) / kTileCols) * n;
+}
+
+// Workgroups that share the tokens of one tile, where all tiles together leave
+// CUs idle: the number that takes least by what was measured, 1.7 us for 64
+// tokens of a tile, and with more than one workgroup 4 us for the second launch,
+// 0.12 us for each partial sum that it adds, and all of them written and read at
+// 5 TB/s.
 int splits_of(int64_t outputs, int64_t inputs, int64_t tokens, int n) {
-    const int64_t tiles = ((outputs + kTileCols - 1) / kTileCols) * ((inputs + kTileCols - 1) / kTileCols) * n;
-    const int64_t most = tokens / 512, want = 256 / tiles;
-    const int64_t s = want < most ? want : most;
-    return s < 1 ? 1 : static_cast<int>(s);
+    const int64_t steps = (tokens + kTileTokens - 1) / kTileTokens;
+    const int64_t most = 256 / tiles_of(outputs, inputs, n);
+    const double part = 0.12 + 8.0 * static_cast<double>(outputs * inputs) * n / 5e6;  // us a workgroup
+    int best = 1;
+    double least = 1.7 * static_cast<double>(steps);
+    for (int64_t s = 2; s <= most && s <= steps; ++s) {
+        const double t = 1.7 * static_cast<double>((steps + s - 1) / s) + 4.0 + part * static_cast<double>(s);
+        if (t < least) {
+            least = t;
+            best = static_cast<int>(s);
+        }
+    }
+    return best;
 }
 
 }  // namespace
 
 int64_t linear_jobs(int64_t outputs, int64_t inputs, int64_t tokens, int n) {
-    const int64_t tiles = ((outputs + kTileCols - 1) / kTileCols) * ((inputs + kTileCols - 1) / kTileCols) * n;
-    return tiles * splits_of(outputs, inputs, tokens, n);
+    return tiles_of(outputs, inputs, n) * splits_of(outputs, inputs, tokens, n);
 }
 
 size_t linear_workspace(int64_t outputs, int64_t inputs, int64_t tokens, int n) {
