@@ -229,13 +229,10 @@ __global__ void __launch_bounds__(kThreads) k_linear(LinearArgs a) {
     __shared__ __align__(1024) unsigned char lds[4 * kTileBytes];  // two turns of a dy and an x tile
     // tiles in the order of their operands' reuse: neighbouring workgroups of one
     // XCD (every eighth) take tiles next to each other
-    const int64_t jobs = static_cast<int64_t>(gridDim.x);
-    const int64_t per = jobs / 8, extra = jobs % 8, xcd = blockIdx.x % 8, in = blockIdx.x / 8;
-    int64_t id = xcd * per + (xcd < extra ? xcd : extra) + in;
-    const int tiles = a.tiles_o * a.tiles_i;
-    const int tile = static_cast<int>(id % tiles);
-    id /= tiles;
-    const int r = static_cast<int>(id % a.n), split = static_cast<int>(id / a.n);
+    const int jobs = gridDim.x, per = jobs / 8, extra = jobs % 8, xcd = blockIdx.x % 8;
+    const int id = xcd * per + (xcd < extra ? xcd : extra) + blockIdx.x / 8;
+    const int tiles = a.tiles_o * a.tiles_i, tile = id % tiles;
+    const int r = id / tiles % a.n, split = id / tiles / a.n;
     const int band = tile / (8 * a.tiles_i), rows = a.tiles_o - 8 * band < 8 ? a.tiles_o - 8 * band : 8;
     const int within = tile - band * 8 * a.tiles_i;
     Job j;
@@ -370,7 +367,7 @@ __global__ void __launch_bounds__(kThreads) k_linear(LinearArgs a) {
         }
     };
     if (row0 + 128 <= height && col0 + 64 <= width) finish(std::true_type{});
-    else finish(std::false_type{});
+    else if (row0 < height && col0 < width) finish(std::false_type{});
 }
 
 // Adds the splits' tiles of every replica, in order, into the accumulators.
