@@ -84,13 +84,11 @@ def _register() -> None:
         "dpl_accumulate_embed": [vp, ctypes.POINTER(Table), i64, PP, c_int, PP, i64, i32, i32, vp, sz, vp],
         "dpl_block_norm": [vp, ctypes.POINTER(Norms), i64, c_int, vp, i64, vp, i64, vp, i64, vp, i64, vp],
         "dpl_block_norm_workspace": [vp, ctypes.POINTER(Norms), i64, PS],
-        "dpl_accumulate_block_norm": [vp, ctypes.POINTER(Norms), i64, c_int, ctypes.POINTER(NormRows), i64, i32, i32,
-                                      vp, sz, vp],
+        "dpl_accumulate_block_norm": [vp, ctypes.POINTER(Norms), i64, c_int, vp, i64, i32, i32, vp, sz, vp],
         "dpl_pack_activations": [i64, i64, c_int, vp, i64, vp, i64, vp, i64, vp],
         "dpl_unpack_activations": [i64, i64, c_int, vp, i64, vp, i64, vp, i64, vp],
         "dpl_linear_workspace": [vp, ctypes.POINTER(Linear), i64, PS],
-        "dpl_accumulate_linear": [vp, ctypes.POINTER(Linear), i64, c_int, ctypes.POINTER(LinearRows), i64, i64, i64,
-                                  i32, i32, vp, sz, vp],
+        "dpl_accumulate_linear": [vp, ctypes.POINTER(Linear), i64, c_int, vp, i64, i64, i64, i32, i32, vp, sz, vp],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -149,10 +147,17 @@ def _like(name: str, t, device: int, shape, dtype) -> int:
     return _rows(name, t, device, shape[0], shape[1], dtype)
 
 
-def _same_stride(name: str, lds: Sequence[int]) -> int:
-    if len(set(lds)) > 1:
-        raise ValueError(f"{name}: every tensor must have the same row stride, got {sorted(set(lds))}")
-    return lds[0]
+def _alike(name: str, ts: Sequence, device: int) -> int:
+    """The row stride of tensors that must all be like the first one."""
+    first = ts[0]
+    shape, dtype, strides = first.shape, first.dtype, first.stride()
+    ld = _rows(name, first, device)
+    for t in ts:
+        if t.stride() != strides or t.shape != shape or t.dtype is not dtype or t.get_device() != device:
+            other = _rows(name, t, device, shape[0], shape[1], dtype)
+            if other != ld:
+                raise ValueError(f"{name}: every tensor must have the same row stride, got {ld} and {other}")
+    return ld
 
 
 def _ids(name: str, t, device: int, tokens: Optional[int] = None) -> int:
@@ -214,11 +219,11 @@ def dpl_accumulate_embed(plan, tensor: int, ids: Sequence, dy: Sequence, first: 
     into the accumulators of plan tensor ``tensor``."""
     dev = torch.cuda.current_device()
     ids, dy = _replicas(plan, "ids", ids), _replicas(plan, "dy", dy)
-    tokens, dim = dy[0].shape
+    (tokens, dim) = dy[0].shape
     sizes = {_ids("ids", x, dev, tokens) for x in ids}
     if len(sizes) > 1:
         raise ValueError("ids: every replica's must have the same type")
-    ld = _same_stride("dy", [_like("dy", x, dev, dy[0].shape, dy[0].dtype) for x in dy])
+    ld = _alike("dy", dy, dev)
     table = Table(tensor, sizes.pop(), dim, scale)
     addr, nbytes = _workspace(workspace, dev)
     _check(lib.dpl_accumulate_embed(plan.handle, ctypes.byref(table), tokens, _array(ids), _dtype(dy[0]), _array(dy),
@@ -251,14 +256,15 @@ def dpl_accumulate_block_norm(plan, norms: BlockNorm, s: Optional[Sequence], y: 
     dev = torch.cuda.current_device()
     given = [None if v is None else _replicas(plan, k, v)
              for k, v in (("s", s), ("y", y), ("dx", dx), ("ds", ds), ("dh", dh), ("dy", dy))]
-    there = [v for v in given if v is not None]
+    there = [t for v in given if v is not None for t in v]
     if not there:
         raise ValueError("no rows are given")
-    one = there[0][0]
-    tokens, dim = shape = one.shape
-    ld = _same_stride("rows", [_like("rows", t, dev, shape, one.dtype) for v in there for t in v])
-    rows = (NormRows * plan.n)(*[NormRows(*[None if v is None else v[r].data_ptr() for v in given])
-                                 for r in range(plan.n)])
+    one = there[0]
+    ld = _alike("rows", there, dev)
+    tokens, dim = one.shape
+    # the structs of all replicas, a pointer after the other
+    rows = (ctypes.c_void_p * (6 * plan.n))(*[None if v is None else v[r].data_ptr() for r in range(plan.n)
+                                              for v in given])
     addr, nbytes = _workspace(workspace, dev)
     _check(lib.dpl_accumulate_block_norm(plan.handle, norms.ref(dim), tokens, _dtype(one), rows, ld, bool(first),
                                          bool(more), addr, nbytes, _stream_of(stream, dev)))
@@ -303,13 +309,12 @@ def dpl_accumulate_linear(plan, tensor: int, dy: Sequence, codes: Sequence, scal
     ``tensor``: outputs x inputs, or inputs x outputs if ``transposed``."""
     dev = torch.cuda.current_device()
     dy, codes, scales = _replicas(plan, "dy", dy), _replicas(plan, "codes", codes), _replicas(plan, "scales", scales)
+    ld_dy, ld_c, ld_s = _alike("dy", dy, dev), _alike("codes", codes, dev), _alike("scales", scales, dev)
     (tokens, outputs), inputs = dy[0].shape, codes[0].shape[1]
-    groups = -(-inputs // DPL_GROUP)
-    ld_dy = _same_stride("dy", [_like("dy", t, dev, dy[0].shape, dy[0].dtype) for t in dy])
-    ld_c = _same_stride("codes", [_like("codes", t, dev, (tokens, inputs), torch.uint8) for t in codes])
-    ld_s = _same_stride("scales", [_like("scales", t, dev, (tokens, groups), torch.uint8) for t in scales])
-    rows = (LinearRows * plan.n)(*[LinearRows(c.data_ptr(), e.data_ptr(), d.data_ptr())
-                                   for c, e, d in zip(codes, scales, dy)])
+    _rows("codes", codes[0], dev, tokens, inputs, torch.uint8)
+    _rows("scales", scales[0], dev, tokens, -(-inputs // DPL_GROUP), torch.uint8)
+    # the structs of all replicas, a pointer after the other
+    rows = (ctypes.c_void_p * (3 * plan.n))(*[t.data_ptr() for xs in zip(codes, scales, dy) for t in xs])
     addr, nbytes = _workspace(workspace, dev)
     _check(lib.dpl_accumulate_linear(plan.handle, ctypes.byref(Linear(tensor, bool(transposed), inputs, outputs)),
                                      tokens, _dtype(dy[0]), rows, ld_c, ld_s, ld_dy, bool(first), bool(more), addr,
