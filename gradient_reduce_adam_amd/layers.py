@@ -65,6 +65,10 @@ class BlockNorm:
             self._refs[dim] = ctypes.byref(Norms(*at, int(self.centered), dim, self.eps, self.residual_scale))
         return self._refs[dim]
 
+    def __reduce__(self):  # copies and pickles leave the references behind
+        return BlockNorm, (self.pre_w, self.pre_b, self.post_w, self.post_b, self.gate, self.centered, self.eps,
+                           self.residual_scale)
+
 
 class Linear(ctypes.Structure):
     _fields_ = [("tensor", ctypes.c_int32), ("transposed", ctypes.c_int32), ("inputs", ctypes.c_int64),

@@ -118,7 +118,8 @@ dp_status dpl_block_norm(dp_plan* plan, const dpl_norms* norms, int64_t tokens, 
                          int64_t ld_h, const void* y, int64_t ld_y, void* s, int64_t ld_s, void* x, int64_t ld_x,
                          hipStream_t stream);
 
-/* Bytes of workspace for dpl_accumulate_block_norm (host work only). */
+/* Bytes of workspace for dpl_accumulate_block_norm with up to `tokens` tokens a
+ * replica (host work only). */
 dp_status dpl_block_norm_workspace(const dp_plan* plan, const dpl_norms* norms, int64_t tokens, size_t* bytes);
 
 /* One replica's rows for the backward.  ds is the gradient that reaches s
@@ -179,7 +180,8 @@ typedef struct dpl_linear_rows {
     const void* dy;
 } dpl_linear_rows;
 
-/* Bytes of workspace for dpl_accumulate_linear (host work only; may be 0). */
+/* Bytes of workspace for dpl_accumulate_linear with up to `tokens` tokens a
+ * replica (host work only; may be 0, at most 64 MiB). */
 dp_status dpl_linear_workspace(const dp_plan* plan, const dpl_linear* linear, int64_t tokens, size_t* bytes);
 
 /* The weight gradient from the packed input:

@@ -2,8 +2,11 @@
 symbol is exported, workspace sizes are sane, and calls that the
 documentation does not allow are refused before anything touches a GPU (the
 addresses here are made up)."""
+import copy
 import ctypes
+import dataclasses
 import os
+import pickle
 import re
 import shutil
 import subprocess
@@ -151,6 +154,23 @@ def test_pack_refusals():
                    dict(x=None), dict(x=A + 1), dict(ld=39), dict(codes=None), dict(ldc=39), dict(scales=None),
                    dict(lds=1), dict(tokens=1 << 24, dim=1 << 12, ld=1 << 12, ldc=1 << 12, lds=1 << 7)):
             bad(lambda: call(fn, **kw))
+
+
+def test_workspaces_serve_fewer_tokens(plan):
+    """A workspace queried for some number of tokens is enough for any smaller one."""
+    ts = [0, 1, 2, 63, 64, 65, 127, 128, 200, 512, 1000, 4095, 4096, 5000, 16384, 16385, 70000, 1 << 20, 1 << 24]
+    for sizes in ([plan.embed_workspace(1, 6, t) for t in ts],
+                  [plan.linear_workspace(t, 1024, 1024) for t in ts], [plan.linear_workspace(t, 6, 10, 1) for t in ts],
+                  [plan.block_norm_workspace(dp.BlockNorm(pre_w=2, centered=True), 10, t) for t in ts]):
+        assert sizes == sorted(sizes)
+    assert plan.linear_workspace(1 << 24, 1024, 1024) <= 64 << 20
+
+
+def test_norm_descriptions_copy_and_pickle():
+    n = dp.BlockNorm(pre_w=2, gate=3, eps=1e-6, residual_scale=0.5)
+    n.ref(10)
+    for m in (copy.deepcopy(n), pickle.loads(pickle.dumps(n)), dataclasses.replace(n)):
+        assert m == n and m.ref(10) is not n.ref(10)
 
 
 def test_linear_refusals(plan):
