@@ -28,8 +28,6 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include <type_traits>
-
 #include "dp_device.h"
 #include "dp_layers.h"
 
@@ -152,6 +150,18 @@ __device__ __forceinline__ void load_full(const unsigned char* dy, const unsigne
     }
 }
 
+// 16 codes of which `valid` exist, for rows of at least 16: a piece that the
+// row's end cuts short is loaded from 16 - valid columns earlier and moved down.
+__device__ __forceinline__ u32x4 codes_piece(const unsigned char* p, int valid) {
+    u32x4 v = gload<u32x4, 1>(p - (16 - valid), 0);
+    const int s = 16 - valid;
+    if (s & 8) v = u32x4{v[2], v[3], 0, 0};
+    if (s & 4) v = u32x4{v[1], v[2], v[3], 0};
+    const unsigned int bits = 8 * (s & 3);
+    return u32x4{__builtin_amdgcn_alignbit(v[1], v[0], bits), __builtin_amdgcn_alignbit(v[2], v[1], bits),
+                 __builtin_amdgcn_alignbit(v[3], v[2], bits), __builtin_amdgcn_alignbit(0, v[3], bits)};
+}
+
 // Tokens [t, end) of a tile, with zeros for tokens and columns that do not exist,
 // which are not read.
 __device__ __forceinline__ void load_checked(const LinearArgs& a, const Job& j, int64_t t, int64_t end, Stage& s) {
@@ -160,15 +170,9 @@ __device__ __forceinline__ void load_checked(const LinearArgs& a, const Job& j, 
         const int id = q * kThreads + threadIdx.x, k = id >> 5, c = (id & 31) << 3;
         const int64_t left = a.outputs - (j.o0 + c);
         const int valid = t + k < end ? left >= 8 ? 8 : left > 0 ? static_cast<int>(left) : 0 : 0;
-        const unsigned short* p = reinterpret_cast<const unsigned short*>(j.dy) + (t + k) * a.ld_dy + j.o0 + c;
-        if (valid == 8) {
-            s.dy[q] = gload<u32x4, 2>(p, 0);
-        } else {
-            unsigned int e[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) e[i] = i < valid ? gload<unsigned short>(p, i) : 0;
-            s.dy[q] = u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
-        }
+        Raw<DP_BF16, 8> piece = load_raw<DP_BF16, 8>(j.dy, (t + k) * a.ld_dy + j.o0 + c, valid, a.outputs >= 8);
+        settle<DP_BF16, 8>(piece, valid, a.outputs >= 8);  // of either 16-bit type
+        s.dy[q] = u32x4{piece.w[0], piece.w[1], piece.w[2], piece.w[3]};
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -176,17 +180,17 @@ __device__ __forceinline__ void load_checked(const LinearArgs& a, const Job& j, 
         const int64_t left = a.inputs - (j.i0 + c);
         const int valid = t + k < end ? left >= 16 ? 16 : left > 0 ? static_cast<int>(left) : 0 : 0;
         const unsigned char* p = j.codes + (t + k) * a.ld_codes + j.i0 + c;
-        if (valid == 16) {
-            s.codes[h] = gload<u32x4, 1>(p, 0);
+        s.codes[h] = u32x4{0, 0, 0, 0};
+        s.unit[h] = 127;
+        if (valid == 0) continue;
+        if (a.inputs >= 16) {
+            s.codes[h] = codes_piece(p, valid);
         } else {
-            unsigned int e[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) e[i] = i < valid ? gload<unsigned char>(p, i) : 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                s.codes[h][i] = e[4 * i] | e[4 * i + 1] << 8 | e[4 * i + 2] << 16 | e[4 * i + 3] << 24;
+            for (int i = 0; i < 15; ++i)
+                s.codes[h][i / 4] |= i < valid ? static_cast<unsigned int>(gload<unsigned char>(p, i)) << (8 * (i % 4)) : 0u;
         }
-        s.unit[h] = valid ? gload<unsigned char>(j.scales, (t + k) * a.ld_scales + (j.i0 + c) / DPL_GROUP) : 127;
+        s.unit[h] = gload<unsigned char>(j.scales, (t + k) * a.ld_scales + (j.i0 + c) / DPL_GROUP);
     }
 }
 
@@ -331,7 +335,7 @@ __global__ void __launch_bounds__(kThreads) k_linear(LinearArgs a) {
     }
 
     // Element e of a 32 x 32 product: row 8 (e / 4) + 4 (l / 32) + e % 4, column l % 32.
-    // Products 2 m + n in turn, each as 16 rows of 32 columns twice, from a
+    // Products 2 m + n in turn, each as 16 rows of 32 columns twice, at a
     // uniform address and a lane's offset; the accumulators of the next two are
     // on their way while one is stored.
     const int64_t row0 = (kSwap ? j.i0 : j.o0) + wm, col0 = (kSwap ? j.o0 : j.i0) + wn;
@@ -340,19 +344,14 @@ __global__ void __launch_bounds__(kThreads) k_linear(LinearArgs a) {
     float* out = a.splits > 1 ? a.part + (static_cast<int64_t>(split) * a.n + r) * height * width : a.acc[r];
     char* corner = reinterpret_cast<char*>(out + row0 * width + col0);
     const uint32_t lane = static_cast<uint32_t>(4 * ((l >> 5) * 4 * width + (l & 31)));
-    const int64_t rows_left = height - row0 - 4 * (l >> 5), cols_left = width - col0 - (l & 31);
     auto place_of = [&](int k, int e) {
         return corner + 4 * ((32 * (k >> 1) + 8 * (e >> 2) + (e & 3)) * width + 32 * (k & 1)) + lane;
     };
-    auto there = [&](int k, int e) {
-        return 32 * (k >> 1) + 8 * (e >> 2) + (e & 3) < rows_left && 32 * (k & 1) < cols_left;
-    };
-    auto finish = [&](auto inside) {  // inside: all of the wave's 128 x 64 elements exist
+    if (row0 + 128 <= height && col0 + 64 <= width) {  // all of the wave's 128 x 64 elements exist
         float old[3][16];
         auto fetch = [&](int k) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-                if (inside || there(k, e)) old[k % 3][e] = gload<float>(place_of(k, e), 0);
+            for (int e = 0; e < 16; ++e) old[k % 3][e] = gload<float>(place_of(k, e), 0);
         };
         if (!over) {
             fetch(0);
@@ -364,12 +363,33 @@ __global__ void __launch_bounds__(kThreads) k_linear(LinearArgs a) {
             if (!over && k + 2 < 8) fetch(k + 2);
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-                if (inside || there(k, e))
-                    gstore<float>(place_of(k, e), 0, over ? c[k >> 1][k & 1][e] : old[k % 3][e] + c[k >> 1][k & 1][e]);
+                gstore<float>(place_of(k, e), 0, over ? c[k >> 1][k & 1][e] : old[k % 3][e] + c[k >> 1][k & 1][e]);
         }
-    };
-    if (row0 + 128 <= height && col0 + 64 <= width) finish(std::true_type{});
-    else if (row0 < height && col0 < width) finish(std::false_type{});
+        return;
+    }
+    // At the matrix' edges eight rows at a time, most of them whole or absent.
+    const int there = static_cast<int>(height - row0 < 128 ? height - row0 : 128);
+    const int64_t cols = width - col0 - (l & 31);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        if (32 * (k & 1) >= cols) continue;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const int row = 32 * (k >> 1) + 8 * g;
+            if (row >= there) continue;
+            const bool whole = row + 8 <= there;
+            float v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const bool in = whole || row + 4 * (l >> 5) + e < there;
+                v[e] = c[k >> 1][k & 1][4 * g + e];
+                if (!over && in) v[e] = gload<float>(place_of(k, 4 * g + e), 0) + v[e];
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (whole || row + 4 * (l >> 5) + e < there) gstore<float>(place_of(k, 4 * g + e), 0, v[e]);
+        }
+    }
 }
 
 // Adds the splits' tiles of every replica, in order, into the accumulators.
