@@ -139,6 +139,11 @@ CASES = [
     (65535, 8, 4096, "text", "bf16", torch.int64, 0, 4, False),
     (65536, 12, 4097, "text", "f16", torch.int32, 0, 4, False),
     (70000, 4, 9001, "reverse", "bf16", torch.int64, 0, 4, False),
+    (300, 8, 1025, "text", "bf16", torch.int64, 0, 4, False),
+    (255, 4, 2049, "same", "f16", torch.int32, 0, 4, False),
+    (9000, 12, 8192, "sorted", "bf16", torch.int64, 0, 4, False),
+    (9000, 12, 8193, "wild", "f32", torch.int64, 0, 4, False),
+    (50257, 8, 16384, "text", "bf16", torch.int32, 0, 4, False),
     (500, 20, 20000, "same", "f32", torch.int64, 0, 4, False),
     (33, 3, 300001, "text", "bf16", torch.int32, 0, 3, False),
 ]
@@ -146,7 +151,7 @@ CASES = [
 
 @pytest.mark.parametrize("V,D,T,kind,dt,id_dtype,pad,off,tensors", CASES)
 def test_gradient(V, D, T, kind, dt, id_dtype, pad, off, tensors):
-    n = 1 if T > 10000 else 3
+    n = 1 if T > 16384 else 3
     g = torch.Generator().manual_seed(T * 7 + V)
     s = Setup(V, D, n, off, tensors)
     scale = 0.75
