@@ -10,8 +10,9 @@
  * up rows, the inputs of a norm, the 8-bit input of a linear layer) and leave
  *   ACC[r] = G_r            (first != 0)
  *   ACC[r] = ACC[r] + G_r   (first == 0)
- * with G_r summed in binary32 in an order that depends on the sizes alone,
- * never on timing: the same call on the same inputs gives the same bits.
+ * with G_r summed in binary32 in an order that depends on the sizes and the
+ * token ids alone, never on timing: the same call on the same inputs gives the
+ * same bits.
  *
  * Micro-steps.  The dpl_accumulate_* calls are buckets of one micro-step of
  * every replica, as those of dp_accumulate_all_range are, each covering its

@@ -144,6 +144,7 @@ CASES = [
     (9000, 12, 8192, "sorted", "bf16", torch.int64, 0, 4, False),
     (9000, 12, 8193, "wild", "f32", torch.int64, 0, 4, False),
     (50257, 8, 16384, "text", "bf16", torch.int32, 0, 4, False),
+    (100003, 241, 33, "text", "bf16", torch.int64, 0, 3, False),  # replicas' tables of 289 MB, a ragged end
     (500, 20, 20000, "same", "f32", torch.int64, 0, 4, False),
     (33, 3, 300001, "text", "bf16", torch.int32, 0, 3, False),
 ]
