@@ -452,6 +452,20 @@ def dp_checkpoint_load(plan: int, directory: str, begin: int, end: int, restore_
 # ----------------------------------------------------------------------------
 # object wrapper
 # ----------------------------------------------------------------------------
+# plans that the interpreter finalised while a stream capture was under way
+_abandoned: list = []
+
+
+def _capturing() -> bool:
+    import torch
+    return torch.cuda.is_initialized() and torch.cuda.is_current_stream_capturing()
+
+
+def _destroy_abandoned() -> None:
+    while _abandoned and not _capturing():
+        dp_plan_destroy(_abandoned.pop())
+
+
 class Plan:
     """One plan over a ragged tensor list (see ``dpstep.h``)."""
 
@@ -460,6 +474,7 @@ class Plan:
         self.numel = tuple(int(x) for x in numel)
         self.n = int(n_replicas)
         self.grad_dtype, self.param_dtype = grad_dtype, param_dtype
+        _destroy_abandoned()
         self.handle = dp_plan_create(self.numel, self.n, grad_dtype, param_dtype, chunk_elems)
         self.P = int(sum(self.numel))
 
@@ -475,8 +490,15 @@ class Plan:
         self.close()
 
     def __del__(self):
+        # The garbage collector may run at any time, also within the capture of
+        # another plan's step, which the synchronisation and the frees of a
+        # destruction would invalidate: the handle waits for the next Plan then.
         try:
-            self.close()
+            if self.handle and _capturing():
+                _abandoned.append(self.handle)
+                self.handle = 0
+            else:
+                self.close()
         except Exception:
             pass
 

@@ -10,6 +10,8 @@ values that are each off by some (D + 60) 2^-24 of their magnitude; with D =
 magnitudes of n T terms of random sign is about sqrt(n T) = 16 times their
 sum.  1e-3 of a tensor's norm covers it; a lost term, scale or weight is of order
 one."""
+import gc
+
 import pytest
 import torch
 
@@ -179,3 +181,44 @@ def test_single_pass_and_partials_refuse():
         with pytest.raises(ValueError):
             d.step_layers(lambda *x: None)
         d.close()
+
+
+def test_a_plan_collected_within_a_capture_leaves_it_whole():
+    """The garbage collector destroys a plan that has device memory while another plan's call is captured."""
+    V, D, T = 16, 8, 40
+    g = torch.Generator().manual_seed(3)
+    ids, dy = torch.randint(0, V, (T,), generator=g).cuda(), torch.randn((T, D), generator=g).bfloat16().cuda()
+
+    def make():
+        p, acc = dp.Plan((V * D,), 1, "bf16", "bf16"), torch.full((V * D,), -7.0, device="cuda")
+        p.bind("acc", acc, 0)
+        return p, acc, torch.zeros(p.embed_workspace(0, D, T), dtype=torch.uint8, device="cuda")
+
+    plan, acc, ws = make()
+    stream = torch.cuda.Stream()
+    gc.collect()
+    gc.disable()
+    try:
+        old, other, other_ws = make()
+        old.accumulate_embed(0, [ids], [dy], True, other_ws)
+        plan.accumulate_embed(0, [ids], [dy], True, ws)
+        torch.cuda.synchronize()
+        want = acc.clone()
+        handle = old.handle
+        old.itself = old  # only the collector can free it
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            del old
+            gc.collect()
+            assert handle in dp._abandoned
+            plan.accumulate_embed(0, [ids], [dy], True, ws)
+    finally:
+        gc.enable()
+    for _ in range(3):
+        acc.fill_(-7.0)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(acc, want)
+    with dp.Plan((1,), 1):
+        assert dp._abandoned == []

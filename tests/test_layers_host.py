@@ -198,3 +198,16 @@ def test_linear_refusals(plan):
                dict(d=(5, 0, 1024, 1024), tokens=8192, ldc=1024, lds=32, ldd=1024, ws=None, n=size.value)):
         bad(lambda: call(**kw))
     refused(dp.DP_ERR_STATE, lambda: call(first=0))
+
+
+def test_a_plan_finalised_during_a_capture_is_destroyed_after_it(monkeypatch):
+    plan = dp.Plan((4,), 1)
+    handle = plan.handle
+    monkeypatch.setattr(dp, "_capturing", lambda: True)
+    plan.__del__()
+    assert plan.handle == 0 and dp._abandoned == [handle]
+    with dp.Plan((5,), 1):  # still within it
+        assert dp._abandoned == [handle]
+    monkeypatch.setattr(dp, "_capturing", lambda: False)
+    with dp.Plan((6,), 1):
+        assert dp._abandoned == []
