@@ -8,8 +8,8 @@
 // t gate w_post gives dy.  Column sums over the tokens: C = sum dx n(s) and E =
 // sum dx are the gradients of w_pre and b_pre.  With A = sum t n(y) and B =
 // sum t the others follow per column: dw_post = gate A, db_post = gate B, dgate
-// = w_post A + b_post B, so a thread keeps two sums per column (four with the
-// mean subtracted) instead of five.
+// = w_post A + b_post B, so a thread keeps four sums per column instead of
+// five; without biases and without the mean, where nothing takes E and B, two.
 //
 // Bound by HBM: four rows read and two written per token, all of them held in
 // registers as in the forward.  The sums of a row that do not depend on each
@@ -39,13 +39,13 @@ struct GradArgs {
 };
 
 // Column sums a workgroup leaves: C = sum dx n(s), A = sum t n(y) (t y without
-// a post norm), and with the mean subtracted E = sum dx, B = sum t.
-template <bool kCentered>
-constexpr int kSums = kCentered ? 4 : 2;
+// a post norm), and in the form with biases E = sum dx, B = sum t.
+template <bool kBias>
+constexpr int kSums = kBias ? 4 : 2;
 
-template <dp_dtype DT, dp_dtype PT, int NT, int NV, int VW, bool kCentered, bool kPost>
+template <dp_dtype DT, dp_dtype PT, int NT, int NV, int VW, bool kCentered, bool kBias, bool kPost>
 __global__ void __launch_bounds__(block_of(NT)) k_block_grad(GradArgs a) {
-    constexpr int kRows = block_of(NT) / NT, kStep = VW * NT, Q = kSums<kCentered>;
+    constexpr int kRows = block_of(NT) / NT, kStep = VW * NT, Q = kSums<kBias>;
     __shared__ float lds[sum_scratch(NT)];
     __shared__ float fold[kRows > 1 ? kRows - 1 : 1][kRows > 1 ? NT * VW * NV : 1];
     int turn = 0;
@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(block_of(NT)) k_block_grad(GradArgs a) {
                 for (int j = 0; j < VW; ++j) {
                     const float n = s[k][j] * r;
                     sum[0][k][j] += e[k][j] * n;
-                    if constexpr (kCentered) sum[2][k][j] += e[k][j];
+                    if constexpr (kBias) sum[2][k][j] += e[k][j];
                     t[k][j] += r * (e[k][j] * w[j] - mean_e - n * mean_en);
                 }
             }
@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(block_of(NT)) k_block_grad(GradArgs a) {
 #pragma unroll
             for (int j = 0; j < VW; ++j) f[j] = a.alpha * t[k][j];
             if (p.dh) store_n<DT, VW>(p.dh, row * a.ld + c, valid, f);
-            if constexpr (kCentered) {
+            if constexpr (kBias) {
 #pragma unroll
                 for (int j = 0; j < VW; ++j) sum[3][k][j] += j < valid ? t[k][j] : 0.0f;
             }
@@ -308,20 +308,20 @@ int64_t groups_of(int64_t dim, int64_t tokens, int n) {
     return want < most ? want : most;
 }
 
-template <dp_dtype DT, dp_dtype PT, bool kCentered, bool kPost>
+template <dp_dtype DT, dp_dtype PT, bool kCentered, bool kBias, bool kPost>
 void backward(const GradArgs& a, int groups, int n, hipStream_t stream) {
     const Shape sh = shape_of(a.dim);
     const dim3 grid(static_cast<unsigned>(groups), static_cast<unsigned>(n));
 #define GO(T, V, W) \
-    { hipLaunchKernelGGL((k_block_grad<DT, PT, T, V, W, kCentered, kPost>), grid, dim3(block_of(T)), 0, stream, a); }
+    { hipLaunchKernelGGL((k_block_grad<DT, PT, T, V, W, kCentered, kBias, kPost>), grid, dim3(block_of(T)), 0, stream, a); }
     DP_SHAPES(GO)
 #undef GO
 }
 
 }  // namespace
 
-size_t block_norm_workspace(int64_t dim, int64_t tokens, int n, bool centered) {
-    return static_cast<size_t>(4) * n * groups_of(dim, tokens, n) * (centered ? 4 : 2) * dim;
+size_t block_norm_workspace(const BlockNorm& b, int64_t tokens, int n) {
+    return static_cast<size_t>(4) * n * groups_of(b.dim, tokens, n) * (b.centered || b.bias ? 4 : 2) * b.dim;
 }
 
 hipError_t launch_block_grad(dp_dtype dt, dp_dtype pdt, const BlockNorm& b, int64_t tokens, int n,
@@ -339,7 +339,7 @@ hipError_t launch_block_grad(dp_dtype dt, dp_dtype pdt, const BlockNorm& b, int6
     const bool post = b.weight[0] != nullptr;
     const int groups = static_cast<int>(groups_of(b.dim, tokens, n));
     if (tokens > 0) {
-#define GO(D, P, C, O) backward<D, P, C, O>(a, groups, n, stream)
+#define GO(D, P, C, B, O) backward<D, P, C, B, O>(a, groups, n, stream)
         DP_KINDS(GO);
 #undef GO
         hipError_t e = hipGetLastError();
@@ -360,9 +360,10 @@ hipError_t launch_block_grad(dp_dtype dt, dp_dtype pdt, const BlockNorm& b, int6
     j.w = a.w;
     const dim3 grid(static_cast<unsigned>((b.dim + kJoinColumns - 1) / kJoinColumns), static_cast<unsigned>(n));
 #define GO(P, S) hipLaunchKernelGGL((k_block_join<P, S>), grid, dim3(kJoinColumns * kJoinLanes), 0, stream, j)
-    if (pdt == DP_BF16 && b.centered) GO(DP_BF16, 4);
+    const bool four = b.centered || b.bias;
+    if (pdt == DP_BF16 && four) GO(DP_BF16, 4);
     else if (pdt == DP_BF16) GO(DP_BF16, 2);
-    else if (b.centered) GO(DP_F16, 4);
+    else if (four) GO(DP_F16, 4);
     else GO(DP_F16, 2);
 #undef GO
     return hipGetLastError();

@@ -80,7 +80,9 @@ inline Weights weights_of(const BlockNorm& b) {
 }
 
 
-// Calls GO with the compile-time choices of a call: row type, weight type, mean, post norm.
+// Calls GO with the compile-time choices of a call: row type, weight type,
+// mean, biases, post norm.  Centred norms take the form with biases whether or not
+// they have any (an absent one reads as zero).
 #define DP_KINDS(GO)                                                        \
     do {                                                                    \
         if (dt == DP_F32 && pdt == DP_BF16) DP_KINDS2(GO, DP_F32, DP_BF16)  \
@@ -88,12 +90,14 @@ inline Weights weights_of(const BlockNorm& b) {
         else if (dt == DP_F16) DP_KINDS2(GO, DP_F16, DP_F16)                \
         else DP_KINDS2(GO, DP_BF16, DP_BF16)                                \
     } while (0)
-#define DP_KINDS2(GO, D, P)                           \
-    {                                                 \
-        if (b.centered && post) GO(D, P, true, true); \
-        else if (b.centered) GO(D, P, true, false);   \
-        else if (post) GO(D, P, false, true);         \
-        else GO(D, P, false, false);                  \
+#define DP_KINDS2(GO, D, P)                                   \
+    {                                                         \
+        if (b.centered && post) GO(D, P, true, true, true);   \
+        else if (b.centered) GO(D, P, true, true, false);     \
+        else if (b.bias && post) GO(D, P, false, true, true); \
+        else if (b.bias) GO(D, P, false, true, false);        \
+        else if (post) GO(D, P, false, false, true);          \
+        else GO(D, P, false, false, false);                   \
     }
 
 }  // namespace dpk

@@ -31,7 +31,7 @@ struct NormArgs {
     Weights w;
 };
 
-template <dp_dtype DT, dp_dtype PT, int NT, int NV, int VW, bool kCentered, bool kPost>
+template <dp_dtype DT, dp_dtype PT, int NT, int NV, int VW, bool kCentered, bool kBias, bool kPost>
 __global__ void __launch_bounds__(block_of(NT)) k_block_norm(NormArgs a) {
     constexpr int kRows = block_of(NT) / NT, kStep = VW * NT;
     __shared__ float lds[sum_scratch(NT)];
@@ -41,11 +41,11 @@ __global__ void __launch_bounds__(block_of(NT)) k_block_norm(NormArgs a) {
     const bool has_gate = a.w.gate != nullptr, has_x = a.x != nullptr;
     Column<PT, NV, VW> post_w, post_b, gate, pre_w, pre_b;
     if constexpr (kPost) post_w.load(a.w.post_w, c0, kStep, a.dim);
-    if constexpr (kPost && kCentered) post_b.load(a.w.post_b, c0, kStep, a.dim);
+    if constexpr (kPost && kBias) post_b.load(a.w.post_b, c0, kStep, a.dim);
     if (has_gate) gate.load(a.w.gate, c0, kStep, a.dim);
     if (has_x) {
         pre_w.load(a.w.pre_w, c0, kStep, a.dim);
-        if constexpr (kCentered) pre_b.load(a.w.pre_b, c0, kStep, a.dim);
+        if constexpr (kBias) pre_b.load(a.w.pre_b, c0, kStep, a.dim);
     }
     // a workgroup's rows: in every turn all its rows run (the last turn's
     // beyond the end are computed on zeros and not stored), so that barriers meet
@@ -100,9 +100,9 @@ __global__ void __launch_bounds__(block_of(NT)) k_block_norm(NormArgs a) {
             for (int k = 0; k < NV; ++k) {
                 float w[VW], b[VW];
                 expand<PT, VW>(post_w.q[k], w);
-                if constexpr (kCentered) expand<PT, VW>(post_b.q[k], b);
+                if constexpr (kBias) expand<PT, VW>(post_b.q[k], b);
 #pragma unroll
-                for (int j = 0; j < VW; ++j) u[k][j] = u[k][j] * r * w[j] + (kCentered ? b[j] : 0.0f);
+                for (int j = 0; j < VW; ++j) u[k][j] = u[k][j] * r * w[j] + (kBias ? b[j] : 0.0f);
             }
         }
 #pragma unroll
@@ -145,9 +145,9 @@ __global__ void __launch_bounds__(block_of(NT)) k_block_norm(NormArgs a) {
         for (int k = 0; k < NV; ++k) {
             float w[VW], b[VW];
             expand<PT, VW>(pre_w.q[k], w);
-            if constexpr (kCentered) expand<PT, VW>(pre_b.q[k], b);
+            if constexpr (kBias) expand<PT, VW>(pre_b.q[k], b);
 #pragma unroll
-            for (int j = 0; j < VW; ++j) h[k][j] = h[k][j] * r * w[j] + (kCentered ? b[j] : 0.0f);
+            for (int j = 0; j < VW; ++j) h[k][j] = h[k][j] * r * w[j] + (kBias ? b[j] : 0.0f);
             const int c = c0 + k * kStep;
             const int valid = row < a.tokens ? valid_of<VW>(a.dim, c) : 0;
             store_n<DT, VW>(a.x, row * a.ld_x + c, valid, h[k]);
@@ -170,13 +170,13 @@ Shape shape_of(int64_t dim) {
     else if (sh.nt == 256) GO(256, 2, 8)               \
     else GO(512, 2, 8)
 
-template <dp_dtype DT, dp_dtype PT, bool kCentered, bool kPost>
+template <dp_dtype DT, dp_dtype PT, bool kCentered, bool kBias, bool kPost>
 void forward(const NormArgs& a, hipStream_t stream) {
     const Shape sh = shape_of(a.dim);
     const int64_t rows = block_of(sh.nt) / sh.nt, want = (a.tokens + rows - 1) / rows;
     const dim3 grid(static_cast<unsigned>(want < 4096 ? want : 4096));
 #define GO(T, V, W) \
-    { hipLaunchKernelGGL((k_block_norm<DT, PT, T, V, W, kCentered, kPost>), grid, dim3(block_of(T)), 0, stream, a); }
+    { hipLaunchKernelGGL((k_block_norm<DT, PT, T, V, W, kCentered, kBias, kPost>), grid, dim3(block_of(T)), 0, stream, a); }
     DP_SHAPES(GO)
 #undef GO
 }
@@ -190,7 +190,7 @@ hipError_t launch_block_norm(dp_dtype dt, dp_dtype pdt, const BlockNorm& b, int6
     NormArgs a{h,    y,    s,     x, ld_h, ld_y, ld_s, ld_x, tokens, static_cast<int32_t>(b.dim), b.eps, b.alpha,
                weights_of(b)};
     const bool post = b.weight[0] != nullptr;
-#define GO(D, P, C, O) forward<D, P, C, O>(a, stream)
+#define GO(D, P, C, B, O) forward<D, P, C, B, O>(a, stream)
     DP_KINDS(GO);
 #undef GO
     return hipGetLastError();

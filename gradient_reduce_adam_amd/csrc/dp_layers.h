@@ -36,11 +36,12 @@ struct BlockNorm {
     int64_t dim;
     float eps, alpha;
     bool centered;
+    bool bias;  // post_b or pre_b is there
 };
 hipError_t launch_block_norm(dp_dtype dt, dp_dtype pdt, const BlockNorm& b, int64_t tokens, const void* h,
                              int64_t ld_h, const void* y, int64_t ld_y, void* s, int64_t ld_s, void* x, int64_t ld_x,
                              hipStream_t stream);
-size_t block_norm_workspace(int64_t dim, int64_t tokens, int n, bool centered);
+size_t block_norm_workspace(const BlockNorm& b, int64_t tokens, int n);  // reads dim, centered and bias
 // at[i]: which accumulator (acc[at * n + r], overwrite[at]) takes the gradient
 // of weight i, -1 for none.
 hipError_t launch_block_grad(dp_dtype dt, dp_dtype pdt, const BlockNorm& b, int64_t tokens, int n,

@@ -123,6 +123,7 @@ dp_status check_norms(const char* where, const dp_plan* plan, const dpl_norms* d
     out->b.eps = eps;
     out->b.alpha = alpha;
     out->b.centered = d->centered != 0;
+    out->b.bias = d->post_b >= 0 || d->pre_b >= 0;
     return DP_OK;
 }
 
@@ -282,7 +283,7 @@ dp_status dpl_block_norm_workspace(const dp_plan* plan, const dpl_norms* norms, 
     if (s == DP_OK) s = check_tokens("dpl_block_norm_workspace", tokens);
     if (s == DP_OK && !bytes) s = fail(DP_ERR_INVALID_ARG, "dpl_block_norm_workspace: null argument");
     if (s != DP_OK) return s;
-    *bytes = dpk::block_norm_workspace(n.b.dim, tokens, plan->n, n.b.centered);
+    *bytes = dpk::block_norm_workspace(n.b, tokens, plan->n);
     return DP_OK;
 }
 
@@ -318,7 +319,7 @@ dp_status dpl_accumulate_block_norm(dp_plan* plan, const dpl_norms* norms, int64
         if (tokens > 0 && ((p.dh && (p.dh == p.dy || p.dh == p.s || p.dh == p.y)) || (p.dy && p.dy == p.s)))
             return fail(DP_ERR_INVALID_ARG, "%s: outputs overlap each other, s or y", where);
     }
-    s = check_workspace(where, workspace, workspace_bytes, dpk::block_norm_workspace(n.b.dim, tokens, plan->n, n.b.centered));
+    s = check_workspace(where, workspace, workspace_bytes, dpk::block_norm_workspace(n.b, tokens, plan->n));
     if (s != DP_OK) return s;
     float* acc[5 * DP_MAX_REPLICAS];
     bool overwrite[5];
