@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sys
 from typing import Iterable, Optional, Sequence
 
 import numpy as np
@@ -457,8 +458,8 @@ _abandoned: list = []
 
 
 def _capturing() -> bool:
-    import torch
-    return torch.cuda.is_initialized() and torch.cuda.is_current_stream_capturing()
+    torch = sys.modules.get("torch")  # not there: no capture of torch's
+    return torch is not None and torch.cuda.is_initialized() and torch.cuda.is_current_stream_capturing()
 
 
 def _destroy_abandoned() -> None:

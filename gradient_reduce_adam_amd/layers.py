@@ -8,6 +8,7 @@ device that is current.  Arguments given per replica are sequences of the
 plan's ``n`` tensors.  A shape, type or device that does not fit raises
 ``ValueError``; what the library refuses raises :class:`DpError`.  ``plan`` is
 a :class:`Plan` (whose methods of the same purpose call these functions).
+Without torch the workspace queries work, and the other calls raise ImportError.
 """
 from __future__ import annotations
 
@@ -15,7 +16,10 @@ import ctypes
 from dataclasses import dataclass, field
 from typing import Optional, Sequence
 
-import torch
+try:
+    import torch
+except ImportError:
+    torch = None
 
 from . import DP_BF16, DP_F16, DP_F32, _check, lib
 
@@ -103,10 +107,15 @@ def _register() -> None:
 _register()
 
 
-_DTYPES = {torch.bfloat16: DP_BF16, torch.float16: DP_F16, torch.float32: DP_F32}
-_IDS = (torch.int32, torch.int64)
-# a launch costs the host about 4 us; the stream's handle without a Stream object saves 2 more
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+if torch is not None:
+    _DTYPES = {torch.bfloat16: DP_BF16, torch.float16: DP_F16, torch.float32: DP_F32}
+    _IDS = (torch.int32, torch.int64)
+    # a launch costs the host about 4 us; the stream's handle without a Stream object saves 2 more
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    _current_device = torch.cuda.current_device
+else:
+    def _current_device() -> int:
+        raise ImportError("the layer operators take torch tensors, and torch cannot be imported")
 
 
 def _stream_of(stream, device: int) -> int:
@@ -206,7 +215,7 @@ def _query(fn, *args) -> int:
 def dpl_embed(plan, tensor: int, ids, out, scale: float = 1.0, stream=None) -> None:
     """out[t] = scale * W[ids[t]] from plan tensor ``tensor``, rows of
     ``out.shape[1]`` parameters; zeros for an id outside the table."""
-    dev = torch.cuda.current_device()
+    dev = _current_device()
     size, tokens = _ids("ids", ids, dev), ids.shape[0]
     ld = _rows("out", out, dev, tokens)
     _check(lib.dpl_embed(plan.handle, ctypes.byref(Table(tensor, size, out.shape[1], scale)), tokens, ids.data_ptr(),
@@ -221,7 +230,7 @@ def dpl_accumulate_embed(plan, tensor: int, ids: Sequence, dy: Sequence, first: 
                          more: bool = False, stream=None) -> None:
     """The lookup's gradient from every replica's token ids and gradient rows,
     into the accumulators of plan tensor ``tensor``."""
-    dev = torch.cuda.current_device()
+    dev = _current_device()
     ids, dy = _replicas(plan, "ids", ids), _replicas(plan, "dy", dy)
     (tokens, dim) = dy[0].shape
     sizes = {_ids("ids", x, dev, tokens) for x in ids}
@@ -238,7 +247,7 @@ def dpl_accumulate_embed(plan, tensor: int, ids: Sequence, dy: Sequence, first: 
 def dpl_block_norm(plan, norms: BlockNorm, h, y, s, x=None, stream=None) -> None:
     """s = residual_scale * h + gate * N_post(y) and, with a norm before the
     next block, x = N_pre(s)."""
-    dev = torch.cuda.current_device()
+    dev = _current_device()
     (tokens, dim), dtype = h.shape, h.dtype
     ld_h, ld_y, ld_s = _rows("h", h, dev), _like("y", y, dev, h.shape, dtype), _like("s", s, dev, h.shape, dtype)
     ld_x, addr_x = (dim, None) if x is None else (_like("x", x, dev, h.shape, dtype), x.data_ptr())
@@ -257,7 +266,7 @@ def dpl_accumulate_block_norm(plan, norms: BlockNorm, s: Optional[Sequence], y: 
     """The backward from every replica's rows: dh, dy, and the gradients of
     the weights and the gate into the accumulators.  None for what is not there
     or not wanted."""
-    dev = torch.cuda.current_device()
+    dev = _current_device()
     given = [None if v is None else _replicas(plan, k, v)
              for k, v in (("s", s), ("y", y), ("dx", dx), ("ds", ds), ("dh", dh), ("dy", dy))]
     there = [t for v in given if v is not None for t in v]
@@ -278,7 +287,7 @@ def dpl_accumulate_block_norm(plan, norms: BlockNorm, s: Optional[Sequence], y: 
 def dpl_pack_activations(x, codes, scales, stream=None) -> None:
     """x [tokens, dim] as e4m3 bytes, codes [tokens, dim], and a scale byte for
     32 channels, scales [tokens, ceil(dim / 32)]."""
-    dev = torch.cuda.current_device()
+    dev = _current_device()
     ld = _rows("x", x, dev)
     tokens, dim = x.shape
     _check(lib.dpl_pack_activations(tokens, dim, _dtype(x), x.data_ptr(), ld, codes.data_ptr(),
@@ -289,7 +298,7 @@ def dpl_pack_activations(x, codes, scales, stream=None) -> None:
 
 def dpl_unpack_activations(codes, scales, x, stream=None) -> None:
     """The values that codes and scales stand for, into x."""
-    dev = torch.cuda.current_device()
+    dev = _current_device()
     ld = _rows("x", x, dev)
     tokens, dim = x.shape
     _check(lib.dpl_unpack_activations(tokens, dim, _dtype(x), codes.data_ptr(),
@@ -311,7 +320,7 @@ def dpl_accumulate_linear(plan, tensor: int, dy: Sequence, codes: Sequence, scal
     """A linear layer's weight gradient from every replica's output gradients
     dy [tokens, outputs] and packed inputs, into the accumulators of plan tensor
     ``tensor``: outputs x inputs, or inputs x outputs if ``transposed``."""
-    dev = torch.cuda.current_device()
+    dev = _current_device()
     dy, codes, scales = _replicas(plan, "dy", dy), _replicas(plan, "codes", codes), _replicas(plan, "scales", scales)
     ld_dy, ld_c, ld_s = _alike("dy", dy, dev), _alike("codes", codes, dev), _alike("scales", scales, dev)
     (tokens, outputs), inputs = dy[0].shape, codes[0].shape[1]

@@ -24,3 +24,40 @@ def test_norm_workspace_holds_the_sums_of_biases():
         for b in (dict(pre_b=1), dict(post_b=3), dict(pre_b=1, post_b=3, gate=4)):
             assert ask(False, **b) == full and ask(True, **b) == full
         assert ask(False, gate=4) == plain
+
+
+WITHOUT_TORCH = """
+import sys
+sys.modules["torch"] = None  # import torch raises ImportError
+import gradient_reduce_adam_amd as dp
+
+destroyed = []
+real = dp.dp_plan_destroy
+dp.dp_plan_destroy = lambda handle: (destroyed.append(handle), real(handle))
+p = dp.Plan((60, 10, 10), 1)
+norms = dp.BlockNorm(pre_w=1, pre_b=2, centered=True)
+assert p.embed_workspace(0, 6, 40) > 0 and p.linear_workspace(64, 6, 10, 0) == 0
+assert p.block_norm_workspace(norms, 10, 4) > 0
+for call in (lambda: p.embed(0, None, None), lambda: p.block_norm(norms, None, None, None),
+             lambda: p.accumulate_embed(0, [None], [None], True, None),
+             lambda: p.accumulate_block_norm(norms, None, None, None, None, None, None, True, None),
+             lambda: p.accumulate_linear(0, [None], [None], [None], True),
+             lambda: dp.dpl_pack_activations(None, None, None), lambda: dp.dpl_unpack_activations(None, None, None)):
+    try:
+        call()
+    except ImportError as e:
+        assert "torch" in str(e)
+    else:
+        raise AssertionError("no ImportError")
+handle = p.handle
+del p
+assert destroyed == [handle] and dp._abandoned == []
+print("fine")
+"""
+
+
+def test_the_package_works_without_torch():
+    """Without torch the package imports, plans and workspace queries work, a finalised plan is destroyed, and
+    the calls that take torch tensors say what they lack."""
+    r = subprocess.run([sys.executable, "-c", WITHOUT_TORCH], capture_output=True, text=True, cwd=ROOT, timeout=120)
+    assert r.returncode == 0 and "fine" in r.stdout, r.stderr
