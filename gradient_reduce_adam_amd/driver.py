@@ -375,10 +375,16 @@ class DPStep:
         return None
 
     def capture_layers(self, backward: LayerBackward) -> "StepGraph":
-        """Captures ``issue_layers`` (with the loss scale of now) into a HIP
-        graph on this step's stream, which must not be the null stream.  The
-        buffers that backward works on have to stay where they are while the
-        graph may replay, as do the workspaces of its calls."""
+        """Captures ``issue_layers`` into a HIP graph on this step's stream,
+        which must not be the null stream.  The buffers that backward works on
+        have to stay where they are while the graph may replay, as do the
+        workspaces of its calls.  The recorded backward pass keeps the loss
+        scale of now, while the update divides by the device's: a dynamic
+        scaler, which changes that one between replays, is refused, and a
+        checkpoint with another scale needs another capture."""
+        if self.scaler == "dynamic":
+            raise ValueError("a captured backward pass keeps its loss scale: capture_layers needs a scaler other than "
+                             "'dynamic'")
         if self.stream.cuda_stream == 0:
             raise ValueError("capture needs a non-default stream: pass stream=torch.cuda.Stream()")
         g = torch.cuda.CUDAGraph()

@@ -1,0 +1,56 @@
+"""The step driver's layer steps on the host: under which stream the caller's
+backward pass runs and what orders it, and what a capture refuses.  The step is
+assembled around stand-ins for the plan and the streams; nothing touches a
+GPU."""
+import contextlib
+
+import pytest
+
+driver = pytest.importorskip("gradient_reduce_adam_amd.driver")
+
+
+class Stream:
+    def __init__(self, name, log, handle):
+        self.name, self.log, self.cuda_stream = name, log, handle
+
+    def wait_stream(self, other):
+        self.log.append(f"{self.name} waits for {other.name}")
+
+
+class Plan:
+    def __init__(self, log):
+        self.log = log
+
+    def __getattr__(self, name):
+        return lambda *args, **kw: self.log.append(name)
+
+
+def step_on(monkeypatch, same=False, n=2, a=2, scaler="none"):
+    log = []
+    mine = Stream("step", log, 7)
+    current = [mine if same else Stream("caller", log, 0)]
+
+    @contextlib.contextmanager
+    def stream(s):
+        before, current[0] = current[0], s
+        yield
+        current[0] = before
+
+    monkeypatch.setattr(driver.torch.cuda, "stream", stream)
+    monkeypatch.setattr(driver.torch.cuda, "current_stream", lambda *device: current[0])
+    d = object.__new__(driver.DPStep)
+    d.n, d.a, d.partials, d.single_pass, d.offload = n, a, False, False, "direct"
+    d.lr, d.eps, d.weight_decay, d.max_norm = 1e-3, 1e-8, 0.0, 0.0
+    d.scaler, d.scale, d.steps_done = scaler, 1.0, 0
+    d.plan, d.stream, d.device, d.shards = Plan(log), mine, None, [(0, 4)]
+    return d, log, current
+
+
+def test_a_capture_under_a_dynamic_loss_scale_is_refused(monkeypatch):
+    """The recorded backward pass would keep the loss scale of the capture, while the update divides by the
+    device's, which an overflow or a growth interval changes."""
+    d, log, _ = step_on(monkeypatch, scaler="dynamic")
+    monkeypatch.setattr(driver.torch.cuda, "CUDAGraph", lambda: pytest.fail("a capture began"))
+    with pytest.raises(ValueError, match="dynamic"):
+        d.capture_layers(lambda *args: log.append("backward"))
+    assert log == []
