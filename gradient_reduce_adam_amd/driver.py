@@ -55,7 +55,7 @@ GradProducer = Callable[[int, int, int, float], int]
 RangeProducer = Callable[[int, int, int, int, int], None]
 
 # backward(step, micro, first, loss_scale): runs every replica's backward pass of
-# that micro-step and accumulates every tensor's gradient
+# that micro-step, on the current stream, and accumulates every tensor's gradient
 LayerBackward = Callable[[int, int, bool, float], None]
 
 
@@ -352,17 +352,27 @@ class DPStep:
     def issue_layers(self, backward: LayerBackward, step: int) -> None:
         """One whole step whose micro-steps' gradients are written into the
         accumulators by ``backward(step, k, first, scale)``: for every replica
-        it runs the backward pass of micro-step k on this step's stream, under
-        the loss scale, and issues the ``accumulate_*`` calls (with that first
-        flag) that together cover every tensor.  No host synchronisation: the
-        form a graph can capture, once one step has run."""
+        it runs the backward pass of micro-step k under the loss scale, and
+        issues the ``accumulate_*`` calls (with that first flag) that together
+        cover every tensor.  It is called with this step's stream current, so
+        what it issues without naming a stream goes there.  The step comes after
+        what the caller's current stream holds, and that stream's later work
+        after the step.  No host synchronisation: the form a graph can capture,
+        once one step has run."""
         if self.partials or self.single_pass:
             raise ValueError("layer operators write accumulators: no incoming partials, and the two-pass update")
-        for k in range(1, self.a + 1):
-            backward(step, k, k == 1, self.scale)
-        if self.n > 1:
-            self.plan.reduce_replicas("acc", stream=self.stream.cuda_stream)
-        self.finish(scan=self.n == 1)  # with one replica g_bar is its accumulator
+        caller = torch.cuda.current_stream(self.device)
+        elsewhere = caller.cuda_stream != self.stream.cuda_stream
+        if elsewhere:
+            self.stream.wait_stream(caller)
+        with torch.cuda.stream(self.stream):
+            for k in range(1, self.a + 1):
+                backward(step, k, k == 1, self.scale)
+            if self.n > 1:
+                self.plan.reduce_replicas("acc", stream=self.stream.cuda_stream)
+            self.finish(scan=self.n == 1)  # with one replica g_bar is its accumulator
+        if elsewhere:
+            caller.wait_stream(self.stream)
 
     def step_layers(self, backward: LayerBackward, sync_scale: bool = True) -> Optional[dict]:
         """``issue_layers`` as one step."""

@@ -54,3 +54,20 @@ def test_a_capture_under_a_dynamic_loss_scale_is_refused(monkeypatch):
     with pytest.raises(ValueError, match="dynamic"):
         d.capture_layers(lambda *args: log.append("backward"))
     assert log == []
+
+
+def test_backward_runs_on_the_steps_stream_in_the_callers_order(monkeypatch):
+    """The calls of a backward pass that names no stream go to the step's stream, behind what the caller issued
+    before the step; what the caller issues after it waits for the step."""
+    d, log, current = step_on(monkeypatch)
+    d.issue_layers(lambda step, k, first, scale: log.append(f"backward {k} on {current[0].name}"), 1)
+    assert log == ["step waits for caller", "backward 1 on step", "backward 2 on step", "reduce_replicas",
+                   "grad_stats", "adam_step", "caller waits for step"]
+    assert current[0].name == "caller"
+
+
+def test_a_step_on_the_current_stream_waits_for_nothing(monkeypatch):
+    """Also the form that a capture on the step's stream records: no stream waits for itself."""
+    d, log, current = step_on(monkeypatch, same=True, n=1, a=1)
+    d.issue_layers(lambda step, k, first, scale: log.append(f"backward {k} on {current[0].name}"), 1)
+    assert log == ["backward 1 on step", "grad_stats", "adam_step"]
