@@ -464,7 +464,11 @@ def _capturing() -> bool:
 
 def _destroy_abandoned() -> None:
     while _abandoned and not _capturing():
-        dp_plan_destroy(_abandoned.pop())
+        try:
+            handle = _abandoned.pop()
+        except IndexError:  # another thread was faster
+            return
+        dp_plan_destroy(handle)
 
 
 class Plan:
@@ -483,6 +487,7 @@ class Plan:
         if self.handle:
             dp_plan_destroy(self.handle)
             self.handle = 0
+        _destroy_abandoned()
 
     def __enter__(self):
         return self
@@ -492,8 +497,9 @@ class Plan:
 
     def __del__(self):
         # The garbage collector may run at any time, also within the capture of
-        # another plan's step, which the synchronisation and the frees of a
-        # destruction would invalidate: the handle waits for the next Plan then.
+        # another plan's step.  There the handle waits for the next call that
+        # makes a plan, closes one or reads a state.  Captures that this thread's
+        # current stream is no part of are left whole by the destruction itself.
         try:
             if self.handle and _capturing():
                 _abandoned.append(self.handle)
@@ -564,7 +570,9 @@ class Plan:
         dp_reduce_adam_finish(self.handle, stream)
 
     def read_state(self, stream=None) -> dict:
-        return dp_read_state(self.handle, stream)
+        state = dp_read_state(self.handle, stream)
+        _destroy_abandoned()
+        return state
 
     def checkpoint_save(self, directory: str, generation: int, begin: int = 0, end: Optional[int] = None,
                         stream=None) -> None:

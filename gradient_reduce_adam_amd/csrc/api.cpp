@@ -524,14 +524,28 @@ dp_status dp_plan_create(const dp_layout* L, dp_plan** out) {
     return DP_OK;
 }
 
+// A binding's garbage collector may destroy a plan at any time, also while this
+// thread or another one captures a stream.  hipDeviceSynchronize invalidates such a
+// capture in every capture mode; frees leave it whole once the thread is in the
+// relaxed mode, and each of them waits for the device's work, which here is what
+// drains the plan's launches (checked on ROCm 7: a free behind a running kernel
+// returns when the kernel has ended, within a capture too).
 dp_status dp_plan_destroy(dp_plan* p) {
     if (!p) return DP_OK;
     if (p->device >= 0) {
-        // free on the plan's device, after its work has drained
         int cur = -1;
         const bool switched = hipGetDevice(&cur) == hipSuccess && cur != p->device &&
                               hipSetDevice(p->device) == hipSuccess;
-        (void)hipDeviceSynchronize();
+        hipStreamCaptureMode mode = hipStreamCaptureModeRelaxed;
+        const bool exchanged = hipThreadExchangeStreamCaptureMode(&mode) == hipSuccess;
+        // the wait, also of a plan that owns no memory
+        void* piece = nullptr;
+        if (hipMalloc(&piece, 256) == hipSuccess) {
+            (void)hipFree(piece);
+        } else {
+            (void)hipGetLastError();
+            (void)hipDeviceSynchronize();
+        }
         for (auto& row : p->roles)
             for (auto& b : row) free_ring(b);
         for (hipEvent_t ev : p->events.ev) (void)hipEventDestroy(ev);
@@ -541,6 +555,7 @@ dp_status dp_plan_destroy(dp_plan* p) {
         if (p->stats.bad) (void)hipFree(p->stats.bad);
         if (p->fold.sumsq) (void)hipFree(p->fold.sumsq);
         if (p->fold.bad) (void)hipFree(p->fold.bad);
+        if (exchanged) (void)hipThreadExchangeStreamCaptureMode(&mode);
         if (switched) (void)hipSetDevice(cur);
     }
     delete p;

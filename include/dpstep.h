@@ -187,7 +187,9 @@ const char* dp_last_error(void);
 dp_status dp_plan_create(const dp_layout* layout, dp_plan** out);
 
 /* Frees the library's device memory (tables, partials, state) and the plan.
- * Synchronises the plan's device first.  Null is accepted. */
+ * Waits for the work of the plan's device first.  A stream capture that is under
+ * way meanwhile, of this thread or of another, stays valid (one that has
+ * recorded calls on this plan must not be replayed).  Null is accepted. */
 dp_status dp_plan_destroy(dp_plan* plan);
 
 dp_status dp_plan_info_get(const dp_plan* plan, dp_plan_info* out);

@@ -61,3 +61,34 @@ def test_the_package_works_without_torch():
     the calls that take torch tensors say what they lack."""
     r = subprocess.run([sys.executable, "-c", WITHOUT_TORCH], capture_output=True, text=True, cwd=ROOT, timeout=120)
     assert r.returncode == 0 and "fine" in r.stdout, r.stderr
+
+
+def test_an_abandoned_plan_that_another_thread_destroys_first(monkeypatch):
+    """Between the look at the list and the pop another thread may have emptied it."""
+    monkeypatch.setattr(dp, "_abandoned", [0])
+
+    def other_thread():
+        dp._abandoned.clear()
+        return False
+
+    monkeypatch.setattr(dp, "_capturing", other_thread)
+    with dp.Plan((4,), 1) as p:
+        assert p.handle
+
+
+def test_abandoned_plans_are_destroyed_at_the_next_call_that_synchronises(monkeypatch):
+    """Not only where another plan is made: closing a plan and reading its state do it too."""
+    destroyed = []
+    monkeypatch.setattr(dp, "_abandoned", [])
+    monkeypatch.setattr(dp, "_capturing", lambda: False)
+    monkeypatch.setattr(dp, "dp_read_state", lambda handle, stream: {"t": 3})
+    plan, other = dp.Plan((4,), 1), dp.Plan((5,), 1)
+    real = dp.dp_plan_destroy
+    monkeypatch.setattr(dp, "dp_plan_destroy", lambda h: (destroyed.append(h), real(h)))
+    for call in (lambda: plan.read_state(), lambda: plan.close()):
+        h = dp.dp_plan_create((6,), 1, "bf16", "bf16")
+        dp._abandoned.append(h)
+        call()
+        assert h in destroyed and dp._abandoned == []
+    other.close()
+    assert len(destroyed) == 4
