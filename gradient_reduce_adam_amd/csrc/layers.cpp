@@ -266,7 +266,7 @@ dp_status dpl_block_norm(dp_plan* plan, const dpl_norms* norms, int64_t tokens, 
     if (s == DP_OK && has_x) s = check_rows(where, "x", x, tokens, n.b.dim, ld_x, e);
     if (s != DP_OK) return s;
     if (!has_x && x) return fail(DP_ERR_INVALID_ARG, "%s: x without a norm before the next block", where);
-    if ((s_out == h && ld_s != ld_h) || (s_out == y && ld_s != ld_y))
+    if (tokens > 1 && ((s_out == h && ld_s != ld_h) || (s_out == y && ld_s != ld_y)))
         return fail(DP_ERR_INVALID_ARG, "%s: s in place of an input needs its row stride", where);
     if (tokens > 0 && x && (x == h || x == y || x == s_out))
         return fail(DP_ERR_INVALID_ARG, "%s: x must not overlap another tensor", where);

@@ -124,3 +124,16 @@ def test_a_bias_moves_in_a_whole_step():
     moved = d.master != start
     assert moved[D:2 * D].float().mean() > 0.9 and moved[3 * D:4 * D].float().mean() > 0.9
     d.close()
+
+
+def test_one_row_in_place_under_any_stride():
+    """A single row has no stride: s in place of h may be given another one."""
+    g = torch.Generator().manual_seed(6)
+    D = 40
+    s = Setup(D, 1, ("pre_w", "post_w"), "bf16", "bf16", g, False, 0.5)
+    h, y = (torch.randn((1, D), generator=g).bfloat16().cuda() for _ in range(2))
+    out, x, x2 = (torch.zeros_like(h) for _ in range(3))
+    s.plan.block_norm(s.norms, h, y, out, x)
+    dp._check(dp.lib.dpl_block_norm(s.plan.handle, s.norms.ref(D), 1, dp.DP_BF16, h.data_ptr(), D, y.data_ptr(), D,
+                                    h.data_ptr(), D + 8, x2.data_ptr(), D, torch.cuda.current_stream().cuda_stream))
+    assert torch.equal(h, out) and torch.equal(x, x2)

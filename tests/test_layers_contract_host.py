@@ -92,3 +92,13 @@ def test_abandoned_plans_are_destroyed_at_the_next_call_that_synchronises(monkey
         assert h in destroyed and dp._abandoned == []
     other.close()
     assert len(destroyed) == 4
+
+
+def test_block_norm_of_no_rows_takes_any_strides():
+    """Without rows the addresses may all be null, which makes s no tensor in place of h or y."""
+    with dp.Plan((8, 8), 1) as plan:
+        plan.bind("param", 1 << 20)
+        norms = ctypes.byref(L.Norms(-1, -1, -1, 0, -1, 0, 8, 1e-5, 1.0))
+        for lds in (8, 9):
+            status = dp.lib.dpl_block_norm(plan.handle, norms, 0, dp.DP_BF16, None, 8, None, 8, None, lds, None, 8, None)
+            assert status != dp.DP_ERR_INVALID_ARG, dp.lib.dp_last_error()
