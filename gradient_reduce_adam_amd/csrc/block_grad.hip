@@ -17,7 +17,11 @@
 // of a workgroup go to the workspace, and a second launch adds the
 // workgroups' sums in a fixed order, so the bits depend on the sizes alone.
 // 8191 rows of 4096 f16 with both norms and the gate take 83 us, 4.8 TB/s, and
-// the second launch 7 us.
+// the second launch 7 us.  With biases, four sums instead of two, 8192 bf16 rows of
+// 4096 take 98 us with the second launch instead of 92, and 113 with the mean
+// subtracted.  Beyond 4096 elements four sums of a thread's 16 columns do not fit
+// 256 registers: 8192 bf16 rows of 8192 take 171 us with two sums, 400 with four (35
+// registers spilled), 463 with the mean (39).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -279,7 +283,8 @@ __global__ void __launch_bounds__(kJoinColumns* kJoinLanes) k_block_join(JoinArg
 // centred, bf16: 128 threads with 8 elements each took 112 us, one wave with 2 x
 // 8 took 94 us and with 3 x 4 (every lane busy, 196 registers) 77 us; forcing a
 // third wave a SIMD spilled 29 registers and took 92 to 114 us.  Without
-// branches around its loads the last form takes 57 us, 5.3 TB/s.
+// branches around its loads the last form takes 57 us, 4.4 TB/s of the five
+// rows a token that it moves (y is read only for a post norm or a gate).
 Shape shape_of(int64_t dim) {
     if (dim <= 512) return {64, 1, 8};
     if (dim <= 768) return {64, 3, 4};

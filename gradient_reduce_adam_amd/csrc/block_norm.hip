@@ -10,7 +10,9 @@
 // barrier.  A workgroup keeps the weights of its columns in registers, walks
 // over rows, and loads the next row before it computes the current one.  16384
 // rows of 4096 f16 with both norms and the gate take 101 us, 5.3 TB/s; rows of
-// 4095, which start at any element, 1.25 times as long.
+// 4095, which start at any element, 1.25 times as long.  With biases 8192 bf16 rows
+// of 4096 take 53 us instead of 51, with the mean subtracted 55; rows of 8192 97, 111
+// and 131 us.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -375,7 +375,8 @@ class DPStep:
             caller.wait_stream(self.stream)
 
     def step_layers(self, backward: LayerBackward, sync_scale: bool = True) -> Optional[dict]:
-        """``issue_layers`` as one step."""
+        """``issue_layers`` as one step.  Without sync_scale the host keeps its
+        loss scale, which has to be the device's: not under a dynamic scaler."""
         self.steps_done += 1
         self.issue_layers(backward, self.steps_done)
         if sync_scale:

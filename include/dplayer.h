@@ -20,9 +20,12 @@
  * call's buckets, take the same first flag (DP_ERR_INVALID_ARG) and do not
  * overlap them (DP_ERR_STATE); the micro-step is complete once all together
  * cover [0, P).  A tensor whose gradient is a sum of several calls (a table
- * tied to the output layer) takes more != 0 in all of them but the last: such
- * a call writes or adds its term and leaves the tensor uncovered, and the
- * next call on it adds.  The caller orders the calls on one tensor.  After the
+ * looked up twice, or tied to a linear layer whose input is packed) takes more
+ * != 0 in all of them but the last: such a call writes or adds its term and
+ * leaves the tensor uncovered, and the next call on it adds.  Every term is a
+ * dpl_accumulate_* call: a dense gradient buffer (dp_accumulate_all_range) covers
+ * its tensors alone and is refused on one with terms still to come
+ * (DP_ERR_STATE).  The caller orders the calls on one tensor.  After the
  * last micro-step the accumulators go on to dp_reduce_replicas(DP_ROLE_ACC)
  * (with one replica and g_bar its accumulator, to dp_grad_stats(scan = 1)).
  *
@@ -154,7 +157,9 @@ dp_status dpl_accumulate_block_norm(dp_plan* plan, const dpl_norms* norms, int64
  * group's largest finite magnitude is at most 448, so that a bf16 holds every
  * value exactly.  Codes are rounded to nearest even: a relative error of at
  * most 2^-4 for magnitudes from 2^-6 * 2^e, and an absolute one of 2^-10 * 2^e
- * below.  An infinity or NaN becomes NaN, so the step's check still finds it.
+ * below.  Magnitudes beyond 448 * 2^119, which DP_F32 and DP_BF16 rows may hold, are
+ * limited to it, an eighth below the largest of them.  An infinity or NaN
+ * becomes NaN, so the step's check still finds it.
  * DP_F16 sources are first limited to +-61440, so that an f16 holds the
  * decoded value exactly too.
  *
@@ -187,9 +192,10 @@ dp_status dpl_linear_workspace(const dp_plan* plan, const dpl_linear* linear, in
 
 /* The weight gradient from the packed input:
  *   G_r[o][i] = sum_t dy[r][t][o] * x[r][t][i]
- * with x decoded to dtype (DP_BF16 or DP_F16, dy's; a value beyond f16's range
- * becomes an infinity there), products exact and sums in binary32.  rows: host
- * array [n_replicas]. */
+ * with x decoded to dtype (DP_BF16 or DP_F16, dy's), products exact and sums in
+ * binary32.  DP_BF16 holds every decoded value; DP_F16 holds those of rows packed
+ * from DP_F16, and others are rounded to it, to nearest even, beyond its range to
+ * an infinity.  rows: host array [n_replicas]. */
 dp_status dpl_accumulate_linear(dp_plan* plan, const dpl_linear* linear, int64_t tokens, dp_dtype dtype,
                                 const dpl_linear_rows* rows, int64_t ld_codes, int64_t ld_scales, int64_t ld_dy,
                                 int32_t first, int32_t more, void* workspace, size_t workspace_bytes,
