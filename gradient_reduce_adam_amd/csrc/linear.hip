@@ -18,8 +18,8 @@
 //    bits (slot ^ (token & 3)), which spreads every fragment read over all
 //    banks.
 // The matrix cores bound it, at the clock that they sustain (1.9 of 2.4 GHz):
-// 11008 x 4096 weights from 8192 tokens take 628 to 654 us on different cards,
-// 1130 to 1175 TFLOP/s, with the matrix pipes busy 67% of the time that the CUs
+// 11008 x 4096 weights from 8192 tokens take 628 to 704 us on different cards,
+// 1050 to 1175 TFLOP/s, with the matrix pipes busy 67% of the time that the CUs
 // are; the LDS reads (192 KiB a step, against 8.4 MFLOP) come next.
 //
 // Few tiles and many tokens leave CUs idle, so the token axis is then split

@@ -11,7 +11,8 @@ pytestmark = pytest.mark.gpu
 CASES = [
     # V, D, T, kinds of the replicas' ids, dtype, id type, pad, offset, per-tensor bindings
     (70000, 4, 20000, ("text", "reverse", "wild"), "bf16", torch.int64, 0, 4, False),   # three passes
-    (300, 8, 70001, ("text", "same"), "f16", torch.int32, 0, 4, False),                 # two passes
+    (300, 8, 70001, ("text", "sorted"), "f16", torch.int32, 0, 4, False),               # two passes
+    (300, 2, 17000, ("same", "text"), "bf16", torch.int32, 0, 2, False),                # one run through every chunk
     (255, 5, 16385, ("sorted", "text", "none", "reverse"), "f32", torch.int64, 3, 3, True),  # one pass
     (65536, 3, 40000, ("reverse", "text"), "bf16", torch.int32, 1, 1, False),
     ((1 << 24) + 3, 1, 17000, ("text", "reverse"), "f16", torch.int64, 0, 0, False),    # four passes
