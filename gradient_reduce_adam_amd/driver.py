@@ -358,21 +358,23 @@ class DPStep:
         what it issues without naming a stream goes there.  The step comes after
         what the caller's current stream holds, and that stream's later work
         after the step.  No host synchronisation: the form a graph can capture,
-        once one step has run."""
+        once one step has run and with a loss scale that stays."""
         if self.partials or self.single_pass:
             raise ValueError("layer operators write accumulators: no incoming partials, and the two-pass update")
         caller = torch.cuda.current_stream(self.device)
         elsewhere = caller.cuda_stream != self.stream.cuda_stream
         if elsewhere:
             self.stream.wait_stream(caller)
-        with torch.cuda.stream(self.stream):
-            for k in range(1, self.a + 1):
-                backward(step, k, k == 1, self.scale)
-            if self.n > 1:
-                self.plan.reduce_replicas("acc", stream=self.stream.cuda_stream)
-            self.finish(scan=self.n == 1)  # with one replica g_bar is its accumulator
-        if elsewhere:
-            caller.wait_stream(self.stream)
+        try:
+            with torch.cuda.stream(self.stream):
+                for k in range(1, self.a + 1):
+                    backward(step, k, k == 1, self.scale)
+                if self.n > 1:
+                    self.plan.reduce_replicas("acc", stream=self.stream.cuda_stream)
+                self.finish(scan=self.n == 1)  # with one replica g_bar is its accumulator
+        finally:  # a step that failed half way may still read the caller's buffers
+            if elsewhere:
+                caller.wait_stream(self.stream)
 
     def step_layers(self, backward: LayerBackward, sync_scale: bool = True) -> Optional[dict]:
         """``issue_layers`` as one step.  Without sync_scale the host keeps its

@@ -33,8 +33,10 @@ def step_on(monkeypatch, same=False, n=2, a=2, scaler="none"):
     @contextlib.contextmanager
     def stream(s):
         before, current[0] = current[0], s
-        yield
-        current[0] = before
+        try:
+            yield
+        finally:
+            current[0] = before
 
     monkeypatch.setattr(driver.torch.cuda, "stream", stream)
     monkeypatch.setattr(driver.torch.cuda, "current_stream", lambda *device: current[0])
@@ -71,3 +73,17 @@ def test_a_step_on_the_current_stream_waits_for_nothing(monkeypatch):
     d, log, current = step_on(monkeypatch, same=True, n=1, a=1)
     d.issue_layers(lambda step, k, first, scale: log.append(f"backward {k} on {current[0].name}"), 1)
     assert log == ["backward 1 on step", "grad_stats", "adam_step"]
+
+
+def test_the_caller_waits_for_a_step_that_failed_half_way(monkeypatch):
+    """Its buffers may still be read on the step's stream when the exception reaches it."""
+    d, log, current = step_on(monkeypatch)
+
+    def backward(step, k, first, scale):
+        if k == 2:
+            raise RuntimeError("lost")
+        log.append("backward")
+
+    with pytest.raises(RuntimeError, match="lost"):
+        d.issue_layers(backward, 1)
+    assert log == ["step waits for caller", "backward", "caller waits for step"] and current[0].name == "caller"
