@@ -617,3 +617,6 @@ class Plan:
 from .layers import (BlockNorm, dpl_accumulate_block_norm, dpl_accumulate_embed,  # noqa: E402
                      dpl_accumulate_linear, dpl_block_norm, dpl_block_norm_workspace, dpl_embed,
                      dpl_embed_workspace, dpl_linear_workspace, dpl_pack_activations, dpl_unpack_activations)
+from .attention import (Attention, Rotary, dpa_attention, dpa_attention_backward,  # noqa: E402
+                        dpa_attention_workspace, dpa_rotary)
+from .distill import Distillation, dpd_distill  # noqa: E402

@@ -18,7 +18,8 @@ HIP_FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
 
 
 SOURCES = ("kernels.hip", "api.cpp", "checkpoint.cpp", "noalloc.hip", "layers.cpp", "embed.hip",
-           "block_norm.hip", "block_grad.hip", "act8.hip", "linear.hip")
+           "block_norm.hip", "block_grad.hip", "act8.hip", "linear.hip", "attention.cpp", "rotary.hip", "attention.hip",
+           "attention_grad.hip", "loss.cpp", "distill.hip")
 
 
 def _run(cmd):

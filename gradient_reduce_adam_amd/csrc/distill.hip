@@ -1,0 +1,317 @@
+// gfx950 kernel of the distillation loss and its gradient, a workgroup for each row
+// of logits.
+//
+// The gradient needs the sums over the whole row, so the row stays in registers
+// between the two (50257 logits of 16 bits are 28 registers of 1024 threads) and
+// is read from memory once: read, greatest logit, sums, gradient, write.  The
+// teacher's list is gathered beside it into LDS, with a bit for each token of the list,
+// by which the sums leave these tokens out of the rest.  The gradient is written as
+// if no token were listed; then the listed ones and the label are written again.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "dp_attention.h"
+#include "dp_device.h"
+
+namespace dpk {
+namespace {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kInf = __builtin_inff();
+
+__device__ __forceinline__ float wave_max(float x) {
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) x = fmaxf(x, __shfl_xor(x, m));
+    return x;
+}
+
+__device__ __forceinline__ float load_any(dp_dtype dt, const void* p, int64_t i) {
+    return dt == DP_F32 ? load1<DP_F32>(p, i) : dt == DP_F16 ? load1<DP_F16>(p, i) : load1<DP_BF16>(p, i);
+}
+__device__ __forceinline__ int64_t load_id(int bytes, const void* p, int64_t i) {
+    return bytes == 4 ? gload<int32_t>(p, i) : gload<int64_t>(p, i);
+}
+
+// One row's logits in pieces of 16 bytes at aligned addresses: piece i holds the
+// logits kN i - shift + 0 .. kN - 1, those outside the row as -infinity.
+template <dp_dtype DT>
+struct Row {
+    static constexpr int kN = DT == DP_F32 ? 4 : 8;
+    const char* p;
+    int shift, vocab, pieces;
+
+    __device__ __forceinline__ Row(const void* logits, int64_t row, int64_t ld, int64_t v) {
+        constexpr int kSize = DT == DP_F32 ? 4 : 2;
+        p = static_cast<const char*>(logits) + row * ld * kSize;
+        shift = static_cast<int>(reinterpret_cast<uintptr_t>(p) / kSize % kN);
+        vocab = static_cast<int>(v);
+        pieces = (vocab + shift + kN - 1) / kN;
+    }
+    __device__ __forceinline__ Raw<DT, kN> load(int i) const {
+        Raw<DT, kN> q;
+        const int at = i * kN - shift;
+        if (at >= 0 && at + kN <= vocab) {
+            const u32x4 v = gload<u32x4>(p + static_cast<int64_t>(at) * (16 / kN), 0);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) q.w[j] = v[j];
+        } else {
+            float x[kN];
+#pragma unroll
+            for (int j = 0; j < kN; ++j) x[j] = at + j >= 0 && at + j < vocab ? load1<DT>(p, at + j) : -kInf;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                q.w[j] = DT == DP_F32 ? __builtin_bit_cast(unsigned int, x[j * kN / 4])
+                                      : pack2<DT == DP_F32 ? DP_BF16 : DT>(x[j * kN / 4], x[j * kN / 4 + kN / 8]);
+        }
+        return q;
+    }
+    __device__ __forceinline__ void store(void* out, int i, const float* x) const {
+        const int at = i * kN - shift;
+        if (at >= 0 && at + kN <= vocab) {
+            store_n<DT, kN, true>(out, at, kN, x);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kN; ++j)
+                if (at + j >= 0 && at + j < vocab) store1<DT>(out, at + j, x[j]);
+        }
+    }
+};
+
+// kKept pieces of a row in a thread's registers; 0: the row is read for each pass.
+template <dp_dtype DT, int kThreads, int kKept>
+__global__ void __launch_bounds__(kThreads) k_distill(DistillArgs a, dp_dtype teacher_dt) {
+    using R = Row<DT>;
+    constexpr int kN = R::kN, kWaves = kThreads / 64, kSums = 5;
+    extern __shared__ unsigned int dyn[];
+    __shared__ float tops[2][kWaves], sums[kSums][kWaves];
+    const int K = a.top, tid = threadIdx.x;
+    int* const ids = reinterpret_cast<int*>(dyn);                   // -1: not in the list
+    float* const teacher = reinterpret_cast<float*>(dyn + K);       // y / tau, then p
+    float* const student = reinterpret_cast<float*>(dyn + 2 * K);   // the logit
+    unsigned int* const bits = dyn + 3 * K;                         // of token v at v + shift
+
+    const int64_t t = blockIdx.x;
+    const float weight = a.weight ? gload<float>(a.weight, t) : 1.0f;
+    const R row(a.logits, t, a.ld, a.vocab);
+    constexpr int kSize = DT == DP_F32 ? 4 : 2;
+    char* const out = a.dlogits ? static_cast<char*>(a.dlogits) + t * a.ld_dlogits * kSize : nullptr;
+    if (weight == 0.0f) {
+        if (a.loss && tid == 0) gstore<float>(a.loss, t, 0.0f);
+        float x[kN];
+#pragma unroll
+        for (int j = 0; j < kN; ++j) x[j] = 0.0f;
+        if (out)
+            for (int i = tid; i < row.pieces; i += kThreads) row.store(out, i, x);
+        return;
+    }
+
+    // 1. the row, the list, and the greatest of both
+    Raw<DT, kN> kept[kKept > 0 ? kKept : 1];
+#pragma unroll
+    for (int k = 0; k < kKept; ++k)
+        if (k * kThreads + tid < row.pieces) kept[k] = row.load(k * kThreads + tid);
+    const auto each = [&](auto&& use) {  // use(piece, its logits)
+        if constexpr (kKept > 0) {
+#pragma unroll
+            for (int k = 0; k < kKept; ++k) {
+                if (k * kThreads + tid < row.pieces) {
+                    float x[kN];
+                    expand<DT, kN>(kept[k], x);
+                    use(k * kThreads + tid, x);
+                }
+            }
+        } else {
+            for (int i = tid; i < row.pieces; i += kThreads) {
+                float x[kN];
+                expand<DT, kN>(row.load(i), x);
+                use(i, x);
+            }
+        }
+    };
+    for (int i = tid; i < (row.vocab + row.shift + 31) / 32; i += kThreads) bits[i] = 0;
+    const float heat = 1.0f / a.temperature;
+    float top = -kInf, list = -kInf;
+    for (int k = tid; k < K; k += kThreads) {
+        const int64_t id = load_id(a.id_bytes, a.ids, t * a.ld_ids + k);
+        const bool there = id >= 0 && id < a.vocab;
+        const float y = there ? load_any(teacher_dt, a.teacher, t * a.ld_teacher + k) * heat : -kInf;
+        ids[k] = there ? static_cast<int>(id) : -1;
+        teacher[k] = y;
+        student[k] = there ? load1<DT>(row.p, id) : 0.0f;
+        list = fmaxf(list, y);
+    }
+    each([&](int, const float* x) {
+#pragma unroll
+        for (int j = 0; j < kN; ++j) top = fmaxf(top, x[j]);
+    });
+    top = wave_max(top);
+    list = wave_max(list);
+    if ((tid & 63) == 0) {
+        tops[0][tid >> 6] = top;
+        tops[1][tid >> 6] = list;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+        top = fmaxf(top, tops[0][w]);
+        list = fmaxf(list, tops[1][w]);
+    }
+    bool twice = false;
+    for (int k = tid; k < K; k += kThreads)
+        if (ids[k] >= 0) {
+            const int at = ids[k] + row.shift;
+            twice |= (atomicOr(&bits[at >> 5], 1u << (at & 31)) >> (at & 31) & 1) != 0;
+        }
+    twice = __syncthreads_or(twice);
+
+    // 2. the sums: of the row at both temperatures, of the tokens outside the list,
+    // and of the list's probabilities and their products with log p / q
+    const float c = kLog2e * heat;
+    const bool rest = a.total != nullptr, both = a.hard != 0.0f && a.temperature != 1.0f;
+    const float base = rest ? gload<float>(a.total, t) : list == -kInf ? 0.0f : list;
+    float s[kSums] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    each([&](int i, const float* x) {
+        float e[kN];
+#pragma unroll
+        for (int j = 0; j < kN; ++j) {
+            e[j] = __builtin_amdgcn_exp2f((x[j] - top) * c);
+            s[0] += e[j];
+        }
+        if (rest) {
+            const unsigned int listed = bits[i * kN >> 5] >> (i * kN & 31);
+#pragma unroll
+            for (int j = 0; j < kN; ++j) s[1] += listed >> j & 1 ? 0.0f : e[j];
+        }
+        if (both) {
+#pragma unroll
+            for (int j = 0; j < kN; ++j) s[2] += __builtin_amdgcn_exp2f((x[j] - top) * kLog2e);
+        }
+    });
+    for (int k = tid; k < K; k += kThreads) {
+        if (ids[k] < 0) continue;
+        const float y = teacher[k] - base, p = __builtin_amdgcn_exp2f(y * kLog2e);
+        teacher[k] = p;
+        s[3] += p;
+        if (p > 0.0f) s[4] += p * (y - (student[k] - top) * heat);
+    }
+#pragma unroll
+    for (int n = 0; n < kSums; ++n) {
+        s[n] = wave_sum(s[n]);
+        if ((tid & 63) == 0) sums[n][tid >> 6] = s[n];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < kSums; ++n) {
+        s[n] = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) s[n] += sums[n][w];
+    }
+    if (!both) s[2] = s[0];
+
+    const float log_all = kLn2 * __builtin_amdgcn_logf(s[0]);
+    float kl = 0.0f, mass = 0.0f, others = 0.0f, norm = 1.0f;  // norm: of the list's p
+    if (rest) {
+        others = 1.0f - s[3];
+        if (!(others > 0.0f) || s[1] == 0.0f) others = s[3] != s[3] ? s[3] : 0.0f;
+        kl = s[4] + s[3] * log_all;
+        if (others > 0.0f) kl += others * (kLn2 * __builtin_amdgcn_logf(others) - (kLn2 * __builtin_amdgcn_logf(s[1]) - log_all));
+        mass = s[3] + others;
+    } else if (list != -kInf) {
+        norm = 1.0f / s[3];
+        kl = s[4] * norm - kLn2 * __builtin_amdgcn_logf(s[3]) + log_all;
+        mass = 1.0f;
+    }
+    int label = -1;
+    float ce = 0.0f, target = 0.0f;
+    if (a.hard != 0.0f && a.labels) {
+        const int64_t y = load_id(a.id_bytes, a.labels, t);
+        if (y >= 0 && y < a.vocab) {
+            label = static_cast<int>(y);
+            target = load1<DT>(row.p, y);
+            ce = kLn2 * __builtin_amdgcn_logf(s[2]) - (target - top);
+        }
+    }
+    if (a.loss && tid == 0)
+        gstore<float>(a.loss, t, a.soft * a.temperature * a.temperature * kl + (label >= 0 ? a.hard * ce : 0.0f));
+    if (!out) return;
+    __syncthreads();  // in place: every logit of the list and the label's are read
+
+    // 3. the gradient of the tokens outside the list, then of the others
+    const float factor = a.scale * weight, soft = factor * a.soft * a.temperature;
+    const float hard = label >= 0 ? factor * a.hard / s[2] : 0.0f;
+    const float in = soft * (mass / s[0]), over = in - (others > 0.0f ? soft * (others / s[1]) : 0.0f);
+    each([&](int i, const float* x) {
+        float g[kN];
+#pragma unroll
+        for (int j = 0; j < kN; ++j) {
+            const float e = __builtin_amdgcn_exp2f((x[j] - top) * c);
+            g[j] = e * over;
+            if (both) g[j] += __builtin_amdgcn_exp2f((x[j] - top) * kLog2e) * hard;
+            else g[j] += e * hard;
+        }
+        row.store(out, i, g);
+    });
+    __syncthreads();
+    const auto again = [&](int id, float z, float p, float coefficient) {
+        const float e = __builtin_amdgcn_exp2f((z - top) * c);
+        float g = e * coefficient - soft * p;
+        const float e1 = both ? __builtin_amdgcn_exp2f((z - top) * kLog2e) : e;
+        g += e1 * hard;
+        if (id == label) g -= factor * a.hard;
+        store1<DT>(out, id, g);
+    };
+    for (int k = tid; k < K; k += kThreads) {
+        if (ids[k] < 0) continue;
+        float p = teacher[k] * norm;
+        if (twice) {  // the first of a token's places in the list writes for all of them
+            bool earlier = false;
+            p = 0.0f;
+            for (int i = 0; i < K; ++i)
+                if (ids[i] == ids[k]) {
+                    earlier |= i < k;
+                    p += teacher[i] * norm;
+                }
+            if (earlier) continue;
+        }
+        again(ids[k], student[k], p, in);
+    }
+    if (tid == 0 && label >= 0) {
+        const int at = label + row.shift;
+        if (!(bits[at >> 5] >> (at & 31) & 1)) again(label, target, 0.0f, over);
+    }
+}
+
+template <dp_dtype DT, int kThreads, int kKept>
+hipError_t go(const DistillArgs& a, dp_dtype teacher_dt, hipStream_t stream) {
+    const size_t lds = 12 * static_cast<size_t>(a.top) + 4 * static_cast<size_t>((a.vocab + 8 + 31) / 32);
+    hipLaunchKernelGGL((k_distill<DT, kThreads, kKept>), dim3(static_cast<unsigned>(a.tokens)), dim3(kThreads), lds, stream,
+                       a, teacher_dt);
+    return hipGetLastError();
+}
+
+// The smallest number of registers that holds a row: of 256 threads for short
+// rows, so that more rows are on their way, of 1024 for longer ones.
+template <dp_dtype DT>
+hipError_t launch_row(const DistillArgs& a, dp_dtype teacher_dt, hipStream_t stream) {
+    constexpr int kN = Row<DT>::kN;
+    const int64_t pieces = (a.vocab + kN - 1 + kN - 1) / kN;  // at any alignment
+    if (pieces <= 256 * 4) return go<DT, 256, 4>(a, teacher_dt, stream);
+    if (pieces <= 256 * 8) return go<DT, 256, 8>(a, teacher_dt, stream);
+    if (pieces <= 1024 * 4) return go<DT, 1024, 4>(a, teacher_dt, stream);
+    if (pieces <= 1024 * 7) return go<DT, 1024, 7>(a, teacher_dt, stream);
+    if (pieces <= 1024 * 13) return go<DT, 1024, 13>(a, teacher_dt, stream);
+    if (pieces <= 1024 * 18) return go<DT, 1024, 18>(a, teacher_dt, stream);
+    return go<DT, 1024, 0>(a, teacher_dt, stream);
+}
+
+}  // namespace
+
+hipError_t launch_distill(dp_dtype dt, dp_dtype teacher_dt, const DistillArgs& a, hipStream_t stream) {
+    if (a.tokens == 0) return hipSuccess;
+    if (dt == DP_F32) return launch_row<DP_F32>(a, teacher_dt, stream);
+    if (dt == DP_F16) return launch_row<DP_F16>(a, teacher_dt, stream);
+    return launch_row<DP_BF16>(a, teacher_dt, stream);
+}
+
+}  // namespace dpk
