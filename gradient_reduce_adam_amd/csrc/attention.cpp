@@ -15,6 +15,7 @@ namespace {
 
 constexpr int64_t kMaxGroups = (int64_t{1} << 24) - 1;  // of 256 threads, fewer than 2^32 in a launch
 constexpr int64_t kMaxStride = int64_t{1} << 36;        // 2^24 rows stay within 63 bits
+constexpr int64_t kMaxRow = (int64_t{1} << 31) - 1;      // of the attention: a row in bytes within 32 bits
 constexpr int32_t kMaxRotaryDim = 4096;
 constexpr int32_t kMaxWindow = 1 << 26;  // beyond any two rows' distance
 
@@ -30,11 +31,11 @@ dp_status check_tokens(const char* where, const char* what, int64_t tokens) {
 }
 
 dp_status check_heads(const char* where, const char* what, const dpa_rows* r, int64_t tokens, int64_t heads, int64_t dim,
-                      int64_t elem, bool output) {
+                      int64_t elem, bool output, int64_t most_ld) {
     if (!r) return fail(DP_ERR_INVALID_ARG, "%s: %s is null", where, what);
     if (tokens > 0 && !r->p) return fail(DP_ERR_INVALID_ARG, "%s: the memory of %s is null", where, what);
     if (!multiple(r->p, elem)) return fail(DP_ERR_INVALID_ARG, "%s: %s is not aligned to its elements", where, what);
-    if (r->ld < 0 || r->head < 0 || r->ld > kMaxStride || r->head > kMaxStride)
+    if (r->ld < 0 || r->head < 0 || r->head > kMaxStride || (tokens > 1 && r->ld > most_ld))
         return fail(DP_ERR_INVALID_ARG, "%s: %s: strides %lld and %lld", where, what, ll(r->ld), ll(r->head));
     if (!output || tokens == 0) return DP_OK;
     const bool heads_in_rows = (heads == 1 || r->head >= dim) && (tokens == 1 || r->ld >= (heads - 1) * r->head + dim);
@@ -137,8 +138,8 @@ dp_status dpa_rotary(const dpa_rotary_desc* d, int64_t tokens, int32_t dim, cons
     for (int32_t i = 0; i < count; ++i) {
         const dpa_rotary_rows& r = rows[i];
         if (r.heads < 1 || r.heads > DPA_MAX_HEADS) return fail(DP_ERR_INVALID_ARG, "%s: %d heads outside [1, %d]", where, r.heads, DPA_MAX_HEADS);
-        s = check_heads(where, "x", &r.x, tokens, r.heads, dim, esize(dtype), false);
-        if (s == DP_OK) s = check_heads(where, "y", &r.y, tokens, r.heads, dim, esize(dtype), true);
+        s = check_heads(where, "x", &r.x, tokens, r.heads, dim, esize(dtype), false, kMaxStride);
+        if (s == DP_OK) s = check_heads(where, "y", &r.y, tokens, r.heads, dim, esize(dtype), true, kMaxStride);
         if (s != DP_OK) return s;
         if (tokens > 0 && r.x.p == r.y.p && ((tokens > 1 && r.x.ld != r.y.ld) || (r.heads > 1 && r.x.head != r.y.head)))
             return fail(DP_ERR_INVALID_ARG, "%s: y in place of x needs its strides", where);
@@ -172,10 +173,10 @@ dp_status dpa_attention(const dpa_attention_desc* d, dp_dtype dtype, const dpa_r
     const char* where = "dpa_attention";
     dpk::AttentionArgs a{};
     dp_status s = check_attention(where, d, dtype, &a.s);
-    if (s == DP_OK) s = check_heads(where, "q", q, d->tokens, d->heads, d->dim, 2, false);
-    if (s == DP_OK) s = check_heads(where, "k", k, d->tokens_k, d->kv_heads, d->dim, 2, false);
-    if (s == DP_OK) s = check_heads(where, "v", v, d->tokens_k, d->kv_heads, d->dim, 2, false);
-    if (s == DP_OK) s = check_heads(where, "out", out, d->tokens, d->heads, d->dim, 2, true);
+    if (s == DP_OK) s = check_heads(where, "q", q, d->tokens, d->heads, d->dim, 2, false, kMaxRow);
+    if (s == DP_OK) s = check_heads(where, "k", k, d->tokens_k, d->kv_heads, d->dim, 2, false, kMaxRow);
+    if (s == DP_OK) s = check_heads(where, "v", v, d->tokens_k, d->kv_heads, d->dim, 2, false, kMaxRow);
+    if (s == DP_OK) s = check_heads(where, "out", out, d->tokens, d->heads, d->dim, 2, true, kMaxRow);
     if (s == DP_OK) s = check_lse(where, lse, d->tokens);
     if (s != DP_OK) return s;
     if (d->tokens > 0 && (out->p == q->p || out->p == k->p || out->p == v->p))
@@ -215,7 +216,7 @@ dp_status dpa_attention_backward(const dpa_attention_desc* d, dp_dtype dtype, co
                {"out", out, false, false, &a.out}, {"dout", dout, false, false, &a.dout},
                {"dq", dq, false, true, &a.dq},     {"dk", dk, true, true, &a.dk}, {"dv", dv, true, true, &a.dv}};
     for (const auto& x : all) {
-        s = check_heads(where, x.name, x.rows, x.keys ? d->tokens_k : d->tokens, x.keys ? d->kv_heads : d->heads, d->dim, 2, x.output);
+        s = check_heads(where, x.name, x.rows, x.keys ? d->tokens_k : d->tokens, x.keys ? d->kv_heads : d->heads, d->dim, 2, x.output, kMaxRow);
         if (s != DP_OK) return s;
         *x.to = *x.rows;
     }

@@ -35,6 +35,7 @@ typedef __attribute__((address_space(3))) float lds_f32;
 typedef __attribute__((address_space(3))) unsigned char lds_u8;
 
 constexpr int kThreads = 256;
+
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kInf = __builtin_inff();
@@ -140,36 +141,67 @@ __device__ __forceinline__ void load_right(const Head& m, int64_t row, bool ther
     for (int s = 0; s < kD / 16; ++s) o[s] = load8(m, row, 16 * s + 8 * half, there && 16 * s + 8 * half < dim);
 }
 
-// A thread's pieces of a tile of kRows rows on the way through registers.
+// A thread's pieces of a tile of kRows rows on the way through registers: piece i
+// is slot threadIdx.x % kWide of row threadIdx.x / kWide + i kStep.  Nothing here
+// depends on a branch, so that no load is waited for where it is issued: rows
+// behind the last one are read from that one (their scores do not count), and slots
+// without elements from the first one; these are zeroed once and never stored.
 template <int kD, int kRows>
 struct Stage {
-    static constexpr int kPieces = kRows * Tile<kD>::kSlots;
-    static constexpr int kEach = (kPieces + kThreads - 1) / kThreads;
-    static constexpr bool kEven = kPieces % kThreads == 0;
+    static constexpr int kWide = Tile<kD>::kLd / 8, kStep = kThreads / kWide, kEach = kRows / kStep;
+    static_assert(kRows % kStep == 0, "a piece of every row");
+    static_assert(kStep % 16 == 0, "the slots' order repeats every 16 rows");
     u32x4 v[kEach];
 
-    static __device__ __forceinline__ int row_of(int i) { return (i * kThreads + static_cast<int>(threadIdx.x)) / Tile<kD>::kSlots; }
-    static __device__ __forceinline__ int slot_of(int i) { return (i * kThreads + static_cast<int>(threadIdx.x)) % Tile<kD>::kSlots; }
+    static __device__ __forceinline__ int slot() { return threadIdx.x % kWide; }
+    static __device__ __forceinline__ int row() { return threadIdx.x / kWide; }
+    static __device__ __forceinline__ bool active(int dim) { return 8 * slot() < dim; }
 
-    // Rows [first, end) of the tile that starts at row `first`; zeros behind them
-    // and behind the elements that exist.
-    __device__ __forceinline__ void load(const Head& m, int64_t first, int64_t end, int dim) {
-        if (kEven && first + kRows <= end && dim == kD) {
-            const unsigned short* p = m.p + first * m.ld;
+    // The tile that starts at row `first` of `end` > first rows.
+    __device__ __forceinline__ void load(const Head& m, int first, int end, int dim) {
+        const char* p = reinterpret_cast<const char*>(m.p + first * m.ld) + (active(dim) ? 16 * slot() : 0);
+        const uint32_t last = end - 1 - first, ld = static_cast<uint32_t>(2 * m.ld);
 #pragma unroll
-            for (int i = 0; i < kEach; ++i) v[i] = gload<u32x4, 2>(p + row_of(i) * m.ld + 8 * slot_of(i), 0);
-        } else {
-#pragma unroll
-            for (int i = 0; i < kEach; ++i)
-                v[i] = load8(m, first + row_of(i), 8 * slot_of(i), first + row_of(i) < end && row_of(i) < kRows && 8 * slot_of(i) < dim);
+        for (int i = 0; i < kEach; ++i) {
+            const uint32_t r = row() + i * kStep;
+            v[i] = gload<u32x4, 2>(p + static_cast<uint64_t>(r < last ? r : last) * ld, 0);
         }
     }
-    __device__ __forceinline__ void store(lds_u8* tile) const {
+    __device__ __forceinline__ void store(lds_u8* tile, int dim) const {
+        const int at = Tile<kD>::place(row(), slot());
+        if (active(dim)) {
 #pragma unroll
-        for (int i = 0; i < kEach; ++i)
-            if (kEven || row_of(i) < kRows) *(lds_u32x4*)(tile + Tile<kD>::place(row_of(i), slot_of(i))) = v[i];
+            for (int i = 0; i < kEach; ++i) *(lds_u32x4*)(tile + at + i * kStep * Tile<kD>::kRowBytes) = v[i];
+        }
+    }
+    static __device__ __forceinline__ void clear(lds_u8* tile, int dim) {
+        const int at = Tile<kD>::place(row(), slot());
+        if (!active(dim)) {
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) *(lds_u32x4*)(tile + at + i * kStep * Tile<kD>::kRowBytes) = u32x4{0, 0, 0, 0};
+        }
     }
 };
+
+// The order of instructions between two branches, for the scheduler: next are n
+// matrix products or LDS reads.  Left alone, it reads each fragment right before
+// its product and waits for it there.
+template <int n>
+__device__ __forceinline__ void products() { __builtin_amdgcn_sched_group_barrier(0x008, n, 0); }
+template <int n>
+__device__ __forceinline__ void reads() { __builtin_amdgcn_sched_group_barrier(0x100, n, 0); }
+// kCount times kProducts products with kReads reads, the reads kAhead times before.
+template <int kCount, int kProducts, int kReads, int kAhead>
+__device__ __forceinline__ void ahead() {
+    constexpr int kFirst = kAhead < kCount ? kAhead : kCount;
+    reads<kFirst * kReads>();
+#pragma unroll
+    for (int i = 0; i < kCount - kFirst; ++i) {
+        products<kProducts>();
+        reads<kReads>();
+    }
+    products<kFirst * kProducts>();
+}
 
 // 32 columns (one a lane) of a product's sum over blocks b of 32 rows, as rows of
 // elements d in memory: each pair of lanes first exchanges the words of two
@@ -197,8 +229,9 @@ __device__ __forceinline__ void store_columns(const dpa_rows& r, int64_t row, in
 }
 
 // ---- sequences --------------------------------------------------------------------------
-// A workgroup's sequence and its tile's place in it.
+// A workgroup's head, its sequence and its tile's place in it.
 struct Place {
+    int head;
     int64_t begin[2];  // first rows of the sequence, among the queries and the keys
     int length[2];
     int tile;   // of the sequence, in rows of the tile's size
@@ -210,29 +243,45 @@ __device__ __forceinline__ int64_t offset_at(const Sequences& s, int side, int64
     return x < 0 ? 0 : x > s.rows[side] ? s.rows[side] : x;
 }
 
-// Slot t of the tiles of all sequences, in the order of the sequences.  With
-// offsets, sequence s has the slots from begin / kRows + s on: these rise with s,
-// and as the next sequence begins behind the last row of this one, there are
+// Member i of n, so that the members with the same i % 8, whose workgroups run on one
+// XCD, are neighbours: heads that read the same keys share its cache.
+__device__ __forceinline__ int neighbour(int i, int n) { return n % 8 == 0 ? i % 8 * (n / 8) + i / 8 : i; }
+
+// The tile of this workgroup, of kRows rows of the queries (side 0) or keys (1), for
+// one of `heads` heads; false where it has none.  Tiles come in the order of their
+// work, the most first (`last_first`: in a sequence from its end), for all
+// sequences and heads at once, so that what is left at the end of the launch is
+// small: head by head instead, a fifth to a quarter of the CUs' time was lost there.
+//
+// With offsets, tiles are found by slots in the order of the sequences, heaviest
+// first in each.  Sequence s has the slots from begin / kRows + s on: these rise
+// with s, and as the next sequence begins behind the last row of this one, there are
 // enough of them for all its tiles.  Some are left over.
 template <int kRows>
-__device__ __forceinline__ bool find(const Sequences& s, int side, int t, Place& o) {
-    int n;  // the sequence
+__device__ __forceinline__ bool find(const Sequences& s, int side, int heads, bool last_first, Place& o) {
+    const int job = blockIdx.x;
+    int n, rank;  // the sequence, and which of its tiles
     if (s.offsets[side]) {
-        // the last sequence whose first slot is not behind t, 64 samples at a time
+        const int slot = job / heads;
+        o.head = neighbour(job % heads, heads);
+        // the last sequence whose first slot is not behind this one, 64 samples at a time
         int lo = 0, hi = s.count;  // in [lo, hi)
         while (hi - lo > 1) {
             const int each = (hi - lo + 63) / 64;
             const int at = lo + static_cast<int>(threadIdx.x & 63) * each;
-            const bool before = at < hi && offset_at(s, side, static_cast<int64_t>(at) * s.step) / kRows + at <= t;
+            const bool before = at < hi && offset_at(s, side, static_cast<int64_t>(at) * s.step) / kRows + at <= slot;
             const int found = __popcll(__ballot(before));
             lo = found > 0 ? lo + (found - 1) * each : lo;
             hi = lo + each < hi ? lo + each : hi;
         }
         n = __builtin_amdgcn_readfirstlane(lo);
+        rank = slot - (static_cast<int>(offset_at(s, side, static_cast<int64_t>(n) * s.step) / kRows) + n);
     } else {
-        const int per = static_cast<int>((s.length[side] + kRows - 1) / kRows);
-        n = per > 0 ? t / per : s.count;
-        if (n >= s.count) return false;
+        const int groups = heads * s.count;
+        rank = job / groups;
+        const int group = neighbour(job % groups, groups);
+        n = group / heads;
+        o.head = group % heads;
     }
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
@@ -247,19 +296,9 @@ __device__ __forceinline__ bool find(const Sequences& s, int side, int t, Place&
         o.begin[x] = b;
         o.length[x] = static_cast<int>(e > b ? e - b : 0);
     }
-    const int first = s.offsets[side] ? static_cast<int>(o.begin[side] / kRows) + n
-                                      : n * static_cast<int>((s.length[side] + kRows - 1) / kRows);
-    o.tile = t - first;
     o.tiles = (o.length[side] + kRows - 1) / kRows;
-    return o.tile >= 0 && o.tile < o.tiles;
-}
-
-// Workgroup i of n as a job: every eighth workgroup runs on the same XCD, and takes
-// the jobs of one eighth in turn, so that those that read the same keys share a
-// cache.
-__device__ __forceinline__ int job_of(int i, int n) {
-    const int per = n / 8, extra = n % 8, xcd = i % 8;
-    return xcd * per + (xcd < extra ? xcd : extra) + i / 8;
+    o.tile = last_first ? o.tiles - 1 - rank : rank;
+    return rank >= 0 && rank < o.tiles;
 }
 
 }  // namespace attn

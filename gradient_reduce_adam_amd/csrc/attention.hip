@@ -25,12 +25,10 @@ __global__ void __launch_bounds__(kThreads, kB == 1 ? 2 : 1) k_attention(Attenti
     constexpr int kTileBytes = kKeys * T::kRowBytes, kRows = 128 * kB, kBlocks = kD / 32;
     __shared__ __align__(1024) unsigned char lds[4 * kTileBytes];  // two turns of a k and a v tile
     const Sequences& sq = a.s;
-    const int slots = gridDim.x / sq.heads, job = job_of(blockIdx.x, gridDim.x);
-    const int h = job / slots, hk = h / (sq.heads / sq.kv_heads);
     Place at;
-    if (!find<kRows>(sq, 0, job % slots, at)) return;
+    if (!find<kRows>(sq, 0, sq.heads, sq.causal, at)) return;
+    const int h = at.head, hk = h / (sq.heads / sq.kv_heads), tile = at.tile;
     const int L = at.length[0], M = at.length[1], shift = M - L;
-    const int tile = sq.causal ? at.tiles - 1 - at.tile : at.tile;  // those with the most keys first
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = threadIdx.x >> 5 & 1;
     const int first = tile * kRows, mine = first + wave * 32 * kB;  // queries of the workgroup, of the wave
 
@@ -65,98 +63,107 @@ __global__ void __launch_bounds__(kThreads, kB == 1 ? 2 : 1) k_attention(Attenti
     const int along = T::along(), across = T::across();
     if (from < to) {
         Stage<kD, kKeys> ks, vs;
-        ks.load(k, from, M, sq.dim);
-        vs.load(v, from, M, sq.dim);
-        ks.store(base);
-        vs.store(base + kTileBytes);
-        if (from + kKeys < to) {
-            ks.load(k, from + kKeys, M, sq.dim);
-            vs.load(v, from + kKeys, M, sq.dim);
-        }
+        const auto load = [&](int t) {
+            ks.load(k, t, M, sq.dim);
+            vs.load(v, t, M, sq.dim);
+        };
+        const auto store = [&](int turn) {
+            ks.store(base + turn, sq.dim);
+            vs.store(base + turn + kTileBytes, sq.dim);
+        };
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ks.clear(base + i * kTileBytes, sq.dim);
+        load(from);
+        store(0);
+        load(from + kKeys < to ? from + kKeys : from);
         __syncthreads();
-        int turn = 0;
-        for (int t = from; t < to; t += kKeys) {
-            if (mine < L && t <= some_hi && t + kKeys > some_lo) {
-                const lds_u8* kt = base + turn;
-                const lds_u8* vt = kt + kTileBytes;
-                f32x16 s[kB][2];
+        const auto step = [&](const lds_u8* kt, int t) {
+            const lds_u8* vt = kt + kTileBytes;
+            f32x16 s[kB][2];
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
+            for (int b = 0; b < kB; ++b) s[b][0] = s[b][1] = zeros();
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                    for (int b = 0; b < kB; ++b) s[b][j] = zeros();
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
-                    for (int n = 0; n < kD / 16; ++n) {
-                        const u32x4 kf = T::read_along(kt, along, j, n);
+                for (int n = 0; n < kD / 16; ++n) {
+                    const u32x4 kf = T::read_along(kt, along, j, n);
 #pragma unroll
-                        for (int b = 0; b < kB; ++b) s[b][j] = mma<DT>(kf, qf[b][n], s[b][j]);
-                    }
+                    for (int b = 0; b < kB; ++b) s[b][j] = mma<DT>(kf, qf[b][n], s[b][j]);
                 }
-                u32x4 p[kB][2][2];
+            ahead<2 * (kD / 16), kB, 1, 6>();
+            u32x4 p[kB][2][2];
 #pragma unroll
-                for (int b = 0; b < kB; ++b) {
-                    if (t < all_lo || t + kKeys - 1 > all_hi) {  // scores that do not count
-                        const int up = hi[b] - t - 4 * half, down = lo[b] - t - 4 * half;
-#pragma unroll
-                        for (int j = 0; j < 2; ++j)
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                const int key = 32 * j + 8 * (e >> 2) + (e & 3);
-                                s[b][j][e] = key > up || key < down ? -kInf : s[b][j][e];
-                            }
-                    }
-                    float top = s[b][0][0];
+            for (int b = 0; b < kB; ++b) {
+                if (t < all_lo || t + kKeys - 1 > all_hi) {  // scores that do not count
+                    const int up = hi[b] - t - 4 * half, down = lo[b] - t - 4 * half;
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) top = fmaxf(top, s[b][j][e]);
-                    const f32x2 both = halves(top);
-                    top = fmaxf(fmaxf(both[0], both[1]), m[b]);
-                    // The sums follow the maximum only where it has risen by more than 8
-                    // powers of two: below that, p stays within 2^8 and keeps all its bits.
-                    if (__ballot(c * (top - m[b]) > 8.0f || m[b] == -kInf)) {
-                        const float alpha = m[b] == -kInf ? 0.0f : __builtin_amdgcn_exp2f(c * (m[b] - top));
-                        sum[b] *= alpha;
-#pragma unroll
-                        for (int n = 0; n < kBlocks; ++n)
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) o[b][n][e] *= alpha;
-                        m[b] = top;
-                    }
-                    const float less = m[b] == -kInf ? 0.0f : c * m[b];
-                    float part[2] = {0.0f, 0.0f};
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-#pragma unroll
                         for (int e = 0; e < 16; ++e) {
-                            s[b][j][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(c, s[b][j][e], -less));
-                            part[e & 1] += s[b][j][e];
+                            const int key = 32 * j + 8 * (e >> 2) + (e & 3);
+                            s[b][j][e] = key > up || key < down ? -kInf : s[b][j][e];
                         }
-#pragma unroll
-                        for (int n = 0; n < 2; ++n) p[b][j][n] = pack8<DT>(s[b][j], n);
-                    }
-                    sum[b] += part[0] + part[1];
                 }
+                float top = s[b][0][0];
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
-                    for (int n = 0; n < 2; ++n)
+                    for (int e = 0; e < 16; ++e) top = fmaxf(top, s[b][j][e]);
+                const f32x2 both = halves(top);
+                top = fmaxf(fmaxf(both[0], both[1]), m[b]);
+                // The sums follow the maximum only where it has risen by more than 8
+                // powers of two: below that, p stays within 2^8 and keeps all its bits.
+                if (__ballot(c * (top - m[b]) > 8.0f || m[b] == -kInf)) {
+                    const float alpha = m[b] == -kInf ? 0.0f : __builtin_amdgcn_exp2f(c * (m[b] - top));
+                    sum[b] *= alpha;
 #pragma unroll
-                        for (int x = 0; x < kBlocks; ++x) {
-                            const u32x4 vf = T::read_across(vt, across, 2 * j + n, x);
+                    for (int n = 0; n < kBlocks; ++n)
 #pragma unroll
-                            for (int b = 0; b < kB; ++b) o[b][x] = mma<DT>(vf, p[b][j][n], o[b][x]);
-                        }
-            }
-            if (t + kKeys < to) {
-                const int other = turn ^ (2 * kTileBytes);
-                ks.store(base + other);
-                vs.store(base + other + kTileBytes);
-                if (t + 2 * kKeys < to) {
-                    ks.load(k, t + 2 * kKeys, M, sq.dim);
-                    vs.load(v, t + 2 * kKeys, M, sq.dim);
+                        for (int e = 0; e < 16; ++e) o[b][n][e] *= alpha;
+                    m[b] = top;
                 }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int b = 0; b < kB; ++b) {
+                const float less = m[b] == -kInf ? 0.0f : c * m[b];
+                float part[2] = {0.0f, 0.0f};
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+#pragma unroll
+                        for (int e = 8 * n; e < 8 * n + 8; ++e) {
+                            s[b][j][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(c, s[b][j][e], -less));
+                            part[e & 1] += s[b][j][e];
+                        }
+                        p[b][j][n] = pack8<DT>(s[b][j], n);
+                    }
+                sum[b] += part[0] + part[1];
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int x = 0; x < kBlocks; ++x) {
+                        const u32x4 vf = T::read_across(vt, across, 2 * j + n, x);
+#pragma unroll
+                        for (int b = 0; b < kB; ++b) o[b][x] = mma<DT>(vf, p[b][j][n], o[b][x]);
+                    }
+            ahead<4 * kBlocks, kB, 2, 4>();
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        int turn = 0;
+        for (int t = from; t < to; t += kKeys) {
+            if (mine < L && t <= some_hi && t + kKeys > some_lo) step(base + turn, t);
+            if (t + kKeys < to) {
+                turn ^= 2 * kTileBytes;
+                store(turn);
+                // past the last tile this one is loaded again, and not used
+                load(t + 2 * kKeys < to ? t + 2 * kKeys : t + kKeys);
                 __syncthreads();
-                turn = other;
             }
         }
     }

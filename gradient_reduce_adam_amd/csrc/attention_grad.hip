@@ -32,12 +32,10 @@ __global__ void __launch_bounds__(kThreads, kB == 1 ? 2 : 1) k_attention_dq(Atte
     constexpr int kTileBytes = kKeys * T::kRowBytes, kRows = 128 * kB, kBlocks = kD / 32;
     __shared__ __align__(1024) unsigned char lds[4 * kTileBytes];  // two turns of a k and a v tile
     const Sequences& sq = a.s;
-    const int slots = gridDim.x / sq.heads, job = job_of(blockIdx.x, gridDim.x);
-    const int h = job / slots, hk = h / (sq.heads / sq.kv_heads);
     Place at;
-    if (!find<kRows>(sq, 0, job % slots, at)) return;
+    if (!find<kRows>(sq, 0, sq.heads, sq.causal, at)) return;
+    const int h = at.head, hk = h / (sq.heads / sq.kv_heads), tile = at.tile;
     const int L = at.length[0], M = at.length[1], shift = M - L;
-    const int tile = sq.causal ? at.tiles - 1 - at.tile : at.tile;  // those with the most keys first
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = threadIdx.x >> 5 & 1;
     const int first = tile * kRows, mine = first + wave * 32 * kB;
 
@@ -93,72 +91,81 @@ __global__ void __launch_bounds__(kThreads, kB == 1 ? 2 : 1) k_attention_dq(Atte
     const int along = T::along(), across = T::across();
     if (from < to) {
         Stage<kD, kKeys> ks, vs;
-        ks.load(k, from, M, sq.dim);
-        vs.load(v, from, M, sq.dim);
-        ks.store(base);
-        vs.store(base + kTileBytes);
-        if (from + kKeys < to) {
-            ks.load(k, from + kKeys, M, sq.dim);
-            vs.load(v, from + kKeys, M, sq.dim);
-        }
+        const auto load = [&](int t) {
+            ks.load(k, t, M, sq.dim);
+            vs.load(v, t, M, sq.dim);
+        };
+        const auto store = [&](int turn) {
+            ks.store(base + turn, sq.dim);
+            vs.store(base + turn + kTileBytes, sq.dim);
+        };
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ks.clear(base + i * kTileBytes, sq.dim);
+        load(from);
+        store(0);
+        load(from + kKeys < to ? from + kKeys : from);
         __syncthreads();
-        int turn = 0;
-        for (int t = from; t < to; t += kKeys) {
-            if (mine < L && t <= some_hi && t + kKeys > some_lo) {
-                const lds_u8* kt = base + turn;
-                const lds_u8* vt = kt + kTileBytes;
-                const bool masked = t < all_lo || t + kKeys - 1 > all_hi;
+        const auto step = [&](const lds_u8* kt, int t) {
+            const lds_u8* vt = kt + kTileBytes;
+            const bool masked = t < all_lo || t + kKeys - 1 > all_hi;
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    f32x16 s[kB], dp[kB];
+            for (int j = 0; j < 2; ++j) {
+                f32x16 s[kB], dp[kB];
 #pragma unroll
-                    for (int b = 0; b < kB; ++b) s[b] = dp[b] = zeros();
+                for (int b = 0; b < kB; ++b) s[b] = dp[b] = zeros();
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                    for (int n = 0; n < kD / 16; ++n) {
-                        const u32x4 kf = T::read_along(kt, along, j, n), vf = T::read_along(vt, along, j, n);
-#pragma unroll
-                        for (int b = 0; b < kB; ++b) {
-                            s[b] = mma<DT>(kf, qf[b][n], s[b]);
-                            dp[b] = mma<DT>(vf, df[b][n], dp[b]);
-                        }
-                    }
-                    u32x4 ds[kB][2];
+                for (int n = 0; n < kD / 16; ++n) {
+                    const u32x4 kf = T::read_along(kt, along, j, n), vf = T::read_along(vt, along, j, n);
 #pragma unroll
                     for (int b = 0; b < kB; ++b) {
-                        if (masked) {
-                            const int up = hi[b] - t - 4 * half, down = lo[b] - t - 4 * half;
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                const int key = 32 * j + 8 * (e >> 2) + (e & 3);
-                                s[b][e] = key > up || key < down ? -kInf : s[b][e];
-                            }
-                        }
-#pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            s[b][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(c, s[b][e], -less[b])) * (dp[b][e] - delta[b]);
-#pragma unroll
-                        for (int n = 0; n < 2; ++n) ds[b][n] = pack8<DT>(s[b], n);
+                        s[b] = mma<DT>(kf, qf[b][n], s[b]);
+                        dp[b] = mma<DT>(vf, df[b][n], dp[b]);
                     }
+                }
+                ahead<kD / 16, 2 * kB, 2, 3>();
+                if (masked) {
 #pragma unroll
-                    for (int n = 0; n < 2; ++n)
+                    for (int b = 0; b < kB; ++b) {
+                        const int up = hi[b] - t - 4 * half, down = lo[b] - t - 4 * half;
 #pragma unroll
-                        for (int x = 0; x < kBlocks; ++x) {
-                            const u32x4 kf = T::read_across(kt, across, 2 * j + n, x);
-#pragma unroll
-                            for (int b = 0; b < kB; ++b) o[b][x] = mma<DT>(kf, ds[b][n], o[b][x]);
+                        for (int e = 0; e < 16; ++e) {
+                            const int key = 32 * j + 8 * (e >> 2) + (e & 3);
+                            s[b][e] = key > up || key < down ? -kInf : s[b][e];
                         }
+                    }
                 }
+                __builtin_amdgcn_sched_barrier(0);
+                u32x4 ds[kB][2];
+#pragma unroll
+                for (int b = 0; b < kB; ++b) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        s[b][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(c, s[b][e], -less[b])) * (dp[b][e] - delta[b]);
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) ds[b][n] = pack8<DT>(s[b], n);
+                }
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int x = 0; x < kBlocks; ++x) {
+                        const u32x4 kf = T::read_across(kt, across, 2 * j + n, x);
+#pragma unroll
+                        for (int b = 0; b < kB; ++b) o[b][x] = mma<DT>(kf, ds[b][n], o[b][x]);
+                    }
+                ahead<2 * kBlocks, kB, 2, 4>();
+                __builtin_amdgcn_sched_barrier(0);
             }
+        };
+        int turn = 0;
+        for (int t = from; t < to; t += kKeys) {
+            if (mine < L && t <= some_hi && t + kKeys > some_lo) step(base + turn, t);
             if (t + kKeys < to) {
-                const int other = turn ^ (2 * kTileBytes);
-                ks.store(base + other);
-                vs.store(base + other + kTileBytes);
-                if (t + 2 * kKeys < to) {
-                    ks.load(k, t + 2 * kKeys, M, sq.dim);
-                    vs.load(v, t + 2 * kKeys, M, sq.dim);
-                }
+                turn ^= 2 * kTileBytes;
+                store(turn);
+                // past the last tile this one is loaded again, and not used
+                load(t + 2 * kKeys < to ? t + 2 * kKeys : t + kKeys);
                 __syncthreads();
-                turn = other;
             }
         }
     }
@@ -169,20 +176,21 @@ __global__ void __launch_bounds__(kThreads, kB == 1 ? 2 : 1) k_attention_dq(Atte
     }
 }
 
-template <dp_dtype DT, int kD, int kB>
-__global__ void __launch_bounds__(kThreads, kB == 1 && kD <= 96 ? 2 : 1) k_attention_dkv(AttentionArgs a) {
+// kShared: v's fragments stay in LDS and are read for each tile, not in registers.
+template <dp_dtype DT, int kD, bool kShared>
+__global__ void __launch_bounds__(kThreads, 2) k_attention_dkv(AttentionArgs a) {
     using T = Tile<kD>;
-    constexpr int kTileBytes = kQueries * T::kRowBytes, kRows = 128 * kB, kBlocks = kD / 32;
+    constexpr int kTileBytes = kQueries * T::kRowBytes, kRows = 128, kBlocks = kD / 32;
     constexpr int kTurn = 2 * kTileBytes + 2 * kQueries * 4;  // a q and a dout tile, -lse / scale and -delta of their rows
-    __shared__ __align__(1024) unsigned char lds[2 * kTurn];
+    constexpr int kValues = kShared ? kRows * T::kRowBytes : 0;
+    __shared__ __align__(1024) unsigned char lds[kValues + 2 * kTurn];
     const Sequences& sq = a.s;
-    const int slots = gridDim.x / sq.kv_heads, job = job_of(blockIdx.x, gridDim.x);
-    const int hk = job / slots, group = sq.heads / sq.kv_heads;
     Place at;
-    if (!find<kRows>(sq, 1, job % slots, at)) return;
+    if (!find<kRows>(sq, 1, sq.kv_heads, false, at)) return;
+    const int hk = at.head, group = sq.heads / sq.kv_heads;
     const int L = at.length[0], M = at.length[1], shift = M - L;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = threadIdx.x >> 5 & 1;
-    const int first = at.tile * kRows, mine = first + wave * 32 * kB;  // keys of the workgroup, of the wave
+    const int first = at.tile * kRows, mine = first + wave * 32;  // keys of the workgroup, of the wave
 
     // The queries that see a key: [lo, hi].
     const auto lowest = [&](int j) { return sq.causal && j - shift > 0 ? j - shift : 0; };
@@ -192,134 +200,125 @@ __global__ void __launch_bounds__(kThreads, kB == 1 && kD <= 96 ? 2 : 1) k_atten
     const int each = to > from ? (to - from + kQueries - 1) / kQueries : 0;  // tiles of a head
 
     const Head k = head_of(a.k, at.begin[1], hk), v = head_of(a.v, at.begin[1], hk);
-    u32x4 kf[kB][kD / 16], vf[kB][kD / 16];
-    f32x16 dk[kB][kBlocks], dv[kB][kBlocks];
-    int lo[kB], hi[kB];
+    const int key = mine + (threadIdx.x & 31);
+    const int lo = lowest(key), hi = highest(key);
+    u32x4 kf[kD / 16], vf[kShared ? 1 : kD / 16];
+    f32x16 dk[kBlocks], dv[kBlocks];
+    load_right<kD>(k, key, key < M, sq.dim, kf);
+    if constexpr (!kShared) load_right<kD>(v, key, key < M, sq.dim, vf);
 #pragma unroll
-    for (int b = 0; b < kB; ++b) {
-        const int j = mine + 32 * b + (threadIdx.x & 31);
-        load_right<kD>(k, j, j < M, sq.dim, kf[b]);
-        load_right<kD>(v, j, j < M, sq.dim, vf[b]);
-        lo[b] = lowest(j);
-        hi[b] = highest(j);
-#pragma unroll
-        for (int n = 0; n < kBlocks; ++n) dk[b][n] = dv[b][n] = zeros();
-    }
-    const int last = mine + 32 * kB - 1;
+    for (int n = 0; n < kBlocks; ++n) dk[n] = dv[n] = zeros();
+    const int last = mine + 31;
     const int some_lo = lowest(mine), some_hi = highest(last), all_lo = lowest(last), all_hi = highest(mine);
 
     const float c = sq.scale * kLog2e, unit = 1.0f / sq.scale;
-    lds_u8* const base = (lds_u8*)lds;
+    lds_u8* const base = (lds_u8*)lds + kValues;
     const int along = T::along(), across = T::across();
     const int tiles = each * group;
     if (tiles > 0) {
+        if constexpr (kShared) {
+            Stage<kD, kRows> vs;
+            vs.clear((lds_u8*)lds, sq.dim);
+            vs.load(v, first, M, sq.dim);
+            vs.store((lds_u8*)lds, sq.dim);
+        }
         Stage<kD, kQueries> qs, ds;
-        float row = 0.0f;  // of threads 0 .. 31: -lse / scale of a query, of 32 .. 63: -delta
+#pragma unroll
+        for (int i = 0; i < 4; ++i) qs.clear(base + (i >> 1) * kTurn + (i & 1) * kTileBytes, sq.dim);
+        // Of threads 0 .. 31: -lse / scale of a query, of 32 .. 63: -delta.  p = 0 for a
+        // query that sees no key, and for one that is not there.
+        float row = 0.0f;
         int g = 0, next = from;  // the next tile to load
         const auto load = [&]() {
             const int h = hk * group + g;
             qs.load(head_of(a.q, at.begin[0], h), next, L, sq.dim);
             ds.load(head_of(a.dout, at.begin[0], h), next, L, sq.dim);
-            if (threadIdx.x < 2 * kQueries) {
-                const int i = next + (threadIdx.x & 31);
-                const int64_t place = h * sq.rows[0] + at.begin[0] + i;
-                row = threadIdx.x < kQueries ? -kInf : 0.0f;
-                if (i < L) {
-                    if (threadIdx.x < kQueries) {
-                        const float lse = a.lse[place];
-                        row = lse == -kInf ? -kInf : -lse * unit;  // p = 0 for a query that sees no key
-                    } else {
-                        row = -a.delta[place];
-                    }
-                }
-            }
+            const int i = next + (threadIdx.x & 31), there = i < L ? i : L - 1;
+            const float* rows = threadIdx.x & 32 ? a.delta : a.lse;
+            row = gload<float>(rows, h * sq.rows[0] + at.begin[0] + there);
+            row = threadIdx.x & 32 ? -row : i < L && row != -kInf ? -row * unit : -kInf;
             next += kQueries;
             if (next >= to) {
                 next = from;
-                ++g;
+                g = g + 1 < group ? g + 1 : g;  // past the last tile: tiles that are not used
             }
         };
         const auto store = [&](int turn) {
-            qs.store(base + turn);
-            ds.store(base + turn + kTileBytes);
+            qs.store(base + turn, sq.dim);
+            ds.store(base + turn + kTileBytes, sq.dim);
             if (threadIdx.x < 2 * kQueries) *(lds_f32*)(base + turn + 2 * kTileBytes + 4 * threadIdx.x) = row;
+        };
+        const auto step = [&](const lds_u8* qt, int t) {
+            const lds_u8* dt = qt + kTileBytes;
+            const lds_u8* rt = dt + kTileBytes + 16 * half;
+            f32x16 s, dp;
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                const f32x4 x = *(const lds_f32x4*)(rt + 32 * n), y = *(const lds_f32x4*)(rt + 4 * kQueries + 32 * n);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    s[4 * n + e] = x[e];
+                    dp[4 * n + e] = y[e];
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < kD / 16; ++n) {
+                s = mma<DT>(T::read_along(qt, along, 0, n), kf[n], s);
+                if constexpr (kShared)
+                    dp = mma<DT>(T::read_along(dt, along, 0, n), T::read_along((lds_u8*)lds, along, wave, n), dp);
+                else dp = mma<DT>(T::read_along(dt, along, 0, n), vf[n], dp);
+            }
+            reads<8>();
+            ahead<kD / 16, 2, kShared ? 3 : 2, 2>();
+            if (t < all_lo || t + kQueries - 1 > all_hi) {
+                const int up = hi - t - 4 * half, down = lo - t - 4 * half;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int query = 8 * (e >> 2) + (e & 3);
+                    s[e] = query > up || query < down ? -kInf : s[e];
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            u32x4 p[2], w[2];
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+#pragma unroll
+                for (int e = 8 * n; e < 8 * n + 8; ++e) {
+                    s[e] = __builtin_amdgcn_exp2f(c * s[e]);
+                    dp[e] *= s[e];
+                }
+                p[n] = pack8<DT>(s, n);
+                w[n] = pack8<DT>(dp, n);
+            }
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int x = 0; x < kBlocks; ++x) {
+                    dv[x] = mma<DT>(T::read_across(dt, across, n, x), p[n], dv[x]);
+                    dk[x] = mma<DT>(T::read_across(qt, across, n, x), w[n], dk[x]);
+                }
+            ahead<4 * kBlocks, 1, 2, 4>();
+            __builtin_amdgcn_sched_barrier(0);
         };
         load();
         store(0);
-        if (tiles > 1) load();
+        load();
         __syncthreads();
         int turn = 0, t = from;
         for (int i = 0; i < tiles; ++i) {
-            if (mine < M && t <= some_hi && t + kQueries > some_lo) {
-                const lds_u8* qt = base + turn;
-                const lds_u8* dt = qt + kTileBytes;
-                const lds_u8* rt = dt + kTileBytes + 16 * half;
-                const bool masked = t < all_lo || t + kQueries - 1 > all_hi;
-                u32x4 p[kB][2], w[kB][2];
-#pragma unroll
-                for (int b = 0; b < kB; ++b) {
-                    f32x16 s, dp;
-#pragma unroll
-                    for (int n = 0; n < 4; ++n) {
-                        const f32x4 x = *(const lds_f32x4*)(rt + 32 * n), y = *(const lds_f32x4*)(rt + 4 * kQueries + 32 * n);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            s[4 * n + e] = x[e];
-                            dp[4 * n + e] = y[e];
-                        }
-                    }
-#pragma unroll
-                    for (int n = 0; n < kD / 16; ++n) {
-                        s = mma<DT>(T::read_along(qt, along, 0, n), kf[b][n], s);
-                        dp = mma<DT>(T::read_along(dt, along, 0, n), vf[b][n], dp);
-                    }
-                    if (masked) {
-                        const int up = hi[b] - t - 4 * half, down = lo[b] - t - 4 * half;
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const int query = 8 * (e >> 2) + (e & 3);
-                            s[e] = query > up || query < down ? -kInf : s[e];
-                        }
-                    }
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        s[e] = __builtin_amdgcn_exp2f(c * s[e]);
-                        dp[e] *= s[e];
-                    }
-#pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        p[b][n] = pack8<DT>(s, n);
-                        w[b][n] = pack8<DT>(dp, n);
-                    }
-                }
-#pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int x = 0; x < kBlocks; ++x) {
-                        const u32x4 df = T::read_across(dt, across, n, x), qf = T::read_across(qt, across, n, x);
-#pragma unroll
-                        for (int b = 0; b < kB; ++b) {
-                            dv[b][x] = mma<DT>(df, p[b][n], dv[b][x]);
-                            dk[b][x] = mma<DT>(qf, w[b][n], dk[b][x]);
-                        }
-                    }
-            }
+            if (mine < M && t <= some_hi && t + kQueries > some_lo) step(base + turn, t);
             t = t + kQueries >= to ? from : t + kQueries;
             if (i + 1 < tiles) {
-                const int other = turn ? 0 : kTurn;
-                store(other);
-                if (i + 2 < tiles) load();
+                turn = kTurn - turn;
+                store(turn);
+                load();
                 __syncthreads();
-                turn = other;
             }
         }
     }
-#pragma unroll
-    for (int b = 0; b < kB; ++b) {
-        const int j = mine + 32 * b + (threadIdx.x & 31);
-        store_columns<DT, kD>(a.dk, at.begin[1] + j, hk, j < M, sq.dim, dk[b], sq.scale);
-        store_columns<DT, kD>(a.dv, at.begin[1] + j, hk, j < M, sq.dim, dv[b], 1.0f);
-    }
+    store_columns<DT, kD>(a.dk, at.begin[1] + key, hk, key < M, sq.dim, dk, sq.scale);
+    store_columns<DT, kD>(a.dv, at.begin[1] + key, hk, key < M, sq.dim, dv, 1.0f);
 }
 
 template <dp_dtype DT, int kD>
@@ -327,7 +326,7 @@ void launch_both(const AttentionArgs& a, hipStream_t stream) {
     const dim3 block(kThreads), gq(static_cast<unsigned>(attention_slots(a.s, 0, 128) * a.s.heads)),
         gk(static_cast<unsigned>(attention_slots(a.s, 1, 128) * a.s.kv_heads));
     if (gq.x > 0) hipLaunchKernelGGL((k_attention_dq<DT, kD, 1>), gq, block, 0, stream, a);
-    if (gk.x > 0) hipLaunchKernelGGL((k_attention_dkv<DT, kD, 1>), gk, block, 0, stream, a);
+    if (gk.x > 0) hipLaunchKernelGGL((k_attention_dkv<DT, kD, (kD > 96)>), gk, block, 0, stream, a);
 }
 
 template <dp_dtype DT>
