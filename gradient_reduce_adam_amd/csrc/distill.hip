@@ -91,8 +91,24 @@ __global__ void __launch_bounds__(kThreads) k_distill(DistillArgs a, dp_dtype te
     float* const student = reinterpret_cast<float*>(dyn + 2 * K);   // the logit
     unsigned int* const bits = dyn + 3 * K;                         // of token v at v + shift
 
+    // What does not depend on anything is asked for first, together: a row of few
+    // rows waits for memory twice, not five times.
     const int64_t t = blockIdx.x;
+    const bool rest = a.total != nullptr;
     const float weight = a.weight ? gload<float>(a.weight, t) : 1.0f;
+    const float total = rest ? gload<float>(a.total, t) : 0.0f;
+    int64_t y_label = -1;
+    if (a.hard != 0.0f && a.labels) y_label = load_id(a.id_bytes, a.labels, t);
+    const float heat = 1.0f / a.temperature;
+    float list = -kInf;
+    for (int k = tid; k < K; k += kThreads) {
+        const int64_t id = load_id(a.id_bytes, a.ids, t * a.ld_ids + k);
+        const float y = load_any(teacher_dt, a.teacher, t * a.ld_teacher + k) * heat;
+        const bool there = id >= 0 && id < a.vocab;
+        ids[k] = there ? static_cast<int>(id) : -1;
+        teacher[k] = there ? y : -kInf;
+        list = fmaxf(list, there ? y : -kInf);
+    }
     const R row(a.logits, t, a.ld, a.vocab);
     constexpr int kSize = DT == DP_F32 ? 4 : 2;
     char* const out = a.dlogits ? static_cast<char*>(a.dlogits) + t * a.ld_dlogits * kSize : nullptr;
@@ -106,11 +122,14 @@ __global__ void __launch_bounds__(kThreads) k_distill(DistillArgs a, dp_dtype te
         return;
     }
 
-    // 1. the row, the list, and the greatest of both
+    // 1. the row, its logits of the list, and the greatest of both
     Raw<DT, kN> kept[kKept > 0 ? kKept : 1];
 #pragma unroll
     for (int k = 0; k < kKept; ++k)
         if (k * kThreads + tid < row.pieces) kept[k] = row.load(k * kThreads + tid);
+    const int label = y_label >= 0 && y_label < a.vocab ? static_cast<int>(y_label) : -1;
+    const float target = label >= 0 ? load1<DT>(row.p, label) : 0.0f;
+    for (int k = tid; k < K; k += kThreads) student[k] = ids[k] >= 0 ? load1<DT>(row.p, ids[k]) : 0.0f;
     const auto each = [&](auto&& use) {  // use(piece, its logits)
         if constexpr (kKept > 0) {
 #pragma unroll
@@ -130,17 +149,7 @@ __global__ void __launch_bounds__(kThreads) k_distill(DistillArgs a, dp_dtype te
         }
     };
     for (int i = tid; i < (row.vocab + row.shift + 31) / 32; i += kThreads) bits[i] = 0;
-    const float heat = 1.0f / a.temperature;
-    float top = -kInf, list = -kInf;
-    for (int k = tid; k < K; k += kThreads) {
-        const int64_t id = load_id(a.id_bytes, a.ids, t * a.ld_ids + k);
-        const bool there = id >= 0 && id < a.vocab;
-        const float y = there ? load_any(teacher_dt, a.teacher, t * a.ld_teacher + k) * heat : -kInf;
-        ids[k] = there ? static_cast<int>(id) : -1;
-        teacher[k] = y;
-        student[k] = there ? load1<DT>(row.p, id) : 0.0f;
-        list = fmaxf(list, y);
-    }
+    float top = -kInf;
     each([&](int, const float* x) {
 #pragma unroll
         for (int j = 0; j < kN; ++j) top = fmaxf(top, x[j]);
@@ -167,15 +176,19 @@ __global__ void __launch_bounds__(kThreads) k_distill(DistillArgs a, dp_dtype te
 
     // 2. the sums: of the row at both temperatures, of the tokens outside the list,
     // and of the list's probabilities and their products with log p / q
-    const float c = kLog2e * heat;
-    const bool rest = a.total != nullptr, both = a.hard != 0.0f && a.temperature != 1.0f;
-    const float base = rest ? gload<float>(a.total, t) : list == -kInf ? 0.0f : list;
+    // Exponentials are 2^(z c - peak), peak = top c as rounded: a row's reference, which
+    // log_all and the label's term take it for, so its rounding cancels.
+    const float c = kLog2e * heat, peak = top * c, peak1 = a.temperature == 2.0f ? 2.0f * peak : top * kLog2e;
+    const bool both = a.hard != 0.0f && a.temperature != 1.0f, square = a.temperature == 2.0f;
+    // the same without the temperature, from that with it: at 2 it is the square
+    const auto plain = [&](float z, float e) { return square ? e * e : __builtin_amdgcn_exp2f(__builtin_fmaf(z, kLog2e, -peak1)); };
+    const float base = rest ? total : list == -kInf ? 0.0f : list;
     float s[kSums] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
     each([&](int i, const float* x) {
         float e[kN];
 #pragma unroll
         for (int j = 0; j < kN; ++j) {
-            e[j] = __builtin_amdgcn_exp2f((x[j] - top) * c);
+            e[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[j], c, -peak));
             s[0] += e[j];
         }
         if (rest) {
@@ -184,8 +197,13 @@ __global__ void __launch_bounds__(kThreads) k_distill(DistillArgs a, dp_dtype te
             for (int j = 0; j < kN; ++j) s[1] += listed >> j & 1 ? 0.0f : e[j];
         }
         if (both) {
+            if (square) {
 #pragma unroll
-            for (int j = 0; j < kN; ++j) s[2] += __builtin_amdgcn_exp2f((x[j] - top) * kLog2e);
+                for (int j = 0; j < kN; ++j) s[2] = __builtin_fmaf(e[j], e[j], s[2]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < kN; ++j) s[2] += plain(x[j], 0.0f);
+            }
         }
     });
     for (int k = tid; k < K; k += kThreads) {
@@ -193,7 +211,7 @@ __global__ void __launch_bounds__(kThreads) k_distill(DistillArgs a, dp_dtype te
         const float y = teacher[k] - base, p = __builtin_amdgcn_exp2f(y * kLog2e);
         teacher[k] = p;
         s[3] += p;
-        if (p > 0.0f) s[4] += p * (y - (student[k] - top) * heat);
+        if (p > 0.0f) s[4] += p * (y - kLn2 * __builtin_fmaf(student[k], c, -peak));
     }
 #pragma unroll
     for (int n = 0; n < kSums; ++n) {
@@ -222,16 +240,7 @@ __global__ void __launch_bounds__(kThreads) k_distill(DistillArgs a, dp_dtype te
         kl = s[4] * norm - kLn2 * __builtin_amdgcn_logf(s[3]) + log_all;
         mass = 1.0f;
     }
-    int label = -1;
-    float ce = 0.0f, target = 0.0f;
-    if (a.hard != 0.0f && a.labels) {
-        const int64_t y = load_id(a.id_bytes, a.labels, t);
-        if (y >= 0 && y < a.vocab) {
-            label = static_cast<int>(y);
-            target = load1<DT>(row.p, y);
-            ce = kLn2 * __builtin_amdgcn_logf(s[2]) - (target - top);
-        }
-    }
+    const float ce = kLn2 * (__builtin_amdgcn_logf(s[2]) - __builtin_fmaf(target, both ? kLog2e : c, both ? -peak1 : -peak));
     if (a.loss && tid == 0)
         gstore<float>(a.loss, t, a.soft * a.temperature * a.temperature * kl + (label >= 0 ? a.hard * ce : 0.0f));
     if (!out) return;
@@ -243,20 +252,27 @@ __global__ void __launch_bounds__(kThreads) k_distill(DistillArgs a, dp_dtype te
     const float in = soft * (mass / s[0]), over = in - (others > 0.0f ? soft * (others / s[1]) : 0.0f);
     each([&](int i, const float* x) {
         float g[kN];
+        if (both && square) {  // e over + e^2 hard
 #pragma unroll
-        for (int j = 0; j < kN; ++j) {
-            const float e = __builtin_amdgcn_exp2f((x[j] - top) * c);
-            g[j] = e * over;
-            if (both) g[j] += __builtin_amdgcn_exp2f((x[j] - top) * kLog2e) * hard;
-            else g[j] += e * hard;
+            for (int j = 0; j < kN; ++j) {
+                const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(x[j], c, -peak));
+                g[j] = e * __builtin_fmaf(e, hard, over);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < kN; ++j) g[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[j], c, -peak)) * (both ? over : over + hard);
+            if (both) {
+#pragma unroll
+                for (int j = 0; j < kN; ++j) g[j] = __builtin_fmaf(plain(x[j], 0.0f), hard, g[j]);
+            }
         }
         row.store(out, i, g);
     });
     __syncthreads();
     const auto again = [&](int id, float z, float p, float coefficient) {
-        const float e = __builtin_amdgcn_exp2f((z - top) * c);
+        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(z, c, -peak));
         float g = e * coefficient - soft * p;
-        const float e1 = both ? __builtin_amdgcn_exp2f((z - top) * kLog2e) : e;
+        const float e1 = both ? plain(z, e) : e;
         g += e1 * hard;
         if (id == label) g -= factor * a.hard;
         store1<DT>(out, id, g);
@@ -290,18 +306,24 @@ hipError_t go(const DistillArgs& a, dp_dtype teacher_dt, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// The smallest number of registers that holds a row: of 256 threads for short
-// rows, so that more rows are on their way, of 1024 for longer ones.
+// The smallest number of registers that holds a row.  Many rows hide each other's
+// waits, so small workgroups, of which three or four are on a CU at once, take them:
+// 16384 x 32000 bf16 logits with their gradient 400 us by 256 threads a row, 446 to
+// 680 by 1024.  Up to one row a CU, a row has all threads that a workgroup can have.
 template <dp_dtype DT>
 hipError_t launch_row(const DistillArgs& a, dp_dtype teacher_dt, hipStream_t stream) {
     constexpr int kN = Row<DT>::kN;
     const int64_t pieces = (a.vocab + kN - 1 + kN - 1) / kN;  // at any alignment
-    if (pieces <= 256 * 4) return go<DT, 256, 4>(a, teacher_dt, stream);
-    if (pieces <= 256 * 8) return go<DT, 256, 8>(a, teacher_dt, stream);
-    if (pieces <= 1024 * 4) return go<DT, 1024, 4>(a, teacher_dt, stream);
+    if (a.tokens > 256) {
+        if (pieces <= 256 * 4) return go<DT, 256, 4>(a, teacher_dt, stream);
+        if (pieces <= 256 * 8) return go<DT, 256, 8>(a, teacher_dt, stream);
+        if (pieces <= 256 * 16) return go<DT, 256, 16>(a, teacher_dt, stream);
+        if (pieces <= 512 * 13) return go<DT, 512, 13>(a, teacher_dt, stream);
+    }
+    if (pieces <= 1024 * 2) return go<DT, 1024, 2>(a, teacher_dt, stream);
     if (pieces <= 1024 * 7) return go<DT, 1024, 7>(a, teacher_dt, stream);
     if (pieces <= 1024 * 13) return go<DT, 1024, 13>(a, teacher_dt, stream);
-    if (pieces <= 1024 * 18) return go<DT, 1024, 18>(a, teacher_dt, stream);
+    if (pieces <= 1024 * 16) return go<DT, 1024, 16>(a, teacher_dt, stream);
     return go<DT, 1024, 0>(a, teacher_dt, stream);
 }
 

@@ -148,7 +148,18 @@ def test_large_vocabularies(V, dt):
     Case(3, V, 33, dt, tau=1.5, soft=0.5, hard=0.5, tail=True, seed=V, weight=False).check()
 
 
-@pytest.mark.parametrize("tau", [0.25, 1.0, 3.0])
+@pytest.mark.parametrize("V,dt", [(500, "f16"), (12001, "bf16"), (12001, "f32"), (30011, "f16"), (50257, "bf16"), (24001, "f32")])
+def test_many_rows(V, dt):
+    """With more rows than CUs small workgroups take them."""
+    Case(261, V, 12, dt, tau=2.0, soft=0.5, hard=0.5, tail=True, seed=V).check()
+    c = Case(261, V, 12, dt, tau=0.7, soft=0.5, hard=0.5, seed=V + 1)
+    c.call()
+    grad = c.dlogits.clone()
+    c.call(dlogits=c.logits)
+    assert torch.equal(c.logits, grad)
+
+
+@pytest.mark.parametrize("tau", [0.25, 1.0, 2.0, 3.0])
 @pytest.mark.parametrize("tail", [False, True])
 @pytest.mark.parametrize("soft,hard", [(1.0, 0.0), (0.0, 1.0), (0.6, 0.4), (-0.5, 2.0)])
 def test_terms(soft, hard, tail, tau):
