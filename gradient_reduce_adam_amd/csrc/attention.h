@@ -34,7 +34,7 @@ typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
 typedef __attribute__((address_space(3))) float lds_f32;
 typedef __attribute__((address_space(3))) unsigned char lds_u8;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;  // of a workgroup, but where it has more waves
 
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
@@ -146,9 +146,9 @@ __device__ __forceinline__ void load_right(const Head& m, int64_t row, bool ther
 // depends on a branch, so that no load is waited for where it is issued: rows
 // behind the last one are read from that one (their scores do not count), and slots
 // without elements from the first one; these are zeroed once and never stored.
-template <int kD, int kRows>
+template <int kD, int kRows, int kAll = kThreads>
 struct Stage {
-    static constexpr int kWide = Tile<kD>::kLd / 8, kStep = kThreads / kWide, kEach = kRows / kStep;
+    static constexpr int kWide = Tile<kD>::kLd / 8, kStep = kAll / kWide, kEach = kRows / kStep;
     static_assert(kRows % kStep == 0, "a piece of every row");
     static_assert(kStep % 16 == 0, "the slots' order repeats every 16 rows");
     u32x4 v[kEach];

@@ -1,8 +1,8 @@
 // gfx950 kernel of the attention's forward pass: out = softmax(scale q k^T) v and
 // the logarithm of each row's sum, in one pass over the keys.
 //
-// A workgroup takes 128 kB queries of one head and goes over the keys that they
-// see in tiles of 64 rows of k and v.  Each of its four waves has 32 kB queries:
+// A workgroup takes 128 queries of one head and goes over the keys that they see in
+// tiles of 64 rows of k and v.  Each of its four waves has 32 queries:
 //   S^T = k q^T       rows are keys, columns queries: a lane holds its query's scores
 //   p = exp2(c S - c m), c = scale log2(e), m a running maximum of the query
 //   out^T += v^T p     p goes into the product from the registers it is in
@@ -19,50 +19,42 @@ using namespace attn;
 
 constexpr int kKeys = 64;  // of a tile
 
-template <dp_dtype DT, int kD, int kB>
-__global__ void __launch_bounds__(kThreads, kB == 1 ? 2 : 1) k_attention(AttentionArgs a) {
+template <dp_dtype DT, int kD, int kWaves>
+__global__ void __launch_bounds__(64 * kWaves, kWaves == 4 ? 2 : 1) k_attention(AttentionArgs a) {
     using T = Tile<kD>;
-    constexpr int kTileBytes = kKeys * T::kRowBytes, kRows = 128 * kB, kBlocks = kD / 32;
+    constexpr int kTileBytes = kKeys * T::kRowBytes, kRows = 32 * kWaves, kBlocks = kD / 32;
     __shared__ __align__(1024) unsigned char lds[4 * kTileBytes];  // two turns of a k and a v tile
     const Sequences& sq = a.s;
     Place at;
     if (!find<kRows>(sq, 0, sq.heads, sq.causal, at)) return;
-    const int h = at.head, hk = h / (sq.heads / sq.kv_heads), tile = at.tile;
+    const int h = at.head, hk = h / (sq.heads / sq.kv_heads);
     const int L = at.length[0], M = at.length[1], shift = M - L;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = threadIdx.x >> 5 & 1;
-    const int first = tile * kRows, mine = first + wave * 32 * kB;  // queries of the workgroup, of the wave
+    const int first = at.tile * kRows, mine = first + wave * 32;  // queries of the workgroup, of the wave
 
     // The keys that a query sees: [lo, hi].
     const auto lowest = [&](int i) { return sq.window > 0 && i + shift >= sq.window ? i + shift - sq.window + 1 : 0; };
     const auto highest = [&](int i) { return sq.causal && i + shift < M ? i + shift : M - 1; };
     const int behind = first + kRows < L ? first + kRows : L;  // the workgroup's queries end
     const int from = lowest(first) / kKeys * kKeys, to = highest(behind - 1) + 1;
+    const int i = mine + (threadIdx.x & 31);
+    const int lo = lowest(i), hi = highest(i);
+    // Tiles that some query of this wave sees, and those that all of them see whole.
+    const int some_lo = lowest(mine), some_hi = highest(mine + 31), all_lo = lowest(mine + 31), all_hi = highest(mine);
 
     const Head q = head_of(a.q, at.begin[0], h), k = head_of(a.k, at.begin[1], hk), v = head_of(a.v, at.begin[1], hk);
-    u32x4 qf[kB][kD / 16];
-    f32x16 o[kB][kBlocks];
-    float m[kB], sum[kB];
-    int lo[kB], hi[kB];
+    u32x4 qf[kD / 16];
+    load_right<kD>(q, i, i < L, sq.dim, qf);
+    f32x16 o[kBlocks];
 #pragma unroll
-    for (int b = 0; b < kB; ++b) {
-        const int i = mine + 32 * b + (threadIdx.x & 31);
-        load_right<kD>(q, i, i < L, sq.dim, qf[b]);
-        m[b] = -kInf;
-        sum[b] = 0.0f;
-        lo[b] = lowest(i);
-        hi[b] = highest(i);
-#pragma unroll
-        for (int n = 0; n < kBlocks; ++n) o[b][n] = zeros();
-    }
-    // Tiles that some query of this wave sees, and those that all of them see whole.
-    const int last = mine + 32 * kB - 1;
-    const int some_lo = lowest(mine), some_hi = highest(last), all_lo = lowest(last), all_hi = highest(mine);
+    for (int n = 0; n < kBlocks; ++n) o[n] = zeros();
+    float m = -kInf, sum = 0.0f;
 
     const float c = sq.scale * kLog2e;
     lds_u8* const base = (lds_u8*)lds;
     const int along = T::along(), across = T::across();
     if (from < to) {
-        Stage<kD, kKeys> ks, vs;
+        Stage<kD, kKeys, 64 * kWaves> ks, vs;
         const auto load = [&](int t) {
             ks.load(k, t, M, sq.dim);
             vs.load(v, t, M, sq.dim);
@@ -71,90 +63,74 @@ __global__ void __launch_bounds__(kThreads, kB == 1 ? 2 : 1) k_attention(Attenti
             ks.store(base + turn, sq.dim);
             vs.store(base + turn + kTileBytes, sq.dim);
         };
-#pragma unroll
-        for (int i = 0; i < 4; ++i) ks.clear(base + i * kTileBytes, sq.dim);
-        load(from);
-        store(0);
-        load(from + kKeys < to ? from + kKeys : from);
-        __syncthreads();
         const auto step = [&](const lds_u8* kt, int t) {
             const lds_u8* vt = kt + kTileBytes;
-            f32x16 s[kB][2];
-#pragma unroll
-            for (int b = 0; b < kB; ++b) s[b][0] = s[b][1] = zeros();
+            f32x16 s[2] = {zeros(), zeros()};
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
-                for (int n = 0; n < kD / 16; ++n) {
-                    const u32x4 kf = T::read_along(kt, along, j, n);
-#pragma unroll
-                    for (int b = 0; b < kB; ++b) s[b][j] = mma<DT>(kf, qf[b][n], s[b][j]);
-                }
-            ahead<2 * (kD / 16), kB, 1, 6>();
-            u32x4 p[kB][2][2];
-#pragma unroll
-            for (int b = 0; b < kB; ++b) {
-                if (t < all_lo || t + kKeys - 1 > all_hi) {  // scores that do not count
-                    const int up = hi[b] - t - 4 * half, down = lo[b] - t - 4 * half;
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const int key = 32 * j + 8 * (e >> 2) + (e & 3);
-                            s[b][j][e] = key > up || key < down ? -kInf : s[b][j][e];
-                        }
-                }
-                float top = s[b][0][0];
+                for (int n = 0; n < kD / 16; ++n) s[j] = mma<DT>(T::read_along(kt, along, j, n), qf[n], s[j]);
+            ahead<2 * (kD / 16), 1, 1, 6>();
+            if (t < all_lo || t + kKeys - 1 > all_hi) {  // scores that do not count
+                const int up = hi - t - 4 * half, down = lo - t - 4 * half;
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) top = fmaxf(top, s[b][j][e]);
-                const f32x2 both = halves(top);
-                top = fmaxf(fmaxf(both[0], both[1]), m[b]);
-                // The sums follow the maximum only where it has risen by more than 8
-                // powers of two: below that, p stays within 2^8 and keeps all its bits.
-                if (__ballot(c * (top - m[b]) > 8.0f || m[b] == -kInf)) {
-                    const float alpha = m[b] == -kInf ? 0.0f : __builtin_amdgcn_exp2f(c * (m[b] - top));
-                    sum[b] *= alpha;
+                    for (int e = 0; e < 16; ++e) {
+                        const int key = 32 * j + 8 * (e >> 2) + (e & 3);
+                        s[j][e] = key > up || key < down ? -kInf : s[j][e];
+                    }
+            }
+            float top = s[0][0];
 #pragma unroll
-                    for (int n = 0; n < kBlocks; ++n)
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) o[b][n][e] *= alpha;
-                    m[b] = top;
-                }
+                for (int e = 0; e < 16; ++e) top = fmaxf(top, s[j][e]);
+            const f32x2 both = halves(top);
+            top = fmaxf(fmaxf(both[0], both[1]), m);
+            // The sums follow the maximum only where it has risen by more than 8
+            // powers of two: below that, p stays within 2^8 and keeps all its bits.
+            if (__ballot(c * (top - m) > 8.0f || m == -kInf)) {
+                const float alpha = m == -kInf ? 0.0f : __builtin_amdgcn_exp2f(c * (m - top));
+                sum *= alpha;
+#pragma unroll
+                for (int n = 0; n < kBlocks; ++n)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[n][e] *= alpha;
+                m = top;
             }
             __builtin_amdgcn_sched_barrier(0);
+            const float less = m == -kInf ? 0.0f : c * m;
+            float part[2] = {0.0f, 0.0f};
+            u32x4 p[2][2];
 #pragma unroll
-            for (int b = 0; b < kB; ++b) {
-                const float less = m[b] == -kInf ? 0.0f : c * m[b];
-                float part[2] = {0.0f, 0.0f};
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
+                for (int n = 0; n < 2; ++n) {
 #pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-#pragma unroll
-                        for (int e = 8 * n; e < 8 * n + 8; ++e) {
-                            s[b][j][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(c, s[b][j][e], -less));
-                            part[e & 1] += s[b][j][e];
-                        }
-                        p[b][j][n] = pack8<DT>(s[b][j], n);
+                    for (int e = 8 * n; e < 8 * n + 8; ++e) {
+                        s[j][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(c, s[j][e], -less));
+                        part[e & 1] += s[j][e];
                     }
-                sum[b] += part[0] + part[1];
-            }
+                    p[j][n] = pack8<DT>(s[j], n);
+                }
+            sum += part[0] + part[1];
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
                 for (int n = 0; n < 2; ++n)
 #pragma unroll
-                    for (int x = 0; x < kBlocks; ++x) {
-                        const u32x4 vf = T::read_across(vt, across, 2 * j + n, x);
-#pragma unroll
-                        for (int b = 0; b < kB; ++b) o[b][x] = mma<DT>(vf, p[b][j][n], o[b][x]);
-                    }
-            ahead<4 * kBlocks, kB, 2, 4>();
+                    for (int x = 0; x < kBlocks; ++x) o[x] = mma<DT>(T::read_across(vt, across, 2 * j + n, x), p[j][n], o[x]);
+            ahead<4 * kBlocks, 1, 2, 4>();
             __builtin_amdgcn_sched_barrier(0);
         };
+#pragma unroll
+        for (int n = 0; n < 4; ++n) ks.clear(base + n * kTileBytes, sq.dim);
+        load(from);
+        store(0);
+        load(from + kKeys < to ? from + kKeys : from);
+        __syncthreads();
         int turn = 0;
         for (int t = from; t < to; t += kKeys) {
             if (mine < L && t <= some_hi && t + kKeys > some_lo) step(base + turn, t);
@@ -167,26 +143,27 @@ __global__ void __launch_bounds__(kThreads, kB == 1 ? 2 : 1) k_attention(Attenti
             }
         }
     }
-#pragma unroll
-    for (int b = 0; b < kB; ++b) {
-        const int i = mine + 32 * b + (threadIdx.x & 31);
-        const f32x2 both = halves(sum[b]);
-        const float total = both[0] + both[1];
-        // a query that sees no key: total 0, m -infinity
-        store_columns<DT, kD>(a.out, at.begin[0] + i, h, i < L, sq.dim, o[b], total == 0.0f ? 0.0f : 1.0f / total);
-        if (i < L && half == 0)
-            a.lse[h * sq.rows[0] + at.begin[0] + i] = total == 0.0f ? -kInf : sq.scale * m[b] + kLn2 * __builtin_amdgcn_logf(total);
-    }
+    const f32x2 both = halves(sum);
+    const float total = both[0] + both[1];
+    // a query that sees no key: total 0, m -infinity
+    store_columns<DT, kD>(a.out, at.begin[0] + i, h, i < L, sq.dim, o, total == 0.0f ? 0.0f : 1.0f / total);
+    if (i < L && half == 0)
+        a.lse[h * sq.rows[0] + at.begin[0] + i] = total == 0.0f ? -kInf : sq.scale * m + kLn2 * __builtin_amdgcn_logf(total);
 }
 
-template <dp_dtype DT, int kB>
+template <dp_dtype DT, int kD, int kWaves>
+void launch_one(const AttentionArgs& a, hipStream_t stream) {
+    const dim3 grid(static_cast<unsigned>(attention_slots(a.s, 0, 32 * kWaves) * a.s.heads));
+    if (grid.x > 0) hipLaunchKernelGGL((k_attention<DT, kD, kWaves>), grid, dim3(64 * kWaves), 0, stream, a);
+}
+
+template <dp_dtype DT>
 void launch_dim(const AttentionArgs& a, hipStream_t stream) {
-    const dim3 grid(static_cast<unsigned>(attention_slots(a.s, 0, 128 * kB) * a.s.heads)), block(kThreads);
-    if (grid.x == 0) return;
-    if (a.s.dim <= 32) hipLaunchKernelGGL((k_attention<DT, 32, kB>), grid, block, 0, stream, a);
-    else if (a.s.dim <= 64) hipLaunchKernelGGL((k_attention<DT, 64, kB>), grid, block, 0, stream, a);
-    else if (a.s.dim <= 96) hipLaunchKernelGGL((k_attention<DT, 96, kB>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((k_attention<DT, 128, kB>), grid, block, 0, stream, a);
+    if (a.s.dim <= 32) launch_one<DT, 32, 4>(a, stream);
+    else if (a.s.dim <= 64) launch_one<DT, 64, 4>(a, stream);
+    else if (a.s.dim <= 96) launch_one<DT, 96, 4>(a, stream);
+    else if (attention_wide(a.s)) launch_one<DT, 128, 8>(a, stream);
+    else launch_one<DT, 128, 4>(a, stream);
 }
 
 }  // namespace
@@ -196,14 +173,24 @@ int64_t attention_slots(const Sequences& s, int side, int64_t tile) {
     return s.offsets[side] ? s.rows[side] / tile + s.count : s.count * ((s.length[side] + tile - 1) / tile);
 }
 
+// Eight waves in a workgroup load each tile of keys half as often and leave more
+// registers to fragments that are read ahead, but wait for each other twice as
+// many, and their 256 queries cross the mask's edge further.  Heads of 128, four
+// against eight waves, forward and dq, TFLOP/s of their products: sequences of 8192
+// 980 and 1055 against 1038 and 1122, of 4096 874 and 967 against 894 and 1020, of
+// 2048 859 and 849 against 856 and 836.  They have to be enough to fill the CUs.
+bool attention_wide(const Sequences& s) {
+    return s.count > 0 && s.rows[1] / s.count >= 3500 && attention_slots(s, 0, 256) * s.heads >= 512;
+}
+
 int64_t attention_groups(const Sequences& s) {
     const int64_t q = attention_slots(s, 0, 128) * s.heads, k = attention_slots(s, 1, 128) * s.heads;
     return q > k ? q : k;
 }
 
 hipError_t launch_attention(dp_dtype dt, const AttentionArgs& a, hipStream_t stream) {
-    if (dt == DP_BF16) launch_dim<DP_BF16, 1>(a, stream);
-    else launch_dim<DP_F16, 1>(a, stream);
+    if (dt == DP_BF16) launch_dim<DP_BF16>(a, stream);
+    else launch_dim<DP_F16>(a, stream);
     return hipGetLastError();
 }
 

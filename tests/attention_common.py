@@ -21,11 +21,11 @@ TINY = {"bf16": FLUSH, "f16": 2.0 ** -25}
 INF = float("inf")
 
 
-def seen(L, M, causal, window):
+def seen(L, M, causal, window, device="cpu"):
     """[L, M]: which keys a query sees."""
-    place = torch.arange(L)[:, None] + M - L
-    j = torch.arange(M)[None, :]
-    ok = torch.ones((L, M), dtype=torch.bool)
+    place = torch.arange(L, device=device)[:, None] + M - L
+    j = torch.arange(M, device=device)[None, :]
+    ok = torch.ones((L, M), dtype=torch.bool, device=device)
     if causal:
         ok &= j <= place
     if window:
@@ -35,10 +35,10 @@ def seen(L, M, causal, window):
 
 def _head(q, k, v, ok, scale, lse=None):
     """Scores, lse and probabilities of a head in 64 bits, and their relative bound r."""
-    s = torch.where(ok, q @ k.t() * scale, torch.tensor(-INF, dtype=torch.float64))
+    s = torch.where(ok, q @ k.t() * scale, -INF)
     if lse is None:
-        lse = torch.logsumexp(s, 1) if k.shape[0] else torch.full((q.shape[0],), -INF, dtype=torch.float64)
-    p = torch.where(ok, torch.exp(s - lse[:, None]), torch.tensor(0.0, dtype=torch.float64))
+        lse = torch.logsumexp(s, 1) if k.shape[0] else torch.full((q.shape[0],), -INF, dtype=torch.float64, device=q.device)
+    p = torch.where(ok, torch.exp(s - lse[:, None]), 0.0)
     D = q.shape[1]
     near = torch.where(lse == -INF, torch.zeros_like(lse), lse.abs())[:, None]
     mag = torch.where(ok, s.abs(), torch.zeros_like(s))
@@ -47,15 +47,15 @@ def _head(q, k, v, ok, scale, lse=None):
     return s, lse, p, 2 * r.amax(1, keepdim=True) if k.shape[0] else r.sum(1, keepdim=True)
 
 
-def forward(q, k, v, spans, spans_k, causal, window, scale, dt):
+def forward(q, k, v, spans, spans_k, causal, window, scale, dt, device="cpu"):
     """(out, lse, bound of out, bound of lse) of rows [T, H, D], [Tk, K, D]; rows of no sequence are NaN."""
-    q, k, v = (x.double().cpu() for x in (q, k, v))
+    q, k, v = (x.double().to(device) for x in (q, k, v))
     T, H, D = q.shape
     group = H // k.shape[1]
-    out, bound = torch.full((T, H, D), float("nan"), dtype=torch.float64), torch.zeros((T, H, D), dtype=torch.float64)
-    lse, lbound = torch.full((H, T), float("nan"), dtype=torch.float64), torch.zeros((H, T), dtype=torch.float64)
+    out, bound = torch.full((T, H, D), float("nan"), dtype=torch.float64, device=device), torch.zeros((T, H, D), dtype=torch.float64, device=device)
+    lse, lbound = torch.full((H, T), float("nan"), dtype=torch.float64, device=device), torch.zeros((H, T), dtype=torch.float64, device=device)
     for (a, b), (e, f) in zip(spans, spans_k):
-        ok = seen(b - a, f - e, causal, window)
+        ok = seen(b - a, f - e, causal, window, device)
         for h in range(H):
             kk, vv = k[e:f, h // group], v[e:f, h // group]
             _, z, p, r = _head(q[a:b, h], kk, vv, ok, scale)
@@ -66,19 +66,19 @@ def forward(q, k, v, spans, spans_k, causal, window, scale, dt):
                              TINY[dt] * (1 + (ok.double() @ vv.abs())))
             near = torch.where(z == -INF, torch.zeros_like(z), z.abs())
             lbound[h, a:b] = r[:, 0] + (f - e + 8) * E + 4 * E * near
-    return out, lse, bound, lbound
+    return out.cpu(), lse.cpu(), bound.cpu(), lbound.cpu()
 
 
-def backward(q, k, v, out, lse, dout, spans, spans_k, causal, window, scale, dt):
+def backward(q, k, v, out, lse, dout, spans, spans_k, causal, window, scale, dt, device="cpu"):
     """((dq, dk, dv), their bounds) with the given out and lse; rows of no sequence are NaN."""
-    q, k, v, out, dout, lse = (x.double().cpu() for x in (q, k, v, out, dout, lse))
+    q, k, v, out, dout, lse = (x.double().to(device) for x in (q, k, v, out, dout, lse))
     T, H, D = q.shape
     Tk, K = k.shape[:2]
     group, u = H // K, U[dt]
-    grads = [torch.full(s, float("nan"), dtype=torch.float64) for s in ((T, H, D), (Tk, K, D), (Tk, K, D))]
+    grads = [torch.full(s, float("nan"), dtype=torch.float64, device=device) for s in ((T, H, D), (Tk, K, D), (Tk, K, D))]
     bounds = [torch.zeros_like(g) for g in grads]
     for (a, b), (e, f) in zip(spans, spans_k):
-        ok = seen(b - a, f - e, causal, window)
+        ok = seen(b - a, f - e, causal, window, device)
         for x in (1, 2):
             grads[x][e:f] = 0
         for h in range(H):
@@ -97,6 +97,7 @@ def backward(q, k, v, out, lse, dout, spans, spans_k, causal, window, scale, dt)
             bounds[1][e:f, g] += scale * ((eds + m * ds.abs()).t() @ qq.abs())
             grads[2][e:f, g] += p.t() @ do
             bounds[2][e:f, g] += (ep + m * p).t() @ do.abs()
+    grads, bounds = [x.cpu() for x in grads], [x.cpu() for x in bounds]
     return grads, [bo + (u + 4 * E) * gr.nan_to_num().abs() + TINY[dt] for gr, bo in zip(grads, bounds)]
 
 

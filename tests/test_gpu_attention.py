@@ -16,7 +16,7 @@ class Case:
     """Inputs of a call and its buffers, which hold a pattern where nothing may be written."""
 
     def __init__(self, spans, H, K, D, dt, seed=0, spans_k=None, causal=True, window=0, T=None, Tk=None, layout="own",
-                 sigma=1.0, scale=None):
+                 sigma=1.0, scale=None, device="cpu"):
         g = torch.Generator().manual_seed(seed)
         self.spans, self.spans_k = spans, spans_k or spans
         self.T = T or max([b for _, b in spans] + [0])
@@ -30,7 +30,7 @@ class Case:
         self.dk, self.dv = (self.tensor(self.Tk, K, layout, torch.full((self.Tk, K, D), 3.0)) for _ in range(2))
         self.lse = torch.full((H, self.T), 5.0, device="cuda")
         self.ws = torch.empty(max(1, dp.dpa_attention_workspace(self.T, H)), dtype=torch.uint8, device="cuda")
-        self.attention = dp.Attention(causal=causal, window=window, scale=scale)
+        self.attention, self.device = dp.Attention(causal=causal, window=window, scale=scale), device
 
     def tensor(self, t, n, layout, x):
         x, D = x.to(DT[self.dt]).cuda(), self.D
@@ -63,7 +63,7 @@ class Case:
     def check(self, **places):
         old = {x: getattr(self, x).clone() for x in ("out", "lse", "dq", "dk", "dv")}
         self.forward(**places)
-        args = (self.spans, self.spans_k, self.causal, self.window, self.scale, self.dt)
+        args = (self.spans, self.spans_k, self.causal, self.window, self.scale, self.dt, self.device)
         out, lse, eo, el = forward(self.q, self.k, self.v, *args)
         compare("out", self.out, out, eo, old["out"])
         compare("lse", self.lse, lse, el, old["lse"])
@@ -155,6 +155,14 @@ def test_many_sequences(S):
 def test_thousands_of_sequences():
     spans = cut(*[1 + i % 3 for i in range(5000)])
     c = Case(spans, 1, 1, 8, "bf16", seed=1)
+    c.check(**c.places())
+
+
+@pytest.mark.parametrize("L,M,H,D,causal,window", [(100, 3501, 512, 104, True, 0), (257, 3700, 256, 128, True, 700),
+                                                    (300, 3600, 256, 128, False, 0), (3600, 3600, 40, 112, True, 0)])
+def test_long_sequences(L, M, H, D, causal, window):
+    """Keys enough for workgroups of eight waves; the definition on the GPU, head by head."""
+    c = Case(cut(L), H, 2, D, "bf16", seed=M, spans_k=cut(M), causal=causal, window=window, device="cuda")
     c.check(**c.places())
 
 
