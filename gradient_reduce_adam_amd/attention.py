@@ -11,7 +11,8 @@ from __future__ import annotations
 
 import ctypes
 import math
-from dataclasses import dataclass
+import struct
+from dataclasses import dataclass, field
 from typing import Optional, Tuple
 
 from . import DP_BF16, DP_F16, _check, lib
@@ -62,6 +63,18 @@ class Rotary:
     base: float = 10000.0
     interleaved: bool = False
     own_ladder: bool = False
+    _refs: list = field(default_factory=list, init=False, repr=False, compare=False)
+
+    def ref(self):
+        """A reference to the ``dpa_rotary_desc``."""
+        if not self._refs:
+            sections = (ctypes.c_int32 * DPA_MAX_AXES)(*self.sections)
+            self._refs.append(ctypes.byref(RotaryDesc(len(self.sections), sections, int(self.interleaved),
+                                                      int(self.own_ladder), 0, self.base)))
+        return self._refs[0]
+
+    def __reduce__(self):  # copies and pickles leave the reference behind
+        return Rotary, (self.sections, self.base, self.interleaved, self.own_ladder)
 
 
 @dataclass(frozen=True)
@@ -75,13 +88,11 @@ class Attention:
 
 def _register() -> None:
     vp, i32, i64, sz, c_int = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
-    PR, PD = ctypes.POINTER(Rows), ctypes.POINTER(AttentionDesc)
-    sig = {
-        "dpa_rotary": [ctypes.POINTER(RotaryDesc), i64, i32, vp, i32, i64, i64, i32, ctypes.POINTER(RotaryRows), c_int,
-                       i32, vp],
-        "dpa_attention": [PD, c_int, PR, PR, PR, PR, vp, vp],
+    sig = {  # descriptions and rows by their addresses
+        "dpa_rotary": [vp, i64, i32, vp, i32, i64, i64, i32, vp, c_int, i32, vp],
+        "dpa_attention": [vp, c_int, vp, vp, vp, vp, vp, vp],
         "dpa_attention_workspace": [i64, i32, ctypes.POINTER(sz)],
-        "dpa_attention_backward": [PD, c_int, PR, PR, PR, PR, vp, PR, PR, PR, PR, vp, sz, vp],
+        "dpa_attention_backward": [vp, c_int, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -92,19 +103,27 @@ def _register() -> None:
 _register()
 
 
-def _heads(name: str, t, device: int, shape=None, dtype=None) -> Rows:
-    """The place and strides of a tensor of heads, after checking it."""
+# A call's structs are packed into one buffer at once, which takes a third of the time of a ctypes
+# structure each: a dpa_rotary_rows, and a dpa_attention_desc with the rows of the call's tensors behind it.
+_ROTARY_ROWS = struct.Struct("PqqPqqii")
+_DESC = "iiiiqdqqqPPii"
+_FORWARD, _BACKWARD = struct.Struct(_DESC + "Pqq" * 4), struct.Struct(_DESC + "Pqq" * 8)
+_DESC_BYTES, _ROWS_BYTES = ctypes.sizeof(AttentionDesc), ctypes.sizeof(Rows)
+
+
+def _heads(name: str, t, device: int, shape=None, dtype=None):
+    """The address and the strides of a tensor of heads, after checking it."""
     if t.get_device() != device:
         raise _elsewhere(name, t, device)
-    have = t.shape
-    if len(have) != 3 or (t.stride(2) != 1 and have[2] > 1):
+    have, strides = t.shape, t.stride()
+    if len(have) != 3 or (strides[2] != 1 and have[2] > 1):
         raise ValueError(f"{name} must be [tokens, heads, dim] with contiguous heads, not {tuple(have)} of strides "
-                         f"{t.stride()}")
+                         f"{strides}")
     if shape is not None and have != shape:
         raise ValueError(f"{name} is {tuple(have)}, expected {tuple(shape)}")
     if dtype is not None and t.dtype is not dtype:
         raise ValueError(f"{name} is {t.dtype}, expected {dtype}")
-    return Rows(t.data_ptr(), t.stride(0), t.stride(1))
+    return t.data_ptr(), strides[0], strides[1]
 
 
 # ---- positions -----------------------------------------------------------------
@@ -119,11 +138,9 @@ def dpa_rotary(rotary: Rotary, positions, x, y, inverse: bool = False, stream=No
     one, axes = xs[0], len(rotary.sections)
     if not 1 <= axes <= DPA_MAX_AXES:
         raise ValueError(f"{axes} axes (up to {DPA_MAX_AXES})")
-    rows = (RotaryRows * len(xs))()
-    for r, a, b in zip(rows, xs, ys):
-        r.x = _heads("x", a, dev, None, one.dtype)
-        r.y = _heads("y", b, dev, a.shape, one.dtype)
-        r.heads = a.shape[1]
+    rows = []
+    for a, b in zip(xs, ys):
+        rows += (*_heads("x", a, dev, None, one.dtype), *_heads("y", b, dev, a.shape, one.dtype), a.shape[1], 0)
         if a.shape[0] != one.shape[0] or a.shape[2] != one.shape[2]:
             raise ValueError(f"x: {tuple(a.shape)} beside {tuple(one.shape)}")
     tokens, _, dim = one.shape
@@ -134,10 +151,11 @@ def dpa_rotary(rotary: Rotary, positions, x, y, inverse: bool = False, stream=No
     at = positions.unsqueeze(1) if positions.dim() == 1 else positions
     if tuple(at.shape) != (tokens, axes):
         raise ValueError(f"positions are {tuple(positions.shape)}, expected ({tokens}, {axes})")
-    desc = RotaryDesc(axes, (ctypes.c_int32 * DPA_MAX_AXES)(*rotary.sections), int(rotary.interleaved),
-                      int(rotary.own_ladder), 0, rotary.base)
-    _check(lib.dpa_rotary(ctypes.byref(desc), tokens, dim, at.data_ptr(), at.element_size(), at.stride(0), at.stride(1),
-                          len(xs), rows, _dtype(one), int(inverse), _stream_of(stream, dev)))
+    buf = ctypes.create_string_buffer(_ROTARY_ROWS.size * len(xs))
+    for i in range(len(xs)):
+        _ROTARY_ROWS.pack_into(buf, i * _ROTARY_ROWS.size, *rows[8 * i:8 * i + 8])
+    _check(lib.dpa_rotary(rotary.ref(), tokens, dim, at.data_ptr(), at.element_size(), at.stride(0), at.stride(1),
+                          len(xs), ctypes.addressof(buf), _dtype(one), bool(inverse), _stream_of(stream, dev)))
 
 
 # ---- attention -----------------------------------------------------------------
@@ -152,11 +170,12 @@ def _offsets(name: str, t, device: int):
     return t.data_ptr(), t.shape[0] if spans else t.shape[0] - 1, t.element_size(), 2 if spans else 1
 
 
-def _describe(attention: Attention, q, k, sequences: Optional[int], offsets, offsets_k, device: int) -> AttentionDesc:
+def _describe(attention: Attention, q, k, sequences: Optional[int], offsets, offsets_k, device: int):
+    """The fields of a dpa_attention_desc."""
     if len(q.shape) != 3 or len(k.shape) != 3:
         raise ValueError(f"q and k must be [tokens, heads, dim], not {tuple(q.shape)} and {tuple(k.shape)}")
     tokens, heads, dim = q.shape
-    at, at_k, size, step = None, None, 0, 0
+    at, at_k, size, step = 0, 0, 0, 0
     if offsets is not None or offsets_k is not None:
         given = [_offsets(n, t, device) for n, t in (("offsets", offsets), ("offsets_k", offsets_k)) if t is not None]
         if len(given) == 2 and given[0][1:] != given[1][1:]:
@@ -165,11 +184,11 @@ def _describe(attention: Attention, q, k, sequences: Optional[int], offsets, off
         if sequences is not None and sequences != count:
             raise ValueError(f"offsets of {count} sequences, expected {sequences}")
         sequences = count
-        at = given[0][0] if offsets is not None else None
-        at_k = given[-1][0] if offsets_k is not None else None
+        at = given[0][0] if offsets is not None else 0
+        at_k = given[-1][0] if offsets_k is not None else 0
     scale = attention.scale if attention.scale is not None else 1.0 / math.sqrt(max(dim, 1))
-    return AttentionDesc(heads, k.shape[1], dim, int(attention.causal), attention.window, scale, tokens, k.shape[0],
-                         1 if sequences is None else sequences, at, at_k, size, step)
+    return (heads, k.shape[1], dim, bool(attention.causal), attention.window, scale, tokens, k.shape[0],
+            1 if sequences is None else sequences, at, at_k, size, step)
 
 
 _SIXTEEN = (DP_BF16, DP_F16)
@@ -196,12 +215,14 @@ def dpa_attention(attention: Attention, q, k, v, out, lse, sequences: Optional[i
     rows one sequence, or ``sequences`` of one length, or those at ``offsets`` (``[sequences + 1]``, or ``[sequences, 2]``
     of begins and ends; ``offsets_k`` for the keys where they lie elsewhere).  q and out are [tokens, heads, dim], k and v
     [tokens_k, kv_heads, dim]."""
-    dev = _current_device()
-    desc = _describe(attention, q, k, sequences, offsets, offsets_k, dev)
-    dtype, ref = q.dtype, ctypes.byref
-    _check(lib.dpa_attention(ref(desc), _attention_dtype(q), ref(_heads("q", q, dev)), ref(_heads("k", k, dev, None, dtype)),
-                             ref(_heads("v", v, dev, k.shape, dtype)), ref(_heads("out", out, dev, q.shape, dtype)),
-                             _lse(lse, q, dev), _stream_of(stream, dev)))
+    dev, dtype = _current_device(), q.dtype
+    code, desc = _attention_dtype(q), _describe(attention, q, k, sequences, offsets, offsets_k, dev)
+    buf = ctypes.create_string_buffer(_FORWARD.size)
+    _FORWARD.pack_into(buf, 0, *desc, *_heads("q", q, dev), *_heads("k", k, dev, None, dtype),
+                       *_heads("v", v, dev, k.shape, dtype), *_heads("out", out, dev, q.shape, dtype))
+    a = ctypes.addressof(buf)
+    r = range(a + _DESC_BYTES, a + _FORWARD.size, _ROWS_BYTES)
+    _check(lib.dpa_attention(a, code, *r, _lse(lse, q, dev), _stream_of(stream, dev)))
 
 
 def dpa_attention_workspace(tokens: int, heads: int) -> int:
@@ -211,13 +232,14 @@ def dpa_attention_workspace(tokens: int, heads: int) -> int:
 def dpa_attention_backward(attention: Attention, q, k, v, out, lse, dout, dq, dk, dv, workspace,
                            sequences: Optional[int] = None, offsets=None, offsets_k=None, stream=None) -> None:
     """The gradients dq, dk and dv of ``dpa_attention`` from dout, with the out and lse that it left."""
-    dev = _current_device()
-    desc = _describe(attention, q, k, sequences, offsets, offsets_k, dev)
-    dtype, ref, qs, ks = q.dtype, ctypes.byref, q.shape, k.shape
+    dev, dtype, qs, ks = _current_device(), q.dtype, q.shape, k.shape
+    code, desc = _attention_dtype(q), _describe(attention, q, k, sequences, offsets, offsets_k, dev)
+    buf = ctypes.create_string_buffer(_BACKWARD.size)
+    _BACKWARD.pack_into(buf, 0, *desc, *_heads("q", q, dev), *_heads("k", k, dev, None, dtype),
+                        *_heads("v", v, dev, ks, dtype), *_heads("out", out, dev, qs, dtype),
+                        *_heads("dout", dout, dev, qs, dtype), *_heads("dq", dq, dev, qs, dtype),
+                        *_heads("dk", dk, dev, ks, dtype), *_heads("dv", dv, dev, ks, dtype))
+    a = ctypes.addressof(buf)
+    r = range(a + _DESC_BYTES, a + _BACKWARD.size, _ROWS_BYTES)
     addr, nbytes = _workspace(workspace, dev)
-    _check(lib.dpa_attention_backward(
-        ref(desc), _attention_dtype(q), ref(_heads("q", q, dev)), ref(_heads("k", k, dev, None, dtype)),
-        ref(_heads("v", v, dev, ks, dtype)), ref(_heads("out", out, dev, qs, dtype)), _lse(lse, q, dev),
-        ref(_heads("dout", dout, dev, qs, dtype)), ref(_heads("dq", dq, dev, qs, dtype)),
-        ref(_heads("dk", dk, dev, ks, dtype)), ref(_heads("dv", dv, dev, ks, dtype)), addr, nbytes,
-        _stream_of(stream, dev)))
+    _check(lib.dpa_attention_backward(a, code, *r[:4], _lse(lse, q, dev), *r[4:], addr, nbytes, _stream_of(stream, dev)))

@@ -148,11 +148,12 @@ dp_status dpa_rotary(const dpa_rotary_desc* d, int64_t tokens, int32_t dim, cons
                 return fail(DP_ERR_INVALID_ARG, "%s: y of tensor %d overlaps tensor %d", where, i, k);
         a.rows[i] = r;
     }
+    const double log_base = std::log(d->base);
     int32_t at = 0;
     for (int32_t x = 0; x < d->axes; ++x)
         for (int32_t j = 0; j < d->sections[x]; ++j, ++at) {
             const double power = d->own_ladder ? static_cast<double>(j) / d->sections[x] : static_cast<double>(at) / static_cast<double>(pairs);
-            a.frequency[at] = std::pow(d->base, -power);
+            a.frequency[at] = std::exp(-power * log_base);  // off by 1e-15 of it where it is below 1/e, less above
             a.axis[at] = static_cast<unsigned char>(x);
         }
     a.positions = positions;

@@ -203,29 +203,48 @@ __device__ __forceinline__ void ahead() {
     products<kFirst * kProducts>();
 }
 
-// 32 columns (one a lane) of a product's sum over blocks b of 32 rows, as rows of
-// elements d in memory: each pair of lanes first exchanges the words of two
-// groups of eight rows, so that every lane stores 16 bytes.
+// 32 columns (one a lane) and 32 rows, d .. d + 31, of a product's sum as elements of
+// rows in memory, of which the first `dim` exist: each pair of lanes first exchanges
+// the words of two groups of eight, so that every lane stores 16 bytes.
+template <dp_dtype DT>
+__device__ __forceinline__ void store_block(unsigned short* p, int d, bool there, int dim, const f32x16& x, float factor) {
+    const int half = threadIdx.x >> 5 & 1;
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+        unsigned int w[2][2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                w[u][e] = pack2<DT>(x[8 * g + 4 * u + 2 * e] * factor, x[8 * g + 4 * u + 2 * e + 1] * factor);
+        const auto lo = __builtin_amdgcn_permlane32_swap(w[0][0], w[1][0], false, false);
+        const auto hi = __builtin_amdgcn_permlane32_swap(w[0][1], w[1][1], false, false);
+        const int at = d + 16 * g + 8 * half;
+        if (there && at < dim) gstore<u32x4, 2>(p + at, 0, u32x4{lo[0], hi[0], lo[1], hi[1]});
+    }
+}
 template <dp_dtype DT, int kD>
 __device__ __forceinline__ void store_columns(const dpa_rows& r, int64_t row, int h, bool there, int dim, const f32x16* x,
                                               float factor) {
     unsigned short* p = static_cast<unsigned short*>(r.p) + row * r.ld + h * r.head;
-    const int half = threadIdx.x >> 5 & 1;
 #pragma unroll
-    for (int b = 0; b < kD / 32; ++b)
+    for (int b = 0; b < (kD + 31) / 32; ++b) store_block<DT>(p, 32 * b, there, dim, x[b], factor);
+}
+
+// The waves' shares of a sum in LDS: block b of this wave, and back that of wave w.
+__device__ __forceinline__ void share_block(lds_u8* at, int blocks, int wave, int b, const f32x16& x) {
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-            unsigned int w[2][2];
+    for (int g = 0; g < 4; ++g)
+        *(lds_f32x4*)(at + ((wave * blocks + b) * 4 + g) * 1024 + 16 * (threadIdx.x & 63)) =
+            f32x4{x[4 * g], x[4 * g + 1], x[4 * g + 2], x[4 * g + 3]};
+}
+__device__ __forceinline__ void add_block(const lds_u8* at, int blocks, int wave, int b, float factor, f32x16& x) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+    for (int g = 0; g < 4; ++g) {
+        const f32x4 v = *(const lds_f32x4*)(at + ((wave * blocks + b) * 4 + g) * 1024 + 16 * (threadIdx.x & 63));
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    w[u][e] = pack2<DT>(x[b][8 * g + 4 * u + 2 * e] * factor, x[b][8 * g + 4 * u + 2 * e + 1] * factor);
-            const auto lo = __builtin_amdgcn_permlane32_swap(w[0][0], w[1][0], false, false);
-            const auto hi = __builtin_amdgcn_permlane32_swap(w[0][1], w[1][1], false, false);
-            const int d = 32 * b + 16 * g + 8 * half;
-            if (there && d < dim) gstore<u32x4, 2>(p + d, 0, u32x4{lo[0], hi[0], lo[1], hi[1]});
-        }
+        for (int e = 0; e < 4; ++e) x[4 * g + e] = __builtin_fmaf(factor, v[e], x[4 * g + e]);
+    }
 }
 
 // ---- sequences --------------------------------------------------------------------------

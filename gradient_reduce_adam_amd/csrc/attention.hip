@@ -7,6 +7,7 @@
 //   p = exp2(c S - c m), c = scale log2(e), m a running maximum of the query
 //   out^T += v^T p     p goes into the product from the registers it is in
 // with v^T read by the transposing LDS load, and sums and maxima kept by each lane.
+// Few queries: the waves have the same 32, and share the keys of a tile.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -17,12 +18,13 @@ namespace {
 
 using namespace attn;
 
-constexpr int kKeys = 64;  // of a tile
-
-template <dp_dtype DT, int kD, int kWaves>
-__global__ void __launch_bounds__(64 * kWaves, kWaves == 4 ? 2 : 1) k_attention(AttentionArgs a) {
+// kSplit: the four waves have the same 32 queries, and 32 keys each of every tile.
+template <dp_dtype DT, int kD, int kWaves, bool kSplit>
+__global__ void __launch_bounds__(64 * kWaves, kWaves == 4 && !kSplit ? 2 : 1) k_attention(AttentionArgs a) {
     using T = Tile<kD>;
-    constexpr int kTileBytes = kKeys * T::kRowBytes, kRows = 32 * kWaves, kBlocks = kD / 32;
+    constexpr int kRows = kSplit ? 32 : 32 * kWaves, kKeys = kSplit ? 32 * kWaves : 64, kBlocks = (kD + 31) / 32;
+    constexpr int kOwn = kSplit ? 1 : 2;  // times 32 keys of a tile that a wave takes
+    constexpr int kTileBytes = kKeys * T::kRowBytes;
     __shared__ __align__(1024) unsigned char lds[4 * kTileBytes];  // two turns of a k and a v tile
     const Sequences& sq = a.s;
     Place at;
@@ -30,7 +32,7 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves == 4 ? 2 : 1) k_attention(
     const int h = at.head, hk = h / (sq.heads / sq.kv_heads);
     const int L = at.length[0], M = at.length[1], shift = M - L;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = threadIdx.x >> 5 & 1;
-    const int first = at.tile * kRows, mine = first + wave * 32;  // queries of the workgroup, of the wave
+    const int first = at.tile * kRows, mine = first + (kSplit ? 0 : wave * 32);  // queries of the workgroup, of the wave
 
     // The keys that a query sees: [lo, hi].
     const auto lowest = [&](int i) { return sq.window > 0 && i + shift >= sq.window ? i + shift - sq.window + 1 : 0; };
@@ -63,19 +65,22 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves == 4 ? 2 : 1) k_attention(
             ks.store(base + turn, sq.dim);
             vs.store(base + turn + kTileBytes, sq.dim);
         };
+        // The wave's keys of a tile, from t on.
         const auto step = [&](const lds_u8* kt, int t) {
             const lds_u8* vt = kt + kTileBytes;
-            f32x16 s[2] = {zeros(), zeros()};
+            f32x16 s[kOwn];
+#pragma unroll
+            for (int j = 0; j < kOwn; ++j) s[j] = zeros();
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < kOwn; ++j)
 #pragma unroll
                 for (int n = 0; n < kD / 16; ++n) s[j] = mma<DT>(T::read_along(kt, along, j, n), qf[n], s[j]);
-            ahead<2 * (kD / 16), 1, 1, 6>();
-            if (t < all_lo || t + kKeys - 1 > all_hi) {  // scores that do not count
+            ahead<kOwn * (kD / 16), 1, 1, 6>();
+            if (t < all_lo || t + 32 * kOwn - 1 > all_hi) {  // scores that do not count
                 const int up = hi - t - 4 * half, down = lo - t - 4 * half;
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
+                for (int j = 0; j < kOwn; ++j)
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         const int key = 32 * j + 8 * (e >> 2) + (e & 3);
@@ -84,7 +89,7 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves == 4 ? 2 : 1) k_attention(
             }
             float top = s[0][0];
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < kOwn; ++j)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) top = fmaxf(top, s[j][e]);
             const f32x2 both = halves(top);
@@ -103,9 +108,9 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves == 4 ? 2 : 1) k_attention(
             __builtin_amdgcn_sched_barrier(0);
             const float less = m == -kInf ? 0.0f : c * m;
             float part[2] = {0.0f, 0.0f};
-            u32x4 p[2][2];
+            u32x4 p[kOwn][2];
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < kOwn; ++j)
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
 #pragma unroll
@@ -117,12 +122,12 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves == 4 ? 2 : 1) k_attention(
                 }
             sum += part[0] + part[1];
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < kOwn; ++j)
 #pragma unroll
                 for (int n = 0; n < 2; ++n)
 #pragma unroll
                     for (int x = 0; x < kBlocks; ++x) o[x] = mma<DT>(T::read_across(vt, across, 2 * j + n, x), p[j][n], o[x]);
-            ahead<4 * kBlocks, 1, 2, 4>();
+            ahead<2 * kOwn * kBlocks, 1, 2, 4>();
             __builtin_amdgcn_sched_barrier(0);
         };
 #pragma unroll
@@ -133,7 +138,9 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves == 4 ? 2 : 1) k_attention(
         __syncthreads();
         int turn = 0;
         for (int t = from; t < to; t += kKeys) {
-            if (mine < L && t <= some_hi && t + kKeys > some_lo) step(base + turn, t);
+            const int skip = kSplit ? 32 * wave : 0;
+            if (mine < L && t + skip <= some_hi && t + skip + 32 * kOwn > some_lo)
+                step(base + turn + skip * T::kRowBytes, t + skip);
             if (t + kKeys < to) {
                 turn ^= 2 * kTileBytes;
                 store(turn);
@@ -144,26 +151,66 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves == 4 ? 2 : 1) k_attention(
         }
     }
     const f32x2 both = halves(sum);
-    const float total = both[0] + both[1];
-    // a query that sees no key: total 0, m -infinity
-    store_columns<DT, kD>(a.out, at.begin[0] + i, h, i < L, sq.dim, o, total == 0.0f ? 0.0f : 1.0f / total);
-    if (i < L && half == 0)
+    float total = both[0] + both[1];
+    if constexpr (kSplit) {
+        // Each wave's sums follow the greatest of the waves' maxima, and are added in
+        // the waves' order, a block of elements by one wave.
+        lds_f32* const stats = (lds_f32*)(base + kWaves * kBlocks * 4096);
+        static_assert(kWaves * kBlocks * 4096 + kWaves * 512 <= 4 * kTileBytes, "the shares fit the tiles' memory");
+        __syncthreads();
+#pragma unroll
+        for (int x = 0; x < kBlocks; ++x) share_block(base, kBlocks, wave, x, o[x]);
+        stats[wave * 128 + (threadIdx.x & 63)] = m;
+        stats[wave * 128 + 64 + (threadIdx.x & 63)] = total;
+        __syncthreads();
+        float factor[kWaves];
+        m = -kInf;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) m = fmaxf(m, stats[w * 128 + (threadIdx.x & 63)]);
+        total = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            const float own = stats[w * 128 + (threadIdx.x & 63)];
+            factor[w] = own == -kInf ? 0.0f : __builtin_amdgcn_exp2f(c * (own - m));
+            total = __builtin_fmaf(factor[w], stats[w * 128 + 64 + (threadIdx.x & 63)], total);
+        }
+        if (wave < kBlocks) {
+            f32x16 sum_o = zeros();
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) add_block(base, kBlocks, w, wave, factor[w], sum_o);
+            unsigned short* p = static_cast<unsigned short*>(a.out.p) + (at.begin[0] + i) * a.out.ld + h * a.out.head;
+            store_block<DT>(p, 32 * wave, i < L, sq.dim, sum_o, total == 0.0f ? 0.0f : 1.0f / total);
+        }
+    } else {
+        // a query that sees no key: total 0, m -infinity
+        store_columns<DT, kD>(a.out, at.begin[0] + i, h, i < L, sq.dim, o, total == 0.0f ? 0.0f : 1.0f / total);
+    }
+    if (i < L && half == 0 && (!kSplit || wave == 0))
         a.lse[h * sq.rows[0] + at.begin[0] + i] = total == 0.0f ? -kInf : sq.scale * m + kLn2 * __builtin_amdgcn_logf(total);
 }
 
-template <dp_dtype DT, int kD, int kWaves>
+template <dp_dtype DT, int kD, int kWaves, bool kSplit>
 void launch_one(const AttentionArgs& a, hipStream_t stream) {
-    const dim3 grid(static_cast<unsigned>(attention_slots(a.s, 0, 32 * kWaves) * a.s.heads));
-    if (grid.x > 0) hipLaunchKernelGGL((k_attention<DT, kD, kWaves>), grid, dim3(64 * kWaves), 0, stream, a);
+    const dim3 grid(static_cast<unsigned>(attention_slots(a.s, 0, kSplit ? 32 : 32 * kWaves) * a.s.heads));
+    if (grid.x > 0) hipLaunchKernelGGL((k_attention<DT, kD, kWaves, kSplit>), grid, dim3(64 * kWaves), 0, stream, a);
+}
+
+template <dp_dtype DT, int kD>
+void launch_shape(const AttentionArgs& a, hipStream_t stream) {
+    const AttentionShape shape = attention_shape(a.s, 0, a.s.heads);
+    if (shape == AttentionShape::kSplit) return launch_one<DT, kD, 4, true>(a, stream);
+    if constexpr (kD > 96)
+        if (shape == AttentionShape::kWide) return launch_one<DT, kD, 8, false>(a, stream);
+    launch_one<DT, kD, 4, false>(a, stream);
 }
 
 template <dp_dtype DT>
 void launch_dim(const AttentionArgs& a, hipStream_t stream) {
-    if (a.s.dim <= 32) launch_one<DT, 32, 4>(a, stream);
-    else if (a.s.dim <= 64) launch_one<DT, 64, 4>(a, stream);
-    else if (a.s.dim <= 96) launch_one<DT, 96, 4>(a, stream);
-    else if (attention_wide(a.s)) launch_one<DT, 128, 8>(a, stream);
-    else launch_one<DT, 128, 4>(a, stream);
+    if (a.s.dim <= 32) launch_shape<DT, 32>(a, stream);
+    else if (a.s.dim <= 64) launch_shape<DT, 64>(a, stream);
+    else if (a.s.dim <= 80) launch_shape<DT, 80>(a, stream);
+    else if (a.s.dim <= 96) launch_shape<DT, 96>(a, stream);
+    else launch_shape<DT, 128>(a, stream);
 }
 
 }  // namespace
@@ -173,17 +220,25 @@ int64_t attention_slots(const Sequences& s, int side, int64_t tile) {
     return s.offsets[side] ? s.rows[side] / tile + s.count : s.count * ((s.length[side] + tile - 1) / tile);
 }
 
-// Eight waves in a workgroup load each tile of keys half as often and leave more
-// registers to fragments that are read ahead, but wait for each other twice as
-// many, and their 256 queries cross the mask's edge further.  Heads of 128, four
-// against eight waves, forward and dq, TFLOP/s of their products: sequences of 8192
-// 980 and 1055 against 1038 and 1122, of 4096 874 and 967 against 894 and 1020, of
-// 2048 859 and 849 against 856 and 836.  They have to be enough to fill the CUs.
-bool attention_wide(const Sequences& s) {
-    return s.count > 0 && s.rows[1] / s.count >= 3500 && attention_slots(s, 0, 256) * s.heads >= 512;
+// Workgroups of four waves with 32 rows each (of the queries, or in k_attention_dkv of
+// the keys) but
+//  - where these are fewer than the CUs, four waves with the same 32 rows, which share
+//    what they go over and join at the end;
+//  - eight waves for heads of more than 96 elements and long sequences.  These load each
+//    tile half as often and leave more registers to fragments that are read ahead, but
+//    wait for each other twice as many, and their 256 rows cross the mask's edge further.
+//    Heads of 128, four against eight waves, forward and dq, TFLOP/s of their products:
+//    sequences of 8192 980 and 1055 against 1038 and 1122, of 4096 874 and 967 against
+//    894 and 1020, of 2048 859 and 849 against 856 and 836.  They have to be enough to
+//    fill the CUs.
+AttentionShape attention_shape(const Sequences& s, int side, int heads) {
+    if (attention_slots(s, side, 128) * heads < 256) return AttentionShape::kSplit;
+    const bool wide = s.count > 0 && s.rows[1 - side] / s.count >= 3500 && attention_slots(s, side, 256) * heads >= 512;
+    return wide && s.dim > 96 ? AttentionShape::kWide : AttentionShape::kPlain;
 }
 
 int64_t attention_groups(const Sequences& s) {
+    // (those of 32 rows are taken where these are fewer than 256)
     const int64_t q = attention_slots(s, 0, 128) * s.heads, k = attention_slots(s, 1, 128) * s.heads;
     return q > k ? q : k;
 }

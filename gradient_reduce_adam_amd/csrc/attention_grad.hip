@@ -23,12 +23,13 @@ namespace {
 
 using namespace attn;
 
-constexpr int kKeys = 64;  // of a tile in k_attention_dq
-
-template <dp_dtype DT, int kD, int kWaves>
-__global__ void __launch_bounds__(64 * kWaves, kWaves == 4 ? 2 : 1) k_attention_dq(AttentionArgs a) {
+// kSplit: the four waves have the same 32 queries, and 32 keys each of every tile.
+template <dp_dtype DT, int kD, int kWaves, bool kSplit>
+__global__ void __launch_bounds__(64 * kWaves, kWaves == 4 && !kSplit ? 2 : 1) k_attention_dq(AttentionArgs a) {
     using T = Tile<kD>;
-    constexpr int kTileBytes = kKeys * T::kRowBytes, kRows = 32 * kWaves, kBlocks = kD / 32;
+    constexpr int kRows = kSplit ? 32 : 32 * kWaves, kKeys = kSplit ? 32 * kWaves : 64, kBlocks = (kD + 31) / 32;
+    constexpr int kOwn = kSplit ? 1 : 2;  // times 32 keys of a tile that a wave takes
+    constexpr int kTileBytes = kKeys * T::kRowBytes;
     __shared__ __align__(1024) unsigned char lds[4 * kTileBytes];  // two turns of a k and a v tile
     const Sequences& sq = a.s;
     Place at;
@@ -36,7 +37,7 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves == 4 ? 2 : 1) k_attention_
     const int h = at.head, hk = h / (sq.heads / sq.kv_heads);
     const int L = at.length[0], M = at.length[1], shift = M - L;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = threadIdx.x >> 5 & 1;
-    const int first = at.tile * kRows, mine = first + wave * 32;  // queries of the workgroup, of the wave
+    const int first = at.tile * kRows, mine = first + (kSplit ? 0 : wave * 32);  // queries of the workgroup, of the wave
 
     // The keys that a query sees: [lo, hi].
     const auto lowest = [&](int i) { return sq.window > 0 && i + shift >= sq.window ? i + shift - sq.window + 1 : 0; };
@@ -72,7 +73,7 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves == 4 ? 2 : 1) k_attention_
         const int64_t row = h * sq.rows[0] + at.begin[0] + i;
         const float lse = a.lse[row];
         less = lse == -kInf ? kInf : kLog2e * lse;
-        if (half == 0) a.delta[row] = delta;
+        if (half == 0 && (!kSplit || wave == 0)) a.delta[row] = delta;
     }
     f32x16 o[kBlocks];
 #pragma unroll
@@ -91,11 +92,12 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves == 4 ? 2 : 1) k_attention_
             ks.store(base + turn, sq.dim);
             vs.store(base + turn + kTileBytes, sq.dim);
         };
+        // The wave's keys of a tile, from t on.
         const auto step = [&](const lds_u8* kt, int t) {
             const lds_u8* vt = kt + kTileBytes;
-            const bool masked = t < all_lo || t + kKeys - 1 > all_hi;
+            const bool masked = t < all_lo || t + 32 * kOwn - 1 > all_hi;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
+            for (int j = 0; j < kOwn; ++j) {
                 f32x16 s = zeros(), dp = zeros();
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -134,7 +136,9 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves == 4 ? 2 : 1) k_attention_
         __syncthreads();
         int turn = 0;
         for (int t = from; t < to; t += kKeys) {
-            if (mine < L && t <= some_hi && t + kKeys > some_lo) step(base + turn, t);
+            const int skip = kSplit ? 32 * wave : 0;
+            if (mine < L && t + skip <= some_hi && t + skip + 32 * kOwn > some_lo)
+                step(base + turn + skip * T::kRowBytes, t + skip);
             if (t + kKeys < to) {
                 turn ^= 2 * kTileBytes;
                 store(turn);
@@ -144,15 +148,31 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves == 4 ? 2 : 1) k_attention_
             }
         }
     }
-    store_columns<DT, kD>(a.dq, at.begin[0] + i, h, i < L, sq.dim, o, sq.scale);
+    if constexpr (kSplit) {  // the waves' shares, added in their order
+        static_assert(kWaves * kBlocks * 4096 <= 4 * kTileBytes, "the shares fit the tiles' memory");
+        __syncthreads();
+#pragma unroll
+        for (int x = 0; x < kBlocks; ++x) share_block(base, kBlocks, wave, x, o[x]);
+        __syncthreads();
+        if (wave < kBlocks) {
+            f32x16 sum = zeros();
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) add_block(base, kBlocks, w, wave, 1.0f, sum);
+            unsigned short* p = static_cast<unsigned short*>(a.dq.p) + (at.begin[0] + i) * a.dq.ld + h * a.dq.head;
+            store_block<DT>(p, 32 * wave, i < L, sq.dim, sum, sq.scale);
+        }
+    } else {
+        store_columns<DT, kD>(a.dq, at.begin[0] + i, h, i < L, sq.dim, o, sq.scale);
+    }
 }
 
 // v's fragments are read from LDS for each tile: in registers they would leave too few
 // for two waves a SIMD (heads of 128: 925 us, from LDS 601) or three (of 64).
-template <dp_dtype DT, int kD, int kWaves, int kQueries>
-__global__ void __launch_bounds__(64 * kWaves, kWaves == 8 ? 1 : kD <= 32 ? 4 : kD <= 64 ? 3 : 2) k_attention_dkv(AttentionArgs a) {
+// kSplit: the four waves have the same 32 keys, and 32 queries each of every tile.
+template <dp_dtype DT, int kD, int kWaves, int kQueries, bool kSplit>
+__global__ void __launch_bounds__(64 * kWaves, kWaves == 8 || kSplit ? 1 : kD <= 32 ? 4 : kD <= 64 ? 3 : 2) k_attention_dkv(AttentionArgs a) {
     using T = Tile<kD>;
-    constexpr int kTileBytes = kQueries * T::kRowBytes, kRows = 32 * kWaves, kBlocks = kD / 32;
+    constexpr int kTileBytes = kQueries * T::kRowBytes, kRows = kSplit ? 32 : 32 * kWaves, kBlocks = (kD + 31) / 32;
     constexpr int kTurn = 2 * kTileBytes + 2 * kQueries * 4;  // a q and a dout tile, -lse / scale and -delta of their rows
     constexpr int kValues = kRows * T::kRowBytes;  // v
     __shared__ __align__(1024) unsigned char lds[kValues + 2 * kTurn];
@@ -162,7 +182,7 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves == 8 ? 1 : kD <= 32 ? 4 : 
     const int hk = at.head, group = sq.heads / sq.kv_heads;
     const int L = at.length[0], M = at.length[1], shift = M - L;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = threadIdx.x >> 5 & 1;
-    const int first = at.tile * kRows, mine = first + wave * 32;  // keys of the workgroup, of the wave
+    const int first = at.tile * kRows, mine = first + (kSplit ? 0 : wave * 32);  // keys of the workgroup, of the wave
 
     // The queries that see a key: [lo, hi].
     const auto lowest = [&](int j) { return sq.causal && j - shift > 0 ? j - shift : 0; };
@@ -239,7 +259,7 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves == 8 ? 1 : kD <= 32 ? 4 : 
 #pragma unroll
             for (int n = 0; n < kD / 16; ++n) {
                 s = mma<DT>(T::read_along(qt, along, 0, n), kf[n], s);
-                dp = mma<DT>(T::read_along(dt, along, 0, n), T::read_along((lds_u8*)lds, along, wave, n), dp);
+                dp = mma<DT>(T::read_along(dt, along, 0, n), T::read_along((lds_u8*)lds, along, kSplit ? 0 : wave, n), dp);
             }
             reads<8>();
             ahead<kD / 16, 2, 3, 2>();
@@ -280,7 +300,7 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves == 8 ? 1 : kD <= 32 ? 4 : 
         int turn = 0, t = from;
         for (int i = 0; i < tiles; ++i) {
 #pragma unroll 1
-            for (int r = 0; r < kQueries; r += 32)
+            for (int r = kSplit ? 32 * wave : 0; r < (kSplit ? 32 * wave + 32 : kQueries); r += 32)
                 if (mine < M && t + r <= some_hi && t + r + 32 > some_lo) step(base + turn, r, t + r);
             t = t + kQueries >= to ? from : t + kQueries;
             if (i + 1 < tiles) {
@@ -291,41 +311,67 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves == 8 ? 1 : kD <= 32 ? 4 : 
             }
         }
     }
-    store_columns<DT, kD>(a.dk, at.begin[1] + key, hk, key < M, sq.dim, dk, sq.scale);
-    store_columns<DT, kD>(a.dv, at.begin[1] + key, hk, key < M, sq.dim, dv, 1.0f);
+    if constexpr (kSplit) {  // the waves' shares, added in their order
+        static_assert(2 * kWaves * kBlocks * 4096 <= kValues + 2 * kTurn, "the shares fit the tiles' memory");
+        lds_u8* const at_dk = (lds_u8*)lds;
+        lds_u8* const at_dv = at_dk + kWaves * kBlocks * 4096;
+        __syncthreads();
+#pragma unroll
+        for (int x = 0; x < kBlocks; ++x) {
+            share_block(at_dk, kBlocks, wave, x, dk[x]);
+            share_block(at_dv, kBlocks, wave, x, dv[x]);
+        }
+        __syncthreads();
+        if (wave < kBlocks) {
+            f32x16 sum_k = zeros(), sum_v = zeros();
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) {
+                add_block(at_dk, kBlocks, w, wave, 1.0f, sum_k);
+                add_block(at_dv, kBlocks, w, wave, 1.0f, sum_v);
+            }
+            unsigned short* pk = static_cast<unsigned short*>(a.dk.p) + (at.begin[1] + key) * a.dk.ld + hk * a.dk.head;
+            unsigned short* pv = static_cast<unsigned short*>(a.dv.p) + (at.begin[1] + key) * a.dv.ld + hk * a.dv.head;
+            store_block<DT>(pk, 32 * wave, key < M, sq.dim, sum_k, sq.scale);
+            store_block<DT>(pv, 32 * wave, key < M, sq.dim, sum_v, 1.0f);
+        }
+    } else {
+        store_columns<DT, kD>(a.dk, at.begin[1] + key, hk, key < M, sq.dim, dk, sq.scale);
+        store_columns<DT, kD>(a.dv, at.begin[1] + key, hk, key < M, sq.dim, dv, 1.0f);
+    }
 }
 
-template <dp_dtype DT, int kD, int kWaves>
+template <dp_dtype DT, int kD, int kWaves, bool kSplit>
 void launch_dq(const AttentionArgs& a, hipStream_t stream) {
-    const dim3 grid(static_cast<unsigned>(attention_slots(a.s, 0, 32 * kWaves) * a.s.heads));
-    if (grid.x > 0) hipLaunchKernelGGL((k_attention_dq<DT, kD, kWaves>), grid, dim3(64 * kWaves), 0, stream, a);
+    const dim3 grid(static_cast<unsigned>(attention_slots(a.s, 0, kSplit ? 32 : 32 * kWaves) * a.s.heads));
+    if (grid.x > 0) hipLaunchKernelGGL((k_attention_dq<DT, kD, kWaves, kSplit>), grid, dim3(64 * kWaves), 0, stream, a);
 }
-
-// Heads of 128: eight waves and tiles of 64 queries 546 us for 2 x 4096 rows of 32
-// heads, four waves and 32 queries 573; smaller heads leave room for three waves a
-// SIMD, which four waves fill better (heads of 64, 1024 rows: 143 us against 169).
-template <dp_dtype DT, int kD>
+template <dp_dtype DT, int kD, int kWaves, int kQueries, bool kSplit>
 void launch_dkv(const AttentionArgs& a, hipStream_t stream) {
-    constexpr int kWaves = kD > 96 ? 8 : 4, kQueries = kD > 96 ? 64 : 32;
-    const dim3 grid(static_cast<unsigned>(attention_slots(a.s, 1, 32 * kWaves) * a.s.kv_heads));
-    if (grid.x > 0) hipLaunchKernelGGL((k_attention_dkv<DT, kD, kWaves, kQueries>), grid, dim3(64 * kWaves), 0, stream, a);
+    const dim3 grid(static_cast<unsigned>(attention_slots(a.s, 1, kSplit ? 32 : 32 * kWaves) * a.s.kv_heads));
+    if (grid.x > 0)
+        hipLaunchKernelGGL((k_attention_dkv<DT, kD, kWaves, kQueries, kSplit>), grid, dim3(64 * kWaves), 0, stream, a);
 }
 
+// In k_attention_dkv heads of more than 96 elements take eight waves and tiles of 64
+// queries (2 x 4096 rows of 32 heads of 128: 546 us, four waves and 32 queries 573);
+// smaller ones leave room for three waves a SIMD, which four waves fill better (heads of
+// 64, 1024 rows: 143 us against 169).
 template <dp_dtype DT, int kD>
 void launch_both(const AttentionArgs& a, hipStream_t stream) {
-    if constexpr (kD > 96) {
-        if (attention_wide(a.s)) launch_dq<DT, kD, 8>(a, stream);
-        else launch_dq<DT, kD, 4>(a, stream);
-    } else {
-        launch_dq<DT, kD, 4>(a, stream);
-    }
-    launch_dkv<DT, kD>(a, stream);
+    constexpr bool kLarge = kD > 96;
+    const AttentionShape q = attention_shape(a.s, 0, a.s.heads), k = attention_shape(a.s, 1, a.s.kv_heads);
+    if (q == AttentionShape::kSplit) launch_dq<DT, kD, 4, true>(a, stream);
+    else if (kLarge && q == AttentionShape::kWide) launch_dq<DT, kD, kLarge ? 8 : 4, false>(a, stream);
+    else launch_dq<DT, kD, 4, false>(a, stream);
+    if (k == AttentionShape::kSplit) launch_dkv<DT, kD, 4, 128, true>(a, stream);
+    else launch_dkv<DT, kD, kLarge ? 8 : 4, kLarge ? 64 : 32, false>(a, stream);
 }
 
 template <dp_dtype DT>
 void launch_dim(const AttentionArgs& a, hipStream_t stream) {
     if (a.s.dim <= 32) launch_both<DT, 32>(a, stream);
     else if (a.s.dim <= 64) launch_both<DT, 64>(a, stream);
+    else if (a.s.dim <= 80) launch_both<DT, 80>(a, stream);
     else if (a.s.dim <= 96) launch_both<DT, 96>(a, stream);
     else launch_both<DT, 128>(a, stream);
 }

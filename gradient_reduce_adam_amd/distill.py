@@ -6,6 +6,7 @@ not fit raises ``ValueError``, what the library refuses :class:`DpError`.
 from __future__ import annotations
 
 import ctypes
+import struct
 from dataclasses import dataclass
 
 from . import _check, lib
@@ -41,11 +42,13 @@ class Distillation:
 def _register() -> None:
     vp, i64, c_int = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
     lib.dpd_distill.restype = c_int
-    lib.dpd_distill.argtypes = [ctypes.POINTER(DistillDesc), i64, c_int, vp, i64, c_int, vp, i64, vp, i64, vp, vp, vp, vp,
+    lib.dpd_distill.argtypes = [vp, i64, c_int, vp, i64, c_int, vp, i64, vp, i64, vp, vp, vp, vp,
                                 vp, i64, vp]
 
 
 _register()
+
+_DESC = struct.Struct("ddddqii")
 
 
 def _line(name: str, t, device: int, tokens: int, dtype) -> int:
@@ -76,8 +79,9 @@ def dpd_distill(distillation: Distillation, logits, teacher, ids, loss, dlogits=
     at, ld_d = (None, vocab) if dlogits is None else (dlogits.data_ptr(),
                                                       _rows("dlogits", dlogits, dev, tokens, vocab, logits.dtype))
     f32 = torch.float32
-    desc = DistillDesc(distillation.temperature, distillation.soft, distillation.hard, scale, vocab, top, ids.element_size())
-    _check(lib.dpd_distill(ctypes.byref(desc), tokens, _dtype(logits), logits.data_ptr(), ld, _dtype(teacher),
+    desc = ctypes.create_string_buffer(_DESC.pack(distillation.temperature, distillation.soft, distillation.hard, scale, vocab,
+                                                  top, ids.element_size()))
+    _check(lib.dpd_distill(ctypes.addressof(desc), tokens, _dtype(logits), logits.data_ptr(), ld, _dtype(teacher),
                            teacher.data_ptr(), ld_teacher, ids.data_ptr(), ld_ids, _line("total", total, dev, tokens, f32),
                            _line("labels", labels, dev, tokens, ids.dtype), _line("weight", weight, dev, tokens, f32),
                            _line("loss", loss, dev, tokens, f32), at, ld_d, _stream_of(stream, dev)))

@@ -158,6 +158,17 @@ def test_thousands_of_sequences():
     c.check(**c.places())
 
 
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 50)])
+@pytest.mark.parametrize("D", [16, 32, 64, 72, 80, 96, 104, 128])
+def test_more_tiles_than_cus(D, causal, window):
+    """Where workgroups are many, each wave has rows of its own."""
+    c = Case(cut(5, 0, 128, 1, 0, 0, 77, 129, 64, 33), 48, 24, D, "bf16" if D % 32 else "f16", seed=D, causal=causal, window=window,
+             T=480, layout="rows")
+    c.check(**c.places())
+    c = Case(cut(160, 160, 160), 96, 96, D, "bf16", seed=D, causal=causal, window=window)
+    c.check(sequences=3)
+
+
 @pytest.mark.parametrize("L,M,H,D,causal,window", [(100, 3501, 512, 104, True, 0), (257, 3700, 256, 128, True, 700),
                                                     (300, 3600, 256, 128, False, 0), (3600, 3600, 40, 112, True, 0)])
 def test_long_sequences(L, M, H, D, causal, window):
