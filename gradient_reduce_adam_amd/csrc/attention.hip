@@ -197,7 +197,7 @@ void launch_one(const AttentionArgs& a, hipStream_t stream) {
 
 template <dp_dtype DT, int kD>
 void launch_shape(const AttentionArgs& a, hipStream_t stream) {
-    const AttentionShape shape = attention_shape(a.s, 0, a.s.heads);
+    const AttentionShape shape = attention_shape(a.s, 0);
     if (shape == AttentionShape::kSplit) return launch_one<DT, kD, 4, true>(a, stream);
     if constexpr (kD > 96)
         if (shape == AttentionShape::kWide) return launch_one<DT, kD, 8, false>(a, stream);
@@ -222,8 +222,13 @@ int64_t attention_slots(const Sequences& s, int side, int64_t tile) {
 
 // Workgroups of four waves with 32 rows each (of the queries, or in k_attention_dkv of
 // the keys) but
-//  - where these are fewer than the CUs, four waves with the same 32 rows, which share
-//    what they go over and join at the end;
+//  - where these are too few for the CUs, four waves with the same 32 rows, which share
+//    what they go over and join at the end.  Their tiles are larger, so that one (heads
+//    of more than 64 elements) or two of them fit a CU, and are read for fewer rows.
+//    Plain against split, us, one sequence: 8 heads of 64, 2048 rows (128 workgroups of
+//    four waves) forward 30 and 21, dk and dv 60 and 30; 16 heads (256) 31 and 32, 61 and
+//    43; 16 heads, 4096 rows (512) 63 and 87, 123 and 129.  Heads of 128: 8 heads, 2048
+//    rows 44 and 35, 108 and 56; 16 heads 46 and 68, 110 and 104.
 //  - eight waves for heads of more than 96 elements and long sequences.  These load each
 //    tile half as often and leave more registers to fragments that are read ahead, but
 //    wait for each other twice as many, and their 256 rows cross the mask's edge further.
@@ -231,14 +236,16 @@ int64_t attention_slots(const Sequences& s, int side, int64_t tile) {
 //    sequences of 8192 980 and 1055 against 1038 and 1122, of 4096 874 and 967 against
 //    894 and 1020, of 2048 859 and 849 against 856 and 836.  They have to be enough to
 //    fill the CUs.
-AttentionShape attention_shape(const Sequences& s, int side, int heads) {
-    if (attention_slots(s, side, 128) * heads < 256) return AttentionShape::kSplit;
+AttentionShape attention_shape(const Sequences& s, int side) {
+    const int heads = side == 0 ? s.heads : s.kv_heads;
+    const int64_t groups = attention_slots(s, side, 128) * heads;
+    if (groups < (side == 0 ? (s.dim > 64 ? 160 : 256) : (s.dim > 64 ? 256 : 448))) return AttentionShape::kSplit;
     const bool wide = s.count > 0 && s.rows[1 - side] / s.count >= 3500 && attention_slots(s, side, 256) * heads >= 512;
     return wide && s.dim > 96 ? AttentionShape::kWide : AttentionShape::kPlain;
 }
 
 int64_t attention_groups(const Sequences& s) {
-    // (those of 32 rows are taken where these are fewer than 256)
+    // (those of 32 rows are taken only where these are few)
     const int64_t q = attention_slots(s, 0, 128) * s.heads, k = attention_slots(s, 1, 128) * s.heads;
     return q > k ? q : k;
 }

@@ -359,7 +359,7 @@ void launch_dkv(const AttentionArgs& a, hipStream_t stream) {
 template <dp_dtype DT, int kD>
 void launch_both(const AttentionArgs& a, hipStream_t stream) {
     constexpr bool kLarge = kD > 96;
-    const AttentionShape q = attention_shape(a.s, 0, a.s.heads), k = attention_shape(a.s, 1, a.s.kv_heads);
+    const AttentionShape q = attention_shape(a.s, 0), k = attention_shape(a.s, 1);
     if (q == AttentionShape::kSplit) launch_dq<DT, kD, 4, true>(a, stream);
     else if (kLarge && q == AttentionShape::kWide) launch_dq<DT, kD, kLarge ? 8 : 4, false>(a, stream);
     else launch_dq<DT, kD, 4, false>(a, stream);
