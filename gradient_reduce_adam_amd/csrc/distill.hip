@@ -34,37 +34,69 @@ __device__ __forceinline__ int64_t load_id(int bytes, const void* p, int64_t i) 
 }
 
 // One row's logits in pieces of 16 bytes at aligned addresses: piece i holds the
-// logits kN i - shift + 0 .. kN - 1, those outside the row as -infinity.
-template <dp_dtype DT>
+// logits kN i - shift + 0 .. kN - 1, those outside the row as -infinity.  A piece that
+// the row's ends cut short is loaded from inside the row and moved into place when
+// it is used (`settle`), so that no load lies behind a branch that waits for it.
+// kTiny: a row shorter than a piece, element by element.
+template <dp_dtype DT, bool kTiny>
 struct Row {
-    static constexpr int kN = DT == DP_F32 ? 4 : 8;
+    static constexpr int kN = DT == DP_F32 ? 4 : 8, kSize = 16 / kN;
+    typedef Raw<DT, kN> Piece;
     const char* p;
     int shift, vocab, pieces;
 
     __device__ __forceinline__ Row(const void* logits, int64_t row, int64_t ld, int64_t v) {
-        constexpr int kSize = DT == DP_F32 ? 4 : 2;
         p = static_cast<const char*>(logits) + row * ld * kSize;
-        shift = static_cast<int>(reinterpret_cast<uintptr_t>(p) / kSize % kN);
+        shift = kTiny ? 0 : static_cast<int>(reinterpret_cast<uintptr_t>(p) / kSize % kN);
         vocab = static_cast<int>(v);
         pieces = (vocab + shift + kN - 1) / kN;
     }
-    __device__ __forceinline__ Raw<DT, kN> load(int i) const {
-        Raw<DT, kN> q;
-        const int at = i * kN - shift;
-        if (at >= 0 && at + kN <= vocab) {
-            const u32x4 v = gload<u32x4>(p + static_cast<int64_t>(at) * (16 / kN), 0);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) q.w[j] = v[j];
-        } else {
+    // -infinity in every element of a word
+    static constexpr unsigned int kNone = DT == DP_F32 ? 0xff800000u : DT == DP_F16 ? 0xfc00fc00u : 0xff80ff80u;
+    __device__ __forceinline__ Piece load(int i) const {  // past the last piece: that one
+        Piece q;
+        if constexpr (kTiny) {
             float x[kN];
 #pragma unroll
-            for (int j = 0; j < kN; ++j) x[j] = at + j >= 0 && at + j < vocab ? load1<DT>(p, at + j) : -kInf;
+            for (int j = 0; j < kN; ++j) x[j] = j < vocab ? load1<DT>(p, j) : -kInf;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 q.w[j] = DT == DP_F32 ? __builtin_bit_cast(unsigned int, x[j * kN / 4])
                                       : pack2<DT == DP_F32 ? DP_BF16 : DT>(x[j * kN / 4], x[j * kN / 4 + kN / 8]);
+        } else {
+            int at = (i < pieces ? i : pieces - 1) * kN - shift;
+            at = at < 0 ? 0 : at > vocab - kN ? vocab - kN : at;
+            const u32x4 v = gload<u32x4, kSize>(p + static_cast<int64_t>(at) * kSize, 0);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) q.w[j] = v[j];
         }
         return q;
+    }
+    __device__ __forceinline__ void settle(int i, Piece& q) const {
+        if (i > 0 && i < pieces - 1) return;
+        const int at = i * kN - shift;
+        if (kTiny || i >= pieces) {
+            if (i >= pieces)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) q.w[j] = kNone;
+            return;
+        }
+        // by how many elements the piece was loaded too late (the first one) or too early
+        const int up = at < 0 ? -at : 0, down = at > vocab - kN ? at - (vocab - kN) : 0;
+        constexpr int kWord = DT == DP_F32 ? 1 : 2;  // elements
+        unsigned int* w = q.w;
+        if (down & (2 * kWord)) w[0] = w[2], w[1] = w[3], w[2] = w[3] = kNone;
+        if (down & kWord) w[0] = w[1], w[1] = w[2], w[2] = w[3], w[3] = kNone;
+        if (up & (2 * kWord)) w[3] = w[1], w[2] = w[0], w[0] = w[1] = kNone;
+        if (up & kWord) w[3] = w[2], w[2] = w[1], w[1] = w[0], w[0] = kNone;
+        if constexpr (kWord == 2) {
+            if (down & 1)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w[j] = __builtin_amdgcn_alignbit(j < 3 ? w[j + 1] : kNone, w[j], 16);
+            if (up & 1)
+#pragma unroll
+                for (int j = 3; j >= 0; --j) w[j] = __builtin_amdgcn_alignbit(w[j], j > 0 ? w[j - 1] : kNone, 16);
+        }
     }
     __device__ __forceinline__ void store(void* out, int i, const float* x) const {
         const int at = i * kN - shift;
@@ -78,10 +110,15 @@ struct Row {
     }
 };
 
-// kKept pieces of a row in a thread's registers; 0: the row is read for each pass.
+constexpr int kStream = 0, kTinyRow = -1;
+
+// kKept pieces of a row in a thread's registers; kStream: the row is read piece by
+// piece, once for the sums, which follow each thread's greatest logit, and once for
+// the gradient; kTinyRow: one piece, read element by element.
 template <dp_dtype DT, int kThreads, int kKept>
 __global__ void __launch_bounds__(kThreads) k_distill(DistillArgs a, dp_dtype teacher_dt) {
-    using R = Row<DT>;
+    using R = Row<DT, kKept == kTinyRow>;
+    constexpr int kPieces = kKept == kTinyRow ? 1 : kKept;
     constexpr int kN = R::kN, kWaves = kThreads / 64, kSums = 5;
     extern __shared__ unsigned int dyn[];
     __shared__ float tops[2][kWaves], sums[kSums][kWaves];
@@ -110,8 +147,7 @@ __global__ void __launch_bounds__(kThreads) k_distill(DistillArgs a, dp_dtype te
         list = fmaxf(list, there ? y : -kInf);
     }
     const R row(a.logits, t, a.ld, a.vocab);
-    constexpr int kSize = DT == DP_F32 ? 4 : 2;
-    char* const out = a.dlogits ? static_cast<char*>(a.dlogits) + t * a.ld_dlogits * kSize : nullptr;
+    char* const out = a.dlogits ? static_cast<char*>(a.dlogits) + t * a.ld_dlogits * R::kSize : nullptr;
     if (weight == 0.0f) {
         if (a.loss && tid == 0) gstore<float>(a.loss, t, 0.0f);
         float x[kN];
@@ -123,37 +159,110 @@ __global__ void __launch_bounds__(kThreads) k_distill(DistillArgs a, dp_dtype te
     }
 
     // 1. the row, its logits of the list, and the greatest of both
-    Raw<DT, kN> kept[kKept > 0 ? kKept : 1];
+    typename R::Piece kept[kPieces > 0 ? kPieces : 1];
 #pragma unroll
-    for (int k = 0; k < kKept; ++k)
-        if (k * kThreads + tid < row.pieces) kept[k] = row.load(k * kThreads + tid);
+    for (int k = 0; k < kPieces; ++k)
+        if (k * kThreads < row.pieces) kept[k] = row.load(k * kThreads + tid);
     const int label = y_label >= 0 && y_label < a.vocab ? static_cast<int>(y_label) : -1;
     const float target = label >= 0 ? load1<DT>(row.p, label) : 0.0f;
     for (int k = tid; k < K; k += kThreads) student[k] = ids[k] >= 0 ? load1<DT>(row.p, ids[k]) : 0.0f;
     const auto each = [&](auto&& use) {  // use(piece, its logits)
-        if constexpr (kKept > 0) {
+        if constexpr (kKept != kStream) {
 #pragma unroll
-            for (int k = 0; k < kKept; ++k) {
-                if (k * kThreads + tid < row.pieces) {
+            for (int k = 0; k < kPieces; ++k) {
+                if (k * kThreads < row.pieces) {
                     float x[kN];
                     expand<DT, kN>(kept[k], x);
                     use(k * kThreads + tid, x);
                 }
             }
         } else {
-            for (int i = tid; i < row.pieces; i += kThreads) {
-                float x[kN];
-                expand<DT, kN>(row.load(i), x);
-                use(i, x);
+            constexpr int kAhead = 4;  // pieces on their way together
+            for (int i = 0; i < row.pieces; i += kAhead * kThreads) {
+                typename R::Piece q[kAhead];
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) q[k] = row.load(i + k * kThreads + tid);
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    float x[kN];
+                    row.settle(i + k * kThreads + tid, q[k]);
+                    expand<DT, kN>(q[k], x);
+                    use(i + k * kThreads + tid, x);
+                }
             }
         }
     };
     for (int i = tid; i < (row.vocab + row.shift + 31) / 32; i += kThreads) bits[i] = 0;
-    float top = -kInf;
-    each([&](int, const float* x) {
+    bool twice = false;
+    const auto mark = [&]() {
+        for (int k = tid; k < K; k += kThreads)
+            if (ids[k] >= 0) {
+                const int at = ids[k] + row.shift;
+                twice |= (atomicOr(&bits[at >> 5], 1u << (at & 31)) >> (at & 31) & 1) != 0;
+            }
+    };
+    // Exponentials are 2^(z c - peak), peak = top c as rounded: a row's reference, which
+    // log_all and the label's term take it for, so its rounding cancels.
+    const bool both = a.hard != 0.0f && a.temperature != 1.0f, square = a.temperature == 2.0f;
+    const float c = kLog2e * heat;
+    float s[kSums] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    // A piece's part of the sums of the row at both temperatures, and of the tokens
+    // outside the list.  At 2 the exponential without the temperature is the square.
+    const auto add = [&](int i, const float* x, float peak, float peak1) {
+        float e[kN];
 #pragma unroll
-        for (int j = 0; j < kN; ++j) top = fmaxf(top, x[j]);
-    });
+        for (int j = 0; j < kN; ++j) {
+            e[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[j], c, -peak));
+            s[0] += e[j];
+        }
+        if (rest) {
+            const unsigned int listed = bits[(i < row.pieces ? i : 0) * kN >> 5] >> (i * kN & 31);
+#pragma unroll
+            for (int j = 0; j < kN; ++j) s[1] += listed >> j & 1 ? 0.0f : e[j];
+        }
+        if (both) {
+            if (square) {
+#pragma unroll
+                for (int j = 0; j < kN; ++j) s[2] = __builtin_fmaf(e[j], e[j], s[2]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < kN; ++j) s[2] += __builtin_amdgcn_exp2f(__builtin_fmaf(x[j], kLog2e, -peak1));
+            }
+        }
+    };
+    float top = -kInf, own = -kInf, own1 = -kInf;  // own: the thread's reference while it streams
+    if constexpr (kKept == kStream) {
+        if (rest) {
+            __syncthreads();
+            mark();
+            __syncthreads();
+        }
+        each([&](int i, const float* x) {
+            float high = x[0];
+#pragma unroll
+            for (int j = 1; j < kN; ++j) high = fmaxf(high, x[j]);
+            if (high > top) {
+                top = high;
+                const float peak = top * c, peak1 = square ? 2.0f * peak : top * kLog2e;
+                const float less = __builtin_amdgcn_exp2f(own - peak);
+                s[0] *= less;
+                s[1] *= less;
+                s[2] *= __builtin_amdgcn_exp2f(own1 - peak1);
+                own = peak;
+                own1 = peak1;
+            }
+            // nothing but -infinity yet: any reference gives zeros
+            add(i, x, own == -kInf ? 0.0f : own, own1 == -kInf ? 0.0f : own1);
+        });
+    } else {
+#pragma unroll
+        for (int k = 0; k < kPieces; ++k)
+            if (k * kThreads < row.pieces && (k == 0 || (k + 1) * kThreads >= row.pieces)) row.settle(k * kThreads + tid, kept[k]);
+        each([&](int, const float* x) {
+#pragma unroll
+            for (int j = 0; j < kN; ++j) top = fmaxf(top, x[j]);
+        });
+    }
     top = wave_max(top);
     list = wave_max(list);
     if ((tid & 63) == 0) {
@@ -166,46 +275,22 @@ __global__ void __launch_bounds__(kThreads) k_distill(DistillArgs a, dp_dtype te
         top = fmaxf(top, tops[0][w]);
         list = fmaxf(list, tops[1][w]);
     }
-    bool twice = false;
-    for (int k = tid; k < K; k += kThreads)
-        if (ids[k] >= 0) {
-            const int at = ids[k] + row.shift;
-            twice |= (atomicOr(&bits[at >> 5], 1u << (at & 31)) >> (at & 31) & 1) != 0;
-        }
+    if (kKept != kStream || !rest) mark();
     twice = __syncthreads_or(twice);
 
-    // 2. the sums: of the row at both temperatures, of the tokens outside the list,
-    // and of the list's probabilities and their products with log p / q
-    // Exponentials are 2^(z c - peak), peak = top c as rounded: a row's reference, which
-    // log_all and the label's term take it for, so its rounding cancels.
-    const float c = kLog2e * heat, peak = top * c, peak1 = a.temperature == 2.0f ? 2.0f * peak : top * kLog2e;
-    const bool both = a.hard != 0.0f && a.temperature != 1.0f, square = a.temperature == 2.0f;
-    // the same without the temperature, from that with it: at 2 it is the square
+    // 2. the sums, and those of the list's probabilities and of their products with
+    // log p / q
+    const float peak = top * c, peak1 = square ? 2.0f * peak : top * kLog2e;
     const auto plain = [&](float z, float e) { return square ? e * e : __builtin_amdgcn_exp2f(__builtin_fmaf(z, kLog2e, -peak1)); };
     const float base = rest ? total : list == -kInf ? 0.0f : list;
-    float s[kSums] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    each([&](int i, const float* x) {
-        float e[kN];
-#pragma unroll
-        for (int j = 0; j < kN; ++j) {
-            e[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[j], c, -peak));
-            s[0] += e[j];
-        }
-        if (rest) {
-            const unsigned int listed = bits[i * kN >> 5] >> (i * kN & 31);
-#pragma unroll
-            for (int j = 0; j < kN; ++j) s[1] += listed >> j & 1 ? 0.0f : e[j];
-        }
-        if (both) {
-            if (square) {
-#pragma unroll
-                for (int j = 0; j < kN; ++j) s[2] = __builtin_fmaf(e[j], e[j], s[2]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < kN; ++j) s[2] += plain(x[j], 0.0f);
-            }
-        }
-    });
+    if constexpr (kKept == kStream) {
+        const float less = __builtin_amdgcn_exp2f(own - peak), less1 = __builtin_amdgcn_exp2f(own1 - peak1);
+        s[0] *= less;
+        s[1] *= less;
+        s[2] *= less1;
+    } else {
+        each([&](int i, const float* x) { add(i, x, peak, peak1); });
+    }
     for (int k = tid; k < K; k += kThreads) {
         if (ids[k] < 0) continue;
         const float y = teacher[k] - base, p = __builtin_amdgcn_exp2f(y * kLog2e);
@@ -266,7 +351,7 @@ __global__ void __launch_bounds__(kThreads) k_distill(DistillArgs a, dp_dtype te
                 for (int j = 0; j < kN; ++j) g[j] = __builtin_fmaf(plain(x[j], 0.0f), hard, g[j]);
             }
         }
-        row.store(out, i, g);
+        if (i < row.pieces) row.store(out, i, g);
     });
     __syncthreads();
     const auto again = [&](int id, float z, float p, float coefficient) {
@@ -308,23 +393,28 @@ hipError_t go(const DistillArgs& a, dp_dtype teacher_dt, hipStream_t stream) {
 
 // The smallest number of registers that holds a row.  Many rows hide each other's
 // waits, so small workgroups, of which three or four are on a CU at once, take them:
-// 16384 x 32000 bf16 logits with their gradient 400 us by 256 threads a row, 446 to
-// 680 by 1024.  Up to one row a CU, a row has all threads that a workgroup can have.
+// 16384 x 32000 bf16 logits with their gradient 390 us by 512 threads a row, 398 by 256,
+// 446 to 680 by 1024.  Up to one row a CU, a row has all threads that a workgroup can have.
+// Many rows' losses alone need no row twice and are streamed: 4096 x 50257 in binary32 139
+// us by 1024 threads a row and 163 by 256, from registers 187; 16384 x 32000 bf16 302, 207
+// and 214.
 template <dp_dtype DT>
 hipError_t launch_row(const DistillArgs& a, dp_dtype teacher_dt, hipStream_t stream) {
-    constexpr int kN = Row<DT>::kN;
+    constexpr int kN = DT == DP_F32 ? 4 : 8;
+    if (a.vocab < kN) return go<DT, 64, kTinyRow>(a, teacher_dt, stream);
     const int64_t pieces = (a.vocab + kN - 1 + kN - 1) / kN;  // at any alignment
     if (a.tokens > 256) {
         if (pieces <= 256 * 4) return go<DT, 256, 4>(a, teacher_dt, stream);
+        if (!a.dlogits) return pieces <= 1024 * 8 ? go<DT, 256, kStream>(a, teacher_dt, stream) : go<DT, 1024, kStream>(a, teacher_dt, stream);
         if (pieces <= 256 * 8) return go<DT, 256, 8>(a, teacher_dt, stream);
-        if (pieces <= 256 * 16) return go<DT, 256, 16>(a, teacher_dt, stream);
+        if (pieces <= 512 * 8) return go<DT, 512, 8>(a, teacher_dt, stream);
         if (pieces <= 512 * 13) return go<DT, 512, 13>(a, teacher_dt, stream);
     }
     if (pieces <= 1024 * 2) return go<DT, 1024, 2>(a, teacher_dt, stream);
     if (pieces <= 1024 * 7) return go<DT, 1024, 7>(a, teacher_dt, stream);
     if (pieces <= 1024 * 13) return go<DT, 1024, 13>(a, teacher_dt, stream);
     if (pieces <= 1024 * 16) return go<DT, 1024, 16>(a, teacher_dt, stream);
-    return go<DT, 1024, 0>(a, teacher_dt, stream);
+    return go<DT, 1024, kStream>(a, teacher_dt, stream);
 }
 
 }  // namespace

@@ -47,6 +47,7 @@ struct RotaryArgs {
     int64_t position_ld, position_axis, tokens;
     int32_t position_bytes, count, dim, pairs;
     bool interleaved, inverse;
+    bool once;  // what is written passes the caches
 };
 hipError_t launch_rotary(dp_dtype dt, const RotaryArgs& a, hipStream_t stream);
 

@@ -159,6 +159,24 @@ def test_many_rows(V, dt):
     assert torch.equal(c.logits, grad)
 
 
+@pytest.mark.parametrize("V,dt", [(1031, "f32"), (9001, "bf16"), (33333, "f32"), (40009, "f32"), (50257, "f16")])
+@pytest.mark.parametrize("tau,hard,tail", [(1.0, 0.0, False), (2.0, 0.5, True), (0.7, 0.5, True), (1.0, 1.0, True)])
+def test_losses_of_many_rows(V, dt, tau, hard, tail):
+    """Without a gradient rows are read once, piece by piece, with sums that follow the greatest logit so far: also
+    where it comes last, and behind nothing but -infinity."""
+    c = Case(260, V, 9, dt, tau=tau, soft=0.7, hard=hard, tail=tail, seed=V, weight=tail)
+    ramp = torch.linspace(-30, 30, V, device="cuda").to(c.logits.dtype)
+    c.logits[0], c.logits[1] = ramp, ramp.flip(0)
+    c.logits[2, :V - 700] = -INF
+    c.ids[2] = torch.arange(V - 9, V, device="cuda").to(c.ids.dtype)
+    if c.labels is not None:
+        c.labels[2] = V - 3
+    loss, lb, _, _ = c.want()
+    c.call(grad=False)
+    err = (c.loss.double().cpu() - loss).abs()
+    assert torch.isfinite(c.loss).all() and (err <= lb).all(), (err / lb).max().item()
+
+
 @pytest.mark.parametrize("tau", [0.25, 1.0, 2.0, 3.0])
 @pytest.mark.parametrize("tail", [False, True])
 @pytest.mark.parametrize("soft,hard", [(1.0, 0.0), (0.0, 1.0), (0.6, 0.4), (-0.5, 2.0)])

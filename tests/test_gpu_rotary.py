@@ -79,6 +79,23 @@ def test_tokens(T):
     check(r, at, x, y, "f32")
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("pairs,D,dt", [(16, 40, "bf16"), (19, 40, "f32")])
+def test_outputs_beyond_the_caches(pairs, D, dt, interleaved):
+    """More than 64 MiB are written with streaming stores."""
+    T, H = 70000, 17
+    r = dp.Rotary((pairs,), interleaved=interleaved)
+    at = torch.arange(T, device="cuda", dtype=torch.int32)
+    x = rows(T, H, D, dt, pairs)
+    y = torch.empty_like(x)
+    dp.dpa_rotary(r, at, x, y)
+    for part in (slice(0, 500), slice(T - 500, T)):
+        check(r, at[part], x[part], y[part], dt)
+    dp.dpa_rotary(r, at, y, y, inverse=True)
+    back = U[dt] * 4 + 64 * 2.0 ** -24
+    assert ((y.float() - x.float()).abs().max() <= back * x.float().abs().max() * 2).item()
+
+
 def test_far_positions_keep_their_phase():
     r = dp.Rotary((16, 16), 500000.0)
     at = torch.tensor([[2 ** 31 - 1, -2 ** 31], [10 ** 6, 2 ** 24 + 1], [2 ** 33 + 3, 12345678]]).cuda()
@@ -114,6 +131,15 @@ def test_a_row_and_a_head_that_repeat_and_positions_of_one_value():
     r = dp.Rotary((16,))
     dp.dpa_rotary(r, at, x, y)
     check(r, at, x, y, "bf16")
+
+
+def test_no_pairs():
+    x = rows(9, 2, 20, "f16", 5)
+    y, at = torch.zeros_like(x), torch.arange(9, device="cuda")
+    dp.dpa_rotary(dp.Rotary((0,)), at, x, y)
+    assert torch.equal(x, y)
+    dp.dpa_rotary(dp.Rotary((0,)), at, x, x)
+    assert torch.equal(x, y)
 
 
 def test_captured():
