@@ -62,6 +62,17 @@ __device__ __forceinline__ u32x4 pack8(const f32x16& x, int s) {
                  pack2<DT>(x[8 * s + 4], x[8 * s + 5]), pack2<DT>(x[8 * s + 6], x[8 * s + 7])};
 }
 
+// -infinity in the rows of a product behind `last`, or before `first` (of the lane's
+// rows 8 (e / 4) + e % 4).
+__device__ __forceinline__ void hide_behind(f32x16& x, int last) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) x[e] = 8 * (e >> 2) + (e & 3) > last ? -kInf : x[e];
+}
+__device__ __forceinline__ void hide_before(f32x16& x, int first) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) x[e] = 8 * (e >> 2) + (e & 3) < first ? -kInf : x[e];
+}
+
 // {x of the lower half's lane, x of the upper half's} of the two lanes that share
 // a column, in both of them.
 __device__ __forceinline__ f32x2 halves(float x) {
@@ -244,6 +255,31 @@ __device__ __forceinline__ void add_block(const lds_u8* at, int blocks, int wave
         const f32x4 v = *(const lds_f32x4*)(at + ((wave * blocks + b) * 4 + g) * 1024 + 16 * (threadIdx.x & 63));
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[4 * g + e] = __builtin_fmaf(factor, v[e], x[4 * g + e]);
+    }
+}
+
+// The two waves of a pair (2 i and 2 i + 1) join their shares of a sum, a block of 32
+// elements each at a time, the even one the even blocks: use(block, its sum).  Each
+// wave's share counts `own` times, the other's `other` times.
+template <int kBlocks, typename Use>
+__device__ __forceinline__ void join_pairs(lds_u8* at, int wave, float own, float other, const f32x16* o, Use&& use) {
+    const bool odd = wave & 1;
+#pragma unroll
+    for (int x = 0; x < kBlocks; x += 2) {
+        const f32x16 even_block = o[x], odd_block = o[x + 1 < kBlocks ? x + 1 : x];
+        f32x16 sum, give;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            sum[e] = own * (odd ? odd_block[e] : even_block[e]);
+            give[e] = odd ? even_block[e] : odd_block[e];
+        }
+        __syncthreads();
+        share_block(at, 1, wave, 0, give);
+        __syncthreads();
+        if (x + odd < kBlocks) {
+            add_block(at, 1, wave ^ 1, 0, other, sum);
+            use(x + odd, sum);
+        }
     }
 }
 

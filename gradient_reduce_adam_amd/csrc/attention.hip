@@ -7,7 +7,8 @@
 //   p = exp2(c S - c m), c = scale log2(e), m a running maximum of the query
 //   out^T += v^T p     p goes into the product from the registers it is in
 // with v^T read by the transposing LDS load, and sums and maxima kept by each lane.
-// Few queries: the waves have the same 32, and share the keys of a tile.
+// Few queries: two or all four of the waves have the same 32, and share the keys of a
+// tile.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -18,21 +19,25 @@ namespace {
 
 using namespace attn;
 
-// kSplit: the four waves have the same 32 queries, and 32 keys each of every tile.
-template <dp_dtype DT, int kD, int kWaves, bool kSplit>
-__global__ void __launch_bounds__(64 * kWaves, kWaves == 4 && !kSplit ? 2 : 1) k_attention(AttentionArgs a) {
+// kShare: so many neighbouring waves have the same 32 queries, and 32 keys each of
+// every tile; with 1 a wave takes all 64 keys.
+template <dp_dtype DT, int kD, int kWaves, int kShare>
+__global__ void __launch_bounds__(64 * kWaves, kWaves == 4 && kShare == 1 ? 2 : 1) k_attention(AttentionArgs a) {
     using T = Tile<kD>;
-    constexpr int kRows = kSplit ? 32 : 32 * kWaves, kKeys = kSplit ? 32 * kWaves : 64, kBlocks = (kD + 31) / 32;
-    constexpr int kOwn = kSplit ? 1 : 2;  // times 32 keys of a tile that a wave takes
+    constexpr int kRows = 32 * kWaves / kShare, kKeys = kShare == 1 ? 64 : 32 * kShare, kBlocks = (kD + 31) / 32;
+    constexpr int kOwn = kShare == 1 ? 2 : 1;  // times 32 keys of a tile that a wave takes
     constexpr int kTileBytes = kKeys * T::kRowBytes;
-    __shared__ __align__(1024) unsigned char lds[4 * kTileBytes];  // two turns of a k and a v tile
+    // two turns of a k and a v tile; then, where waves share queries, their sums and maxima
+    constexpr int kShares = kShare == 1 ? 0 : kWaves * (kShare == 4 ? kBlocks : 1) * 4096;
+    constexpr int kBytes = 4 * kTileBytes > kShares + kWaves * 512 ? 4 * kTileBytes : kShares + kWaves * 512;
+    __shared__ __align__(1024) unsigned char lds[kBytes];
     const Sequences& sq = a.s;
     Place at;
     if (!find<kRows>(sq, 0, sq.heads, sq.causal, at)) return;
     const int h = at.head, hk = h / (sq.heads / sq.kv_heads);
     const int L = at.length[0], M = at.length[1], shift = M - L;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = threadIdx.x >> 5 & 1;
-    const int first = at.tile * kRows, mine = first + (kSplit ? 0 : wave * 32);  // queries of the workgroup, of the wave
+    const int first = at.tile * kRows, mine = first + wave / kShare * 32;  // queries of the workgroup, of the wave
 
     // The keys that a query sees: [lo, hi].
     const auto lowest = [&](int i) { return sq.window > 0 && i + shift >= sq.window ? i + shift - sq.window + 1 : 0; };
@@ -77,16 +82,13 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves == 4 && !kSplit ? 2 : 1) k
 #pragma unroll
                 for (int n = 0; n < kD / 16; ++n) s[j] = mma<DT>(T::read_along(kt, along, j, n), qf[n], s[j]);
             ahead<kOwn * (kD / 16), 1, 1, 6>();
-            if (t < all_lo || t + 32 * kOwn - 1 > all_hi) {  // scores that do not count
-                const int up = hi - t - 4 * half, down = lo - t - 4 * half;
+            // scores that do not count
+            if (t + 32 * kOwn - 1 > all_hi)
 #pragma unroll
-                for (int j = 0; j < kOwn; ++j)
+                for (int j = 0; j < kOwn; ++j) hide_behind(s[j], hi - t - 32 * j - 4 * half);
+            if (t < all_lo)
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const int key = 32 * j + 8 * (e >> 2) + (e & 3);
-                        s[j][e] = key > up || key < down ? -kInf : s[j][e];
-                    }
-            }
+                for (int j = 0; j < kOwn; ++j) hide_before(s[j], lo - t - 32 * j - 4 * half);
             float top = s[0][0];
 #pragma unroll
             for (int j = 0; j < kOwn; ++j)
@@ -138,7 +140,7 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves == 4 && !kSplit ? 2 : 1) k
         __syncthreads();
         int turn = 0;
         for (int t = from; t < to; t += kKeys) {
-            const int skip = kSplit ? 32 * wave : 0;
+            const int skip = 32 * (wave % kShare);
             if (mine < L && t + skip <= some_hi && t + skip + 32 * kOwn > some_lo)
                 step(base + turn + skip * T::kRowBytes, t + skip);
             if (t + kKeys < to) {
@@ -152,11 +154,11 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves == 4 && !kSplit ? 2 : 1) k
     }
     const f32x2 both = halves(sum);
     float total = both[0] + both[1];
-    if constexpr (kSplit) {
+    if constexpr (kShare == 4) {
         // Each wave's sums follow the greatest of the waves' maxima, and are added in
         // the waves' order, a block of elements by one wave.
-        lds_f32* const stats = (lds_f32*)(base + kWaves * kBlocks * 4096);
-        static_assert(kWaves * kBlocks * 4096 + kWaves * 512 <= 4 * kTileBytes, "the shares fit the tiles' memory");
+        static_assert(kBlocks <= kWaves, "a block of elements for each wave");
+        lds_f32* const stats = (lds_f32*)(base + kShares);
         __syncthreads();
 #pragma unroll
         for (int x = 0; x < kBlocks; ++x) share_block(base, kBlocks, wave, x, o[x]);
@@ -181,27 +183,43 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves == 4 && !kSplit ? 2 : 1) k
             unsigned short* p = static_cast<unsigned short*>(a.out.p) + (at.begin[0] + i) * a.out.ld + h * a.out.head;
             store_block<DT>(p, 32 * wave, i < L, sq.dim, sum_o, total == 0.0f ? 0.0f : 1.0f / total);
         }
+    } else if constexpr (kShare == 2) {
+        lds_f32* const stats = (lds_f32*)(base + kShares);
+        __syncthreads();
+        stats[wave * 128 + (threadIdx.x & 63)] = m;
+        stats[wave * 128 + 64 + (threadIdx.x & 63)] = total;
+        __syncthreads();
+        const float m2 = stats[(wave ^ 1) * 128 + (threadIdx.x & 63)], top = fmaxf(m, m2);
+        const float own = m == -kInf ? 0.0f : __builtin_amdgcn_exp2f(c * (m - top));
+        const float other = m2 == -kInf ? 0.0f : __builtin_amdgcn_exp2f(c * (m2 - top));
+        total = own * total + other * stats[(wave ^ 1) * 128 + 64 + (threadIdx.x & 63)];
+        m = top;
+        const float norm = total == 0.0f ? 0.0f : 1.0f / total;
+        unsigned short* const p = static_cast<unsigned short*>(a.out.p) + (at.begin[0] + i) * a.out.ld + h * a.out.head;
+        join_pairs<kBlocks>(base, wave, own, other, o,
+                            [&](int x, const f32x16& sum_o) { store_block<DT>(p, 32 * x, i < L, sq.dim, sum_o, norm); });
     } else {
         // a query that sees no key: total 0, m -infinity
         store_columns<DT, kD>(a.out, at.begin[0] + i, h, i < L, sq.dim, o, total == 0.0f ? 0.0f : 1.0f / total);
     }
-    if (i < L && half == 0 && (!kSplit || wave == 0))
+    if (i < L && half == 0 && wave % kShare == 0)
         a.lse[h * sq.rows[0] + at.begin[0] + i] = total == 0.0f ? -kInf : sq.scale * m + kLn2 * __builtin_amdgcn_logf(total);
 }
 
-template <dp_dtype DT, int kD, int kWaves, bool kSplit>
+template <dp_dtype DT, int kD, int kWaves, int kShare>
 void launch_one(const AttentionArgs& a, hipStream_t stream) {
-    const dim3 grid(static_cast<unsigned>(attention_slots(a.s, 0, kSplit ? 32 : 32 * kWaves) * a.s.heads));
-    if (grid.x > 0) hipLaunchKernelGGL((k_attention<DT, kD, kWaves, kSplit>), grid, dim3(64 * kWaves), 0, stream, a);
+    const dim3 grid(static_cast<unsigned>(attention_slots(a.s, 0, 32 * kWaves / kShare) * a.s.heads));
+    if (grid.x > 0) hipLaunchKernelGGL((k_attention<DT, kD, kWaves, kShare>), grid, dim3(64 * kWaves), 0, stream, a);
 }
 
 template <dp_dtype DT, int kD>
 void launch_shape(const AttentionArgs& a, hipStream_t stream) {
     const AttentionShape shape = attention_shape(a.s, 0);
-    if (shape == AttentionShape::kSplit) return launch_one<DT, kD, 4, true>(a, stream);
+    if (shape == AttentionShape::kSplit) return launch_one<DT, kD, 4, 4>(a, stream);
+    if (shape == AttentionShape::kPairs) return launch_one<DT, kD, 8, 2>(a, stream);
     if constexpr (kD > 96)
-        if (shape == AttentionShape::kWide) return launch_one<DT, kD, 8, false>(a, stream);
-    launch_one<DT, kD, 4, false>(a, stream);
+        if (shape == AttentionShape::kWide) return launch_one<DT, kD, 8, 1>(a, stream);
+    launch_one<DT, kD, 4, 1>(a, stream);
 }
 
 template <dp_dtype DT>
@@ -221,14 +239,23 @@ int64_t attention_slots(const Sequences& s, int side, int64_t tile) {
 }
 
 // Workgroups of four waves with 32 rows each (of the queries, or in k_attention_dkv of
-// the keys) but
-//  - where these are too few for the CUs, four waves with the same 32 rows, which share
-//    what they go over and join at the end.  Their tiles are larger, so that one (heads
-//    of more than 64 elements) or two of them fit a CU, and are read for fewer rows.
-//    Plain against split, us, one sequence: 8 heads of 64, 2048 rows (128 workgroups of
-//    four waves) forward 30 and 21, dk and dv 60 and 30; 16 heads (256) 31 and 32, 61 and
-//    43; 16 heads, 4096 rows (512) 63 and 87, 123 and 129.  Heads of 128: 8 heads, 2048
-//    rows 44 and 35, 108 and 56; 16 heads 46 and 68, 110 and 104.
+// the keys) where these are enough for the 256 CUs, but
+//  - where they are too few, waves with the same 32 rows share what they go over, and join
+//    their sums at the end: two of eight waves, or all four (whose tiles are larger, so that
+//    one workgroup, or two for heads of up to 64 elements, fits a CU).  One causal sequence,
+//    us as one wave | two | four a run of 32 rows, by workgroups of 128 rows:
+//                                    forward        dq             dk and dv
+//      heads of 64, 2048 rows   128   30  28  21     39  32  24     61  43  29
+//                               256   31  30  32     41  34  38     63  43  42
+//                   4096 rows   512   63  59  86     81  70 103    127  91 127
+//                               768   77  77 128    100 109 152    149 136
+//                              1024                                160 165
+//      heads of 128, 2048 rows  128   44  41  36     66  49  47    108  66  50
+//                               256   45  42  67     69  51  91    111  72  96
+//                    4096 rows  512   99  91 231    146 117 308
+//                               768  124 142 345    170 183 464    235 237 494
+//                              1024                                291 301 679
+//    (between 128 and 256 all four waves' times rise with the workgroups)
 //  - eight waves for heads of more than 96 elements and long sequences.  These load each
 //    tile half as often and leave more registers to fragments that are read ahead, but
 //    wait for each other twice as many, and their 256 rows cross the mask's edge further.
@@ -239,7 +266,8 @@ int64_t attention_slots(const Sequences& s, int side, int64_t tile) {
 AttentionShape attention_shape(const Sequences& s, int side) {
     const int heads = side == 0 ? s.heads : s.kv_heads;
     const int64_t groups = attention_slots(s, side, 128) * heads;
-    if (groups < (side == 0 ? (s.dim > 64 ? 160 : 256) : (s.dim > 64 ? 256 : 448))) return AttentionShape::kSplit;
+    if (groups < (s.dim > 64 ? 160 : 240)) return AttentionShape::kSplit;
+    if (groups < (side == 0 ? 640 : 800)) return AttentionShape::kPairs;
     const bool wide = s.count > 0 && s.rows[1 - side] / s.count >= 3500 && attention_slots(s, side, 256) * heads >= 512;
     return wide && s.dim > 96 ? AttentionShape::kWide : AttentionShape::kPlain;
 }

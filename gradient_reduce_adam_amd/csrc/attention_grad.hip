@@ -23,12 +23,13 @@ namespace {
 
 using namespace attn;
 
-// kSplit: the four waves have the same 32 queries, and 32 keys each of every tile.
-template <dp_dtype DT, int kD, int kWaves, bool kSplit>
-__global__ void __launch_bounds__(64 * kWaves, kWaves == 4 && !kSplit ? 2 : 1) k_attention_dq(AttentionArgs a) {
+// kShare: so many neighbouring waves have the same 32 queries, and 32 keys each of
+// every tile; with 1 a wave takes all 64 keys.
+template <dp_dtype DT, int kD, int kWaves, int kShare>
+__global__ void __launch_bounds__(64 * kWaves, kWaves == 4 && kShare == 1 ? 2 : 1) k_attention_dq(AttentionArgs a) {
     using T = Tile<kD>;
-    constexpr int kRows = kSplit ? 32 : 32 * kWaves, kKeys = kSplit ? 32 * kWaves : 64, kBlocks = (kD + 31) / 32;
-    constexpr int kOwn = kSplit ? 1 : 2;  // times 32 keys of a tile that a wave takes
+    constexpr int kRows = 32 * kWaves / kShare, kKeys = kShare == 1 ? 64 : 32 * kShare, kBlocks = (kD + 31) / 32;
+    constexpr int kOwn = kShare == 1 ? 2 : 1;  // times 32 keys of a tile that a wave takes
     constexpr int kTileBytes = kKeys * T::kRowBytes;
     __shared__ __align__(1024) unsigned char lds[4 * kTileBytes];  // two turns of a k and a v tile
     const Sequences& sq = a.s;
@@ -37,7 +38,7 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves == 4 && !kSplit ? 2 : 1) k
     const int h = at.head, hk = h / (sq.heads / sq.kv_heads);
     const int L = at.length[0], M = at.length[1], shift = M - L;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = threadIdx.x >> 5 & 1;
-    const int first = at.tile * kRows, mine = first + (kSplit ? 0 : wave * 32);  // queries of the workgroup, of the wave
+    const int first = at.tile * kRows, mine = first + wave / kShare * 32;  // queries of the workgroup, of the wave
 
     // The keys that a query sees: [lo, hi].
     const auto lowest = [&](int i) { return sq.window > 0 && i + shift >= sq.window ? i + shift - sq.window + 1 : 0; };
@@ -50,10 +51,17 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves == 4 && !kSplit ? 2 : 1) k
 
     const Head q = head_of(a.q, at.begin[0], h), k = head_of(a.k, at.begin[1], hk), v = head_of(a.v, at.begin[1], hk);
     const Head out = head_of(a.out, at.begin[0], h), dout = head_of(a.dout, at.begin[0], h);
+    // the first tile is on its way while delta is computed
+    Stage<kD, kKeys, 64 * kWaves> ks, vs;
+    const auto load = [&](int t) {
+        ks.load(k, t, M, sq.dim);
+        vs.load(v, t, M, sq.dim);
+    };
     u32x4 qf[kD / 16], df[kD / 16], of[kD / 16];
     load_right<kD>(q, i, i < L, sq.dim, qf);
     load_right<kD>(dout, i, i < L, sq.dim, df);
     load_right<kD>(out, i, i < L, sq.dim, of);
+    if (from < to) load(from);
     float delta = 0.0f;
 #pragma unroll
     for (int n = 0; n < kD / 16; ++n)
@@ -73,7 +81,7 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves == 4 && !kSplit ? 2 : 1) k
         const int64_t row = h * sq.rows[0] + at.begin[0] + i;
         const float lse = a.lse[row];
         less = lse == -kInf ? kInf : kLog2e * lse;
-        if (half == 0 && (!kSplit || wave == 0)) a.delta[row] = delta;
+        if (half == 0 && wave % kShare == 0) a.delta[row] = delta;
     }
     f32x16 o[kBlocks];
 #pragma unroll
@@ -83,11 +91,6 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves == 4 && !kSplit ? 2 : 1) k
     lds_u8* const base = (lds_u8*)lds;
     const int along = T::along(), across = T::across();
     if (from < to) {
-        Stage<kD, kKeys, 64 * kWaves> ks, vs;
-        const auto load = [&](int t) {
-            ks.load(k, t, M, sq.dim);
-            vs.load(v, t, M, sq.dim);
-        };
         const auto store = [&](int turn) {
             ks.store(base + turn, sq.dim);
             vs.store(base + turn + kTileBytes, sq.dim);
@@ -95,7 +98,6 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves == 4 && !kSplit ? 2 : 1) k
         // The wave's keys of a tile, from t on.
         const auto step = [&](const lds_u8* kt, int t) {
             const lds_u8* vt = kt + kTileBytes;
-            const bool masked = t < all_lo || t + 32 * kOwn - 1 > all_hi;
 #pragma unroll
             for (int j = 0; j < kOwn; ++j) {
                 f32x16 s = zeros(), dp = zeros();
@@ -106,14 +108,8 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves == 4 && !kSplit ? 2 : 1) k
                     dp = mma<DT>(T::read_along(vt, along, j, n), df[n], dp);
                 }
                 ahead<kD / 16, 2, 2, 3>();
-                if (masked) {
-                    const int up = hi - t - 4 * half, down = lo - t - 4 * half;
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const int key = 32 * j + 8 * (e >> 2) + (e & 3);
-                        s[e] = key > up || key < down ? -kInf : s[e];
-                    }
-                }
+                if (t + 32 * j + 31 > all_hi) hide_behind(s, hi - t - 32 * j - 4 * half);
+                if (t + 32 * j < all_lo) hide_before(s, lo - t - 32 * j - 4 * half);
                 __builtin_amdgcn_sched_barrier(0);
                 u32x4 ds[2];
 #pragma unroll
@@ -130,13 +126,12 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves == 4 && !kSplit ? 2 : 1) k
         };
 #pragma unroll
         for (int n = 0; n < 4; ++n) ks.clear(base + n * kTileBytes, sq.dim);
-        load(from);
         store(0);
         load(from + kKeys < to ? from + kKeys : from);
         __syncthreads();
         int turn = 0;
         for (int t = from; t < to; t += kKeys) {
-            const int skip = kSplit ? 32 * wave : 0;
+            const int skip = 32 * (wave % kShare);
             if (mine < L && t + skip <= some_hi && t + skip + 32 * kOwn > some_lo)
                 step(base + turn + skip * T::kRowBytes, t + skip);
             if (t + kKeys < to) {
@@ -148,8 +143,9 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves == 4 && !kSplit ? 2 : 1) k
             }
         }
     }
-    if constexpr (kSplit) {  // the waves' shares, added in their order
-        static_assert(kWaves * kBlocks * 4096 <= 4 * kTileBytes, "the shares fit the tiles' memory");
+    unsigned short* const p = static_cast<unsigned short*>(a.dq.p) + (at.begin[0] + i) * a.dq.ld + h * a.dq.head;
+    if constexpr (kShare == 4) {  // the waves' shares, added in their order
+        static_assert(kBlocks <= kWaves && kWaves * kBlocks * 4096 <= 4 * kTileBytes, "the shares fit the tiles' memory");
         __syncthreads();
 #pragma unroll
         for (int x = 0; x < kBlocks; ++x) share_block(base, kBlocks, wave, x, o[x]);
@@ -158,9 +154,12 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves == 4 && !kSplit ? 2 : 1) k
             f32x16 sum = zeros();
 #pragma unroll
             for (int w = 0; w < kWaves; ++w) add_block(base, kBlocks, w, wave, 1.0f, sum);
-            unsigned short* p = static_cast<unsigned short*>(a.dq.p) + (at.begin[0] + i) * a.dq.ld + h * a.dq.head;
             store_block<DT>(p, 32 * wave, i < L, sq.dim, sum, sq.scale);
         }
+    } else if constexpr (kShare == 2) {
+        static_assert(kWaves * 4096 <= 4 * kTileBytes, "the shares fit the tiles' memory");
+        join_pairs<kBlocks>(base, wave, 1.0f, 1.0f, o,
+                            [&](int x, const f32x16& sum) { store_block<DT>(p, 32 * x, i < L, sq.dim, sum, sq.scale); });
     } else {
         store_columns<DT, kD>(a.dq, at.begin[0] + i, h, i < L, sq.dim, o, sq.scale);
     }
@@ -168,11 +167,12 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves == 4 && !kSplit ? 2 : 1) k
 
 // v's fragments are read from LDS for each tile: in registers they would leave too few
 // for two waves a SIMD (heads of 128: 925 us, from LDS 601) or three (of 64).
-// kSplit: the four waves have the same 32 keys, and 32 queries each of every tile.
-template <dp_dtype DT, int kD, int kWaves, int kQueries, bool kSplit>
-__global__ void __launch_bounds__(64 * kWaves, kWaves == 8 || kSplit ? 1 : kD <= 32 ? 4 : kD <= 64 ? 3 : 2) k_attention_dkv(AttentionArgs a) {
+// kShare: so many neighbouring waves have the same 32 keys, and share the queries of
+// every tile.
+template <dp_dtype DT, int kD, int kWaves, int kQueries, int kShare>
+__global__ void __launch_bounds__(64 * kWaves, kWaves == 8 || kShare == 4 ? 1 : kD <= 32 ? 4 : kD <= 64 ? 3 : 2) k_attention_dkv(AttentionArgs a) {
     using T = Tile<kD>;
-    constexpr int kTileBytes = kQueries * T::kRowBytes, kRows = kSplit ? 32 : 32 * kWaves, kBlocks = (kD + 31) / 32;
+    constexpr int kTileBytes = kQueries * T::kRowBytes, kRows = 32 * kWaves / kShare, kBlocks = (kD + 31) / 32;
     constexpr int kTurn = 2 * kTileBytes + 2 * kQueries * 4;  // a q and a dout tile, -lse / scale and -delta of their rows
     constexpr int kValues = kRows * T::kRowBytes;  // v
     __shared__ __align__(1024) unsigned char lds[kValues + 2 * kTurn];
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves == 8 || kSplit ? 1 : kD <=
     const int hk = at.head, group = sq.heads / sq.kv_heads;
     const int L = at.length[0], M = at.length[1], shift = M - L;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = threadIdx.x >> 5 & 1;
-    const int first = at.tile * kRows, mine = first + (kSplit ? 0 : wave * 32);  // keys of the workgroup, of the wave
+    const int first = at.tile * kRows, run = wave / kShare, mine = first + 32 * run;  // keys of the workgroup, of the wave
 
     // The queries that see a key: [lo, hi].
     const auto lowest = [&](int j) { return sq.causal && j - shift > 0 ? j - shift : 0; };
@@ -207,12 +207,6 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves == 8 || kSplit ? 1 : kD <=
     const int along = T::along(), across = T::across();
     const int tiles = each * group;
     if (tiles > 0) {
-        {
-            Stage<kD, kRows, 64 * kWaves> vs;
-            vs.clear((lds_u8*)lds, sq.dim);
-            vs.load(v, first, M, sq.dim);
-            vs.store((lds_u8*)lds, sq.dim);
-        }
         Stage<kD, kQueries, 64 * kWaves> qs, ds;
 #pragma unroll
         for (int i = 0; i < 4; ++i) qs.clear(base + (i >> 1) * kTurn + (i & 1) * kTileBytes, sq.dim);
@@ -259,18 +253,12 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves == 8 || kSplit ? 1 : kD <=
 #pragma unroll
             for (int n = 0; n < kD / 16; ++n) {
                 s = mma<DT>(T::read_along(qt, along, 0, n), kf[n], s);
-                dp = mma<DT>(T::read_along(dt, along, 0, n), T::read_along((lds_u8*)lds, along, kSplit ? 0 : wave, n), dp);
+                dp = mma<DT>(T::read_along(dt, along, 0, n), T::read_along((lds_u8*)lds, along, run, n), dp);
             }
             reads<8>();
             ahead<kD / 16, 2, 3, 2>();
-            if (t < all_lo || t + 31 > all_hi) {
-                const int up = hi - t - 4 * half, down = lo - t - 4 * half;
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int query = 8 * (e >> 2) + (e & 3);
-                    s[e] = query > up || query < down ? -kInf : s[e];
-                }
-            }
+            if (t + 31 > all_hi) hide_behind(s, hi - t - 4 * half);
+            if (t < all_lo) hide_before(s, lo - t - 4 * half);
             __builtin_amdgcn_sched_barrier(0);
             u32x4 p[2], w[2];
 #pragma unroll
@@ -293,14 +281,18 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves == 8 || kSplit ? 1 : kD <=
             ahead<4 * kBlocks, 1, 2, 4>();
             __builtin_amdgcn_sched_barrier(0);
         };
+        Stage<kD, kRows, 64 * kWaves> vs;
+        vs.clear((lds_u8*)lds, sq.dim);
+        vs.load(v, first, M, sq.dim);
         load();
+        vs.store((lds_u8*)lds, sq.dim);
         store(0);
         load();
         __syncthreads();
         int turn = 0, t = from;
         for (int i = 0; i < tiles; ++i) {
 #pragma unroll 1
-            for (int r = kSplit ? 32 * wave : 0; r < (kSplit ? 32 * wave + 32 : kQueries); r += 32)
+            for (int r = 32 * (wave % kShare); r < kQueries; r += 32 * kShare)
                 if (mine < M && t + r <= some_hi && t + r + 32 > some_lo) step(base + turn, r, t + r);
             t = t + kQueries >= to ? from : t + kQueries;
             if (i + 1 < tiles) {
@@ -311,8 +303,10 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves == 8 || kSplit ? 1 : kD <=
             }
         }
     }
-    if constexpr (kSplit) {  // the waves' shares, added in their order
-        static_assert(2 * kWaves * kBlocks * 4096 <= kValues + 2 * kTurn, "the shares fit the tiles' memory");
+    unsigned short* const pk = static_cast<unsigned short*>(a.dk.p) + (at.begin[1] + key) * a.dk.ld + hk * a.dk.head;
+    unsigned short* const pv = static_cast<unsigned short*>(a.dv.p) + (at.begin[1] + key) * a.dv.ld + hk * a.dv.head;
+    if constexpr (kShare == 4) {  // the waves' shares, added in their order
+        static_assert(kBlocks <= kWaves && 2 * kWaves * kBlocks * 4096 <= kValues + 2 * kTurn, "the shares fit the tiles' memory");
         lds_u8* const at_dk = (lds_u8*)lds;
         lds_u8* const at_dv = at_dk + kWaves * kBlocks * 4096;
         __syncthreads();
@@ -329,10 +323,19 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves == 8 || kSplit ? 1 : kD <=
                 add_block(at_dk, kBlocks, w, wave, 1.0f, sum_k);
                 add_block(at_dv, kBlocks, w, wave, 1.0f, sum_v);
             }
-            unsigned short* pk = static_cast<unsigned short*>(a.dk.p) + (at.begin[1] + key) * a.dk.ld + hk * a.dk.head;
-            unsigned short* pv = static_cast<unsigned short*>(a.dv.p) + (at.begin[1] + key) * a.dv.ld + hk * a.dv.head;
             store_block<DT>(pk, 32 * wave, key < M, sq.dim, sum_k, sq.scale);
             store_block<DT>(pv, 32 * wave, key < M, sq.dim, sum_v, 1.0f);
+        }
+    } else if constexpr (kShare == 2) {  // the even wave of a pair sums dk, the odd one dv, a block at a time
+        static_assert(kWaves * 4096 <= kValues + 2 * kTurn, "the shares fit the tiles' memory");
+#pragma unroll
+        for (int x = 0; x < kBlocks; ++x) {
+            __syncthreads();
+            share_block((lds_u8*)lds, 1, wave, 0, wave & 1 ? dk[x] : dv[x]);
+            __syncthreads();
+            f32x16 sum = wave & 1 ? dv[x] : dk[x];
+            add_block((lds_u8*)lds, 1, wave ^ 1, 0, 1.0f, sum);
+            store_block<DT>(wave & 1 ? pv : pk, 32 * x, key < M, sq.dim, sum, wave & 1 ? 1.0f : sq.scale);
         }
     } else {
         store_columns<DT, kD>(a.dk, at.begin[1] + key, hk, key < M, sq.dim, dk, sq.scale);
@@ -340,16 +343,16 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves == 8 || kSplit ? 1 : kD <=
     }
 }
 
-template <dp_dtype DT, int kD, int kWaves, bool kSplit>
+template <dp_dtype DT, int kD, int kWaves, int kShare>
 void launch_dq(const AttentionArgs& a, hipStream_t stream) {
-    const dim3 grid(static_cast<unsigned>(attention_slots(a.s, 0, kSplit ? 32 : 32 * kWaves) * a.s.heads));
-    if (grid.x > 0) hipLaunchKernelGGL((k_attention_dq<DT, kD, kWaves, kSplit>), grid, dim3(64 * kWaves), 0, stream, a);
+    const dim3 grid(static_cast<unsigned>(attention_slots(a.s, 0, 32 * kWaves / kShare) * a.s.heads));
+    if (grid.x > 0) hipLaunchKernelGGL((k_attention_dq<DT, kD, kWaves, kShare>), grid, dim3(64 * kWaves), 0, stream, a);
 }
-template <dp_dtype DT, int kD, int kWaves, int kQueries, bool kSplit>
+template <dp_dtype DT, int kD, int kWaves, int kQueries, int kShare>
 void launch_dkv(const AttentionArgs& a, hipStream_t stream) {
-    const dim3 grid(static_cast<unsigned>(attention_slots(a.s, 1, kSplit ? 32 : 32 * kWaves) * a.s.kv_heads));
+    const dim3 grid(static_cast<unsigned>(attention_slots(a.s, 1, 32 * kWaves / kShare) * a.s.kv_heads));
     if (grid.x > 0)
-        hipLaunchKernelGGL((k_attention_dkv<DT, kD, kWaves, kQueries, kSplit>), grid, dim3(64 * kWaves), 0, stream, a);
+        hipLaunchKernelGGL((k_attention_dkv<DT, kD, kWaves, kQueries, kShare>), grid, dim3(64 * kWaves), 0, stream, a);
 }
 
 // In k_attention_dkv heads of more than 96 elements take eight waves and tiles of 64
@@ -360,11 +363,13 @@ template <dp_dtype DT, int kD>
 void launch_both(const AttentionArgs& a, hipStream_t stream) {
     constexpr bool kLarge = kD > 96;
     const AttentionShape q = attention_shape(a.s, 0), k = attention_shape(a.s, 1);
-    if (q == AttentionShape::kSplit) launch_dq<DT, kD, 4, true>(a, stream);
-    else if (kLarge && q == AttentionShape::kWide) launch_dq<DT, kD, kLarge ? 8 : 4, false>(a, stream);
-    else launch_dq<DT, kD, 4, false>(a, stream);
-    if (k == AttentionShape::kSplit) launch_dkv<DT, kD, 4, 128, true>(a, stream);
-    else launch_dkv<DT, kD, kLarge ? 8 : 4, kLarge ? 64 : 32, false>(a, stream);
+    if (q == AttentionShape::kSplit) launch_dq<DT, kD, 4, 4>(a, stream);
+    else if (q == AttentionShape::kPairs) launch_dq<DT, kD, 8, 2>(a, stream);
+    else if (kLarge && q == AttentionShape::kWide) launch_dq<DT, kD, kLarge ? 8 : 4, 1>(a, stream);
+    else launch_dq<DT, kD, 4, 1>(a, stream);
+    if (k == AttentionShape::kSplit) launch_dkv<DT, kD, 4, 128, 4>(a, stream);
+    else if (k == AttentionShape::kPairs) launch_dkv<DT, kD, 8, 64, 2>(a, stream);
+    else launch_dkv<DT, kD, kLarge ? 8 : 4, kLarge ? 64 : 32, 1>(a, stream);
 }
 
 template <dp_dtype DT>

@@ -33,7 +33,7 @@ struct AttentionArgs {
 // Workgroups of a launch for tiles of `tile` rows of the queries (side 0) or the keys (1).
 int64_t attention_slots(const Sequences& s, int side, int64_t tile);
 // How the waves of a workgroup share the rows of the queries (side 0) or the keys (1).
-enum class AttentionShape { kPlain, kWide, kSplit };
+enum class AttentionShape { kPlain, kWide, kPairs, kSplit };
 AttentionShape attention_shape(const Sequences& s, int side);
 int64_t attention_groups(const Sequences& s);  // most workgroups of any launch
 hipError_t launch_attention(dp_dtype dt, const AttentionArgs& a, hipStream_t stream);

@@ -169,6 +169,16 @@ def test_more_tiles_than_cus(D, causal, window):
     c.check(sequences=3)
 
 
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 50)])
+@pytest.mark.parametrize("D", [16, 32, 64, 72, 80, 96, 104, 128])
+def test_tiles_enough_for_the_cus(D, causal, window):
+    """More tiles yet: none is shared by waves."""
+    c = Case(cut(160, 160, 160), 160, 160, D, "bf16" if D % 32 else "f16", seed=D + 1, causal=causal, window=window)
+    c.check(sequences=3)
+    c = Case(cut(33, 0, 128, 257, 1, 62), 270, 135, D, "bf16", seed=D, causal=causal, window=window, layout="heads")
+    c.check(**c.places())
+
+
 @pytest.mark.parametrize("L,M,H,D,causal,window", [(100, 3501, 512, 104, True, 0), (257, 3700, 256, 128, True, 700),
                                                     (300, 3600, 256, 128, False, 0), (3600, 3600, 40, 112, True, 0)])
 def test_long_sequences(L, M, H, D, causal, window):
