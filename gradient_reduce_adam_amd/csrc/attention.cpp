@@ -13,7 +13,7 @@ using dpapi::hip_fail;
 
 namespace {
 
-constexpr int64_t kMaxGroups = (int64_t{1} << 24) - 1;  // of 256 threads, fewer than 2^32 in a launch
+constexpr int64_t kMaxGroups = (int64_t{1} << 23) - 1;  // of up to 512 threads, fewer than 2^32 in a launch
 constexpr int64_t kMaxStride = int64_t{1} << 36;        // 2^24 rows stay within 63 bits
 constexpr int64_t kMaxRow = (int64_t{1} << 31) - 1;      // of the attention: a row in bytes within 32 bits
 constexpr int32_t kMaxRotaryDim = 4096;

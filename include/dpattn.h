@@ -11,7 +11,9 @@
  * workspace is scratch for the length of that call on its stream: calls that
  * may run at the same time, and graphs that may replay at the same time, need a
  * workspace each.  Outputs must not overlap inputs or each other unless a call
- * says so.  The same call on the same inputs gives the same bits.
+ * says so.  The same call on the same inputs gives the same bits; how a sum is
+ * split among waves, and so its last bits, depends on the rows and heads of the
+ * call.
  *
  * Rows of heads.  A tensor has `tokens` rows of heads of `dim` elements of a
  * dtype.  Element d of head h in row t is p[t * ld + h * head + d]: the rows of
@@ -109,7 +111,10 @@ dp_status dpa_rotary(const dpa_rotary_desc* rotary, int64_t tokens, int32_t dim,
  *   j <= place           with causal != 0
  *   j >  place - window  with window > 0 (0: no window)
  * Rows of no sequence (padding between or behind them) are neither read nor
- * written, in any tensor. */
+ * written, in any tensor.  An infinity or NaN in a key or value may reach other
+ * queries of its sequence than those that see it: a masked score counts 0 times
+ * the value, as in the product by a matrix of probabilities.
+ * A call has fewer than 2^23 tiles: (rows / 128 + sequences) times heads. */
 typedef struct dpa_attention_desc {
     int32_t heads;    /* of the queries, 1 .. DPA_MAX_HEADS, a multiple of kv_heads */
     int32_t kv_heads; /* query head h reads key head h / (heads / kv_heads) */

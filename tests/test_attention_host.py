@@ -78,7 +78,8 @@ BAD_DESC = (dict(heads=0), dict(heads=1025, kv_heads=1), dict(kv_heads=0), dict(
             dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=1e-46), dict(scale=1e39), dict(tokens=-1),
             dict(tokens=(1 << 24) + 1), dict(tokens_k=-1), dict(sequences=-1), dict(sequences=5), dict(sequences=(1 << 24) + 1),
             dict(offsets=P, tokens_k=31), dict(offsets=P, offset_bytes=3), dict(offsets=P, step=3), dict(offsets=P + 2),
-            dict(offsets_k=P + 4, offset_bytes=8), dict(tokens_k=33, sequences=2), dict(tokens=1 << 24, tokens_k=1 << 24, heads=1024))
+            dict(offsets_k=P + 4, offset_bytes=8), dict(tokens_k=33, sequences=2), dict(tokens=1 << 24, tokens_k=1 << 24, heads=1024),
+            dict(offsets=P, sequences=1 << 23, heads=1, kv_heads=1), dict(offsets=P, sequences=1 << 17, heads=64, kv_heads=64, dim=128))
 
 
 def forward(d=None, dtype=dp.DP_BF16, q=None, k=None, v=None, out=None, lse=P, handle=True):
