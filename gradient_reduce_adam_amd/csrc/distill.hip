@@ -7,6 +7,9 @@
 // teacher's list is gathered beside it into LDS, with a bit for each token of the list,
 // by which the sums leave these tokens out of the rest.  The gradient is written as
 // if no token were listed; then the listed ones and the label are written again.
+// Memory bound: 16384 x 32000 bf16 logits with their gradient 393 to 405 us, 5.2 to 5.3 TB/s of
+// what is read and written once (a large copy 4.9); losses alone, 4096 x 50257 binary32, 130
+// us, 6.3 TB/s.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
