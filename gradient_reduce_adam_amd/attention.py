@@ -103,12 +103,12 @@ def _register() -> None:
 _register()
 
 
-# A call's structs are packed into one buffer at once, which takes a third of the time of a ctypes
-# structure each: a dpa_rotary_rows, and a dpa_attention_desc with the rows of the call's tensors behind it.
+# A call's structs are packed as bytes, which takes a fifth of the time of a ctypes structure each.
 _ROTARY_ROWS = struct.Struct("PqqPqqii")
-_DESC = "iiiiqdqqqPPii"
-_FORWARD, _BACKWARD = struct.Struct(_DESC + "Pqq" * 4), struct.Struct(_DESC + "Pqq" * 8)
-_DESC_BYTES, _ROWS_BYTES = ctypes.sizeof(AttentionDesc), ctypes.sizeof(Rows)
+_ROTARY_CALL = [struct.Struct(_ROTARY_ROWS.format * n) for n in range(DPA_MAX_TENSORS + 1)]
+_DESC, _ROWS = struct.Struct("iiiiqdqqqPPii"), struct.Struct("Pqq")
+_pack = _ROWS.pack
+_POSITION_BYTES = {} if torch is None else {torch.int32: 4, torch.int64: 8}
 
 
 def _heads(name: str, t, device: int, shape=None, dtype=None):
@@ -132,30 +132,32 @@ def dpa_rotary(rotary: Rotary, positions, x, y, inverse: bool = False, stream=No
     to four of them, with the same rows and their own heads; y may be x.  positions: int32 or int64, ``[tokens, axes]``
     of any strides, or ``[tokens]`` for one axis."""
     dev = _current_device()
-    xs, ys = (list(v) if isinstance(v, (list, tuple)) else [v] for v in (x, y))
-    if len(xs) != len(ys) or not 1 <= len(xs) <= DPA_MAX_TENSORS:
-        raise ValueError(f"{len(xs)} tensors x and {len(ys)} tensors y (the same number, up to {DPA_MAX_TENSORS})")
-    one, axes = xs[0], len(rotary.sections)
+    xs, ys = x if isinstance(x, (list, tuple)) else (x,), y if isinstance(y, (list, tuple)) else (y,)
+    count, axes = len(xs), len(rotary.sections)
+    if count != len(ys) or not 1 <= count <= DPA_MAX_TENSORS:
+        raise ValueError(f"{count} tensors x and {len(ys)} tensors y (the same number, up to {DPA_MAX_TENSORS})")
     if not 1 <= axes <= DPA_MAX_AXES:
         raise ValueError(f"{axes} axes (up to {DPA_MAX_AXES})")
-    rows = []
+    one, rows = xs[0], []
+    dtype, first = one.dtype, one.shape
     for a, b in zip(xs, ys):
-        rows += (*_heads("x", a, dev, None, one.dtype), *_heads("y", b, dev, a.shape, one.dtype), a.shape[1], 0)
-        if a.shape[0] != one.shape[0] or a.shape[2] != one.shape[2]:
-            raise ValueError(f"x: {tuple(a.shape)} beside {tuple(one.shape)}")
-    tokens, _, dim = one.shape
+        shape = a.shape
+        rows += (*_heads("x", a, dev, None, dtype), *_heads("y", b, dev, shape, dtype), shape[1], 0)
+        if shape[0] != first[0] or shape[2] != first[2]:
+            raise ValueError(f"x: {tuple(shape)} beside {tuple(first)}")
+    tokens = first[0]
     if positions.get_device() != dev:
         raise _elsewhere("positions", positions, dev)
-    if positions.dtype not in (torch.int32, torch.int64):
+    bits = _POSITION_BYTES.get(positions.dtype)
+    if bits is None:
         raise ValueError(f"positions are int32 or int64, not {positions.dtype}")
-    at = positions.unsqueeze(1) if positions.dim() == 1 else positions
-    if tuple(at.shape) != (tokens, axes):
+    shape, strides = positions.shape, positions.stride()
+    if len(shape) == 1 and axes == 1:
+        shape, strides = (shape[0], 1), (strides[0], 0)
+    if len(shape) != 2 or shape[0] != tokens or shape[1] != axes:
         raise ValueError(f"positions are {tuple(positions.shape)}, expected ({tokens}, {axes})")
-    buf = ctypes.create_string_buffer(_ROTARY_ROWS.size * len(xs))
-    for i in range(len(xs)):
-        _ROTARY_ROWS.pack_into(buf, i * _ROTARY_ROWS.size, *rows[8 * i:8 * i + 8])
-    _check(lib.dpa_rotary(rotary.ref(), tokens, dim, at.data_ptr(), at.element_size(), at.stride(0), at.stride(1),
-                          len(xs), ctypes.addressof(buf), _dtype(one), bool(inverse), _stream_of(stream, dev)))
+    _check(lib.dpa_rotary(rotary.ref(), tokens, first[2], positions.data_ptr(), bits, strides[0], strides[1], count,
+                          _ROTARY_CALL[count].pack(*rows), _dtype(one), bool(inverse), _stream_of(stream, dev)))
 
 
 # ---- attention -----------------------------------------------------------------
@@ -170,11 +172,14 @@ def _offsets(name: str, t, device: int):
     return t.data_ptr(), t.shape[0] if spans else t.shape[0] - 1, t.element_size(), 2 if spans else 1
 
 
-def _describe(attention: Attention, q, k, sequences: Optional[int], offsets, offsets_k, device: int):
-    """The fields of a dpa_attention_desc."""
-    if len(q.shape) != 3 or len(k.shape) != 3:
-        raise ValueError(f"q and k must be [tokens, heads, dim], not {tuple(q.shape)} and {tuple(k.shape)}")
-    tokens, heads, dim = q.shape
+def _describe(attention: Attention, qs, ks, sequences: Optional[int], offsets, offsets_k, device: int):
+    """The dpa_attention_desc of a call whose queries and keys have the shapes qs and ks."""
+    if len(qs) != 3 or len(ks) != 3:
+        raise ValueError(f"q and k must be [tokens, heads, dim], not {tuple(qs)} and {tuple(ks)}")
+    tokens, heads, dim = qs
+    tokens_k, kv_heads, dim_k = ks
+    if dim_k != dim:
+        raise ValueError(f"heads of {dim} elements in q and of {dim_k} in k")
     at, at_k, size, step = 0, 0, 0, 0
     if offsets is not None or offsets_k is not None:
         given = [_offsets(n, t, device) for n, t in (("offsets", offsets), ("offsets_k", offsets_k)) if t is not None]
@@ -187,8 +192,8 @@ def _describe(attention: Attention, q, k, sequences: Optional[int], offsets, off
         at = given[0][0] if offsets is not None else 0
         at_k = given[-1][0] if offsets_k is not None else 0
     scale = attention.scale if attention.scale is not None else 1.0 / math.sqrt(max(dim, 1))
-    return (heads, k.shape[1], dim, bool(attention.causal), attention.window, scale, tokens, k.shape[0],
-            1 if sequences is None else sequences, at, at_k, size, step)
+    return _DESC.pack(heads, kv_heads, dim, bool(attention.causal), attention.window, scale, tokens, tokens_k,
+                      1 if sequences is None else sequences, at, at_k, size, step)
 
 
 _SIXTEEN = (DP_BF16, DP_F16)
@@ -201,11 +206,12 @@ def _attention_dtype(q) -> int:
     return code
 
 
-def _lse(lse, q, device: int) -> int:
+def _lse(lse, qs, device: int) -> int:
     if lse.get_device() != device:
         raise _elsewhere("lse", lse, device)
-    if lse.dtype is not torch.float32 or tuple(lse.shape) != (q.shape[1], q.shape[0]) or not lse.is_contiguous():
-        raise ValueError(f"lse must be a contiguous float32 tensor of [heads, tokens] = ({q.shape[1]}, {q.shape[0]})")
+    have = lse.shape
+    if lse.dtype is not torch.float32 or len(have) != 2 or have[0] != qs[1] or have[1] != qs[0] or not lse.is_contiguous():
+        raise ValueError(f"lse must be a contiguous float32 tensor of [heads, tokens] = ({qs[1]}, {qs[0]})")
     return lse.data_ptr()
 
 
@@ -215,14 +221,11 @@ def dpa_attention(attention: Attention, q, k, v, out, lse, sequences: Optional[i
     rows one sequence, or ``sequences`` of one length, or those at ``offsets`` (``[sequences + 1]``, or ``[sequences, 2]``
     of begins and ends; ``offsets_k`` for the keys where they lie elsewhere).  q and out are [tokens, heads, dim], k and v
     [tokens_k, kv_heads, dim]."""
-    dev, dtype = _current_device(), q.dtype
-    code, desc = _attention_dtype(q), _describe(attention, q, k, sequences, offsets, offsets_k, dev)
-    buf = ctypes.create_string_buffer(_FORWARD.size)
-    _FORWARD.pack_into(buf, 0, *desc, *_heads("q", q, dev), *_heads("k", k, dev, None, dtype),
-                       *_heads("v", v, dev, k.shape, dtype), *_heads("out", out, dev, q.shape, dtype))
-    a = ctypes.addressof(buf)
-    r = range(a + _DESC_BYTES, a + _FORWARD.size, _ROWS_BYTES)
-    _check(lib.dpa_attention(a, code, *r, _lse(lse, q, dev), _stream_of(stream, dev)))
+    dev, dtype, qs, ks = _current_device(), q.dtype, q.shape, k.shape
+    code, desc = _attention_dtype(q), _describe(attention, qs, ks, sequences, offsets, offsets_k, dev)
+    _check(lib.dpa_attention(desc, code, _pack(*_heads("q", q, dev)), _pack(*_heads("k", k, dev, None, dtype)),
+                             _pack(*_heads("v", v, dev, ks, dtype)), _pack(*_heads("out", out, dev, qs, dtype)),
+                             _lse(lse, qs, dev), _stream_of(stream, dev)))
 
 
 def dpa_attention_workspace(tokens: int, heads: int) -> int:
@@ -233,13 +236,10 @@ def dpa_attention_backward(attention: Attention, q, k, v, out, lse, dout, dq, dk
                            sequences: Optional[int] = None, offsets=None, offsets_k=None, stream=None) -> None:
     """The gradients dq, dk and dv of ``dpa_attention`` from dout, with the out and lse that it left."""
     dev, dtype, qs, ks = _current_device(), q.dtype, q.shape, k.shape
-    code, desc = _attention_dtype(q), _describe(attention, q, k, sequences, offsets, offsets_k, dev)
-    buf = ctypes.create_string_buffer(_BACKWARD.size)
-    _BACKWARD.pack_into(buf, 0, *desc, *_heads("q", q, dev), *_heads("k", k, dev, None, dtype),
-                        *_heads("v", v, dev, ks, dtype), *_heads("out", out, dev, qs, dtype),
-                        *_heads("dout", dout, dev, qs, dtype), *_heads("dq", dq, dev, qs, dtype),
-                        *_heads("dk", dk, dev, ks, dtype), *_heads("dv", dv, dev, ks, dtype))
-    a = ctypes.addressof(buf)
-    r = range(a + _DESC_BYTES, a + _BACKWARD.size, _ROWS_BYTES)
+    code, desc = _attention_dtype(q), _describe(attention, qs, ks, sequences, offsets, offsets_k, dev)
+    rows = [_pack(*_heads(*x)) for x in (("q", q, dev), ("k", k, dev, None, dtype), ("v", v, dev, ks, dtype),
+                                         ("out", out, dev, qs, dtype), ("dout", dout, dev, qs, dtype),
+                                         ("dq", dq, dev, qs, dtype), ("dk", dk, dev, ks, dtype), ("dv", dv, dev, ks, dtype))]
     addr, nbytes = _workspace(workspace, dev)
-    _check(lib.dpa_attention_backward(a, code, *r[:4], _lse(lse, q, dev), *r[4:], addr, nbytes, _stream_of(stream, dev)))
+    _check(lib.dpa_attention_backward(desc, code, *rows[:4], _lse(lse, qs, dev), *rows[4:], addr, nbytes,
+                                      _stream_of(stream, dev)))

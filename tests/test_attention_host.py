@@ -7,7 +7,6 @@ import os
 import pickle
 import re
 import shutil
-import struct
 import subprocess
 import sys
 
@@ -52,14 +51,11 @@ def test_headers_are_plain_c_and_exports_match(tmp_path, header, module, count):
 
 
 def test_packed_structs_have_the_layout_of_c():
-    """The binding packs the structs of a call into one buffer."""
-    assert struct.calcsize(A._DESC) == ctypes.sizeof(A.AttentionDesc) == A._DESC_BYTES
-    assert A._FORWARD.size == A._DESC_BYTES + 4 * ctypes.sizeof(A.Rows)
-    assert A._BACKWARD.size == A._DESC_BYTES + 8 * ctypes.sizeof(A.Rows)
+    """The binding packs the structs of a call as bytes."""
+    assert A._DESC.size == ctypes.sizeof(A.AttentionDesc) and A._ROWS.size == ctypes.sizeof(A.Rows)
     assert A._ROTARY_ROWS.size == ctypes.sizeof(A.RotaryRows) and D._DESC.size == ctypes.sizeof(D.DistillDesc)
-    buf = ctypes.create_string_buffer(A._DESC_BYTES)
-    struct.pack_into(A._DESC, buf, 0, 8, 2, 64, 1, 100, 0.5, 7, 9, 3, 40, 48, 4, 2)
-    d = A.AttentionDesc.from_buffer(buf)
+    assert [x.size for x in A._ROTARY_CALL] == [i * ctypes.sizeof(A.RotaryRows) for i in range(A.DPA_MAX_TENSORS + 1)]
+    d = A.AttentionDesc.from_buffer_copy(A._DESC.pack(8, 2, 64, 1, 100, 0.5, 7, 9, 3, 40, 48, 4, 2))
     assert [getattr(d, k) for k, _ in d._fields_] == [8, 2, 64, 1, 100, 0.5, 7, 9, 3, 40, 48, 4, 2]
 
 

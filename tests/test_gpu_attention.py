@@ -349,3 +349,18 @@ def test_binding_refuses():
         with pytest.raises(dp.DpError):
             dp.dpa_attention_backward(c.attention, *args, ws)
     assert (c.out == 3).all() and (c.dq == 3).all()
+
+
+def test_binding_refuses_heads_of_different_sizes():
+    c = Case(cut(10), 4, 2, 16, "bf16")
+    short, long = (torch.zeros((10, 2, d), dtype=torch.bfloat16, device="cuda") for d in (8, 24))
+    for kv in (short, long):
+        with pytest.raises(ValueError):
+            dp.dpa_attention(c.attention, c.q, kv, kv, c.out, c.lse)
+        with pytest.raises(ValueError):
+            dp.dpa_attention_backward(c.attention, c.q, kv, kv, c.out, c.lse, c.dout, c.dq, kv.clone(), kv.clone(), c.ws)
+    with pytest.raises(ValueError):
+        dp.dpa_attention(c.attention, c.q, c.k, short, c.out, c.lse)
+    with pytest.raises(ValueError):
+        dp.dpa_attention_backward(c.attention, c.q, c.k, c.v, c.out, c.lse, c.dout, c.dq, c.dk, short, c.ws)
+    assert (c.out == 3).all() and (c.dq == 3).all() and (c.dk == 3).all()
