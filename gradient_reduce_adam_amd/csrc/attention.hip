@@ -7,8 +7,9 @@
 //   p = exp2(c S - c m), c = scale log2(e), m a running maximum of the query
 //   out^T += v^T p     p goes into the product from the registers it is in
 // with v^T read by the transposing LDS load, and sums and maxima kept by each lane.
-// Few queries: two or all four of the waves have the same 32, and share the keys of a
-// tile.
+// Queries that see many keys: eight waves, whose halves take turns at the matrix and
+// the vector units.  Few queries: two or all four of the waves have the same 32, and
+// share the keys of a tile.
 //
 // What bounds it.  Heads of 128: matrix pipes and vector units each 47% of the time that
 // the CUs are busy, two waves a SIMD (o, the queries and two tiles on their way fill the
@@ -35,6 +36,7 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves == 4 && kShare == 1 ? 2 : 
     constexpr int kRows = 32 * kWaves / kShare, kKeys = kShare == 1 ? 64 : 32 * kShare, kBlocks = (kD + 31) / 32;
     constexpr int kOwn = kShare == 1 ? 2 : 1;  // times 32 keys of a tile that a wave takes
     constexpr int kTileBytes = kKeys * T::kRowBytes;
+    constexpr bool kTurns = kWaves == 8 && kShare == 1;  // halves of the waves in turns
     // two turns of a k and a v tile; then, where waves share queries, their sums and maxima
     constexpr int kShares = kShare == 1 ? 0 : kWaves * (kShare == 4 ? kBlocks : 1) * 4096;
     constexpr int kBytes = 4 * kTileBytes > kShares + kWaves * 512 ? 4 * kTileBytes : kShares + kWaves * 512;
@@ -70,27 +72,22 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves == 4 && kShare == 1 ? 2 : 
     const int along = T::along(), across = T::across();
     if (from < to) {
         Stage<kD, kKeys, 64 * kWaves> ks, vs;
-        const auto load = [&](int t) {
-            ks.load(k, t, M, sq.dim);
-            vs.load(v, t, M, sq.dim);
-        };
-        const auto store = [&](int turn) {
-            ks.store(base + turn, sq.dim);
-            vs.store(base + turn + kTileBytes, sq.dim);
-        };
-        // The wave's keys of a tile, from t on.
-        const auto step = [&](const lds_u8* kt, int t) {
-            const lds_u8* vt = kt + kTileBytes;
-            f32x16 s[kOwn];
+        f32x16 s[kOwn];
+        u32x4 p[kOwn][2];
+        const auto clear = [&]() {
 #pragma unroll
             for (int j = 0; j < kOwn; ++j) s[j] = zeros();
             __builtin_amdgcn_sched_barrier(0);
+        };
+        // The scores of the wave's keys of a tile.
+        const auto score = [&](const lds_u8* kt) {
 #pragma unroll
             for (int j = 0; j < kOwn; ++j)
 #pragma unroll
                 for (int n = 0; n < kD / 16; ++n) s[j] = mma<DT>(T::read_along(kt, along, j, n), qf[n], s[j]);
-            ahead<kOwn * (kD / 16), 1, 1, 6>();
-            // scores that do not count
+        };
+        // Their probabilities, with those keys from t on that count.
+        const auto soften = [&](int t) {
             if (t + 32 * kOwn - 1 > all_hi)
 #pragma unroll
                 for (int j = 0; j < kOwn; ++j) hide_behind(s[j], hi - t - 32 * j - 4 * half);
@@ -118,7 +115,6 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves == 4 && kShare == 1 ? 2 : 
             __builtin_amdgcn_sched_barrier(0);
             const float less = m == -kInf ? 0.0f : c * m;
             float part[2] = {0.0f, 0.0f};
-            u32x4 p[kOwn][2];
 #pragma unroll
             for (int j = 0; j < kOwn; ++j)
 #pragma unroll
@@ -131,32 +127,113 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves == 4 && kShare == 1 ? 2 : 
                     p[j][n] = pack8<DT>(s[j], n);
                 }
             sum += part[0] + part[1];
+        };
+        const auto add = [&](const lds_u8* vt) {
 #pragma unroll
             for (int j = 0; j < kOwn; ++j)
 #pragma unroll
                 for (int n = 0; n < 2; ++n)
 #pragma unroll
                     for (int x = 0; x < kBlocks; ++x) o[x] = mma<DT>(T::read_across(vt, across, 2 * j + n, x), p[j][n], o[x]);
-            ahead<2 * kOwn * kBlocks, 1, 2, 4>();
-            __builtin_amdgcn_sched_barrier(0);
         };
 #pragma unroll
         for (int n = 0; n < 4; ++n) ks.clear(base + n * kTileBytes, sq.dim);
-        load(from);
-        store(0);
-        load(from + kKeys < to ? from + kKeys : from);
-        __syncthreads();
-        int turn = 0;
-        for (int t = from; t < to; t += kKeys) {
-            const int skip = 32 * (wave % kShare);
-            if (mine < L && t + skip <= some_hi && t + skip + 32 * kOwn > some_lo)
-                step(base + turn + skip * T::kRowBytes, t + skip);
-            if (t + kKeys < to) {
-                turn ^= 2 * kTileBytes;
-                store(turn);
-                // past the last tile this one is loaded again, and not used
-                load(t + 2 * kKeys < to ? t + 2 * kKeys : t + kKeys);
+        if constexpr (kTurns) {
+            // Half of the waves, one on each SIMD, run one phase behind the other half: while
+            // these multiply, those take exponentials.  Tile i of k is read in phases 2 i and
+            // 2 i + 1, of v in the next two, and each is stored in the two phases before its
+            // first, k by a wave behind its products and v behind its exponentials: alone beside
+            // either, the moves made that phase the longer one (8192 rows 1039 TFLOP/s instead
+            // of 1071; both in front of the exponentials 948).
+            const int late = wave >> 2, n = (to - from + kKeys - 1) / kKeys;
+            const bool works = mine < L;
+            const auto tile_k = [&](int i) { return base + (i & 1) * kTileBytes; };
+            const auto tile_v = [&](int i) { return base + (2 + (i & 1)) * kTileBytes; };
+            // past the last tile the first one is loaded again, and not used
+            const auto place = [&](int i) { return i < n ? from + i * kKeys : from; };
+            const auto move_k = [&](int i) {
+                if (i < n) ks.store(tile_k(i), sq.dim);
+                ks.load(k, place(i + 1), M, sq.dim);
+            };
+            const auto move_v = [&](int i) {
+                if (i < n) vs.store(tile_v(i), sq.dim);
+                vs.load(v, place(i + 1), M, sq.dim);
+            };
+            ks.load(k, from, M, sq.dim);
+            vs.load(v, from, M, sq.dim);
+            move_k(0);
+            __syncthreads();
+            if (late) {
+                move_v(0);
                 __syncthreads();
+            }
+            if (works) {
+                clear();
+                score(tile_k(0));
+                ahead<kOwn * (kD / 16), 1, 1, 6>();
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            move_k(1);
+            __syncthreads();
+            for (int i = 0; i < n; ++i) {
+                if (works) soften(from + i * kKeys);
+                __builtin_amdgcn_sched_barrier(0);
+                move_v(i + late);
+                __syncthreads();
+                if (i + 1 < n) {
+                    if (works) {
+                        clear();
+                        add(tile_v(i));
+                        score(tile_k(i + 1));
+                        ahead<2 * kOwn * kBlocks, 1, 2, 4>();
+                        ahead<kOwn * (kD / 16), 1, 1, 6>();
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                    move_k(i + 2);
+                    __syncthreads();
+                }
+            }
+            if (works) {
+                __builtin_amdgcn_sched_barrier(0);
+                add(tile_v(n - 1));
+                ahead<2 * kOwn * kBlocks, 1, 2, 4>();
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            // (as many barriers for the waves in front as for those behind)
+            if (!late) __syncthreads();
+        } else {
+            const auto load = [&](int t) {
+                ks.load(k, t, M, sq.dim);
+                vs.load(v, t, M, sq.dim);
+            };
+            const auto store = [&](int turn) {
+                ks.store(base + turn, sq.dim);
+                vs.store(base + turn + kTileBytes, sq.dim);
+            };
+            load(from);
+            store(0);
+            load(from + kKeys < to ? from + kKeys : from);
+            __syncthreads();
+            int turn = 0;
+            for (int t = from; t < to; t += kKeys) {
+                const int own = t + 32 * (wave % kShare);
+                if (mine < L && own <= some_hi && own + 32 * kOwn > some_lo) {
+                    const lds_u8* const kt = base + turn + (own - t) * T::kRowBytes;
+                    clear();
+                    score(kt);
+                    ahead<kOwn * (kD / 16), 1, 1, 6>();
+                    soften(own);
+                    add(kt + kTileBytes);
+                    ahead<2 * kOwn * kBlocks, 1, 2, 4>();
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                if (t + kKeys < to) {
+                    turn ^= 2 * kTileBytes;
+                    store(turn);
+                    // past the last tile this one is loaded again, and not used
+                    load(t + 2 * kKeys < to ? t + 2 * kKeys : t + kKeys);
+                    __syncthreads();
+                }
             }
         }
     }
@@ -225,7 +302,7 @@ void launch_shape(const AttentionArgs& a, hipStream_t stream) {
     const AttentionShape shape = attention_shape(a.s, 0);
     if (shape == AttentionShape::kSplit) return launch_one<DT, kD, 4, 4>(a, stream);
     if (shape == AttentionShape::kPairs) return launch_one<DT, kD, 8, 2>(a, stream);
-    if constexpr (kD > 96)
+    if constexpr (kD > 64)
         if (shape == AttentionShape::kWide) return launch_one<DT, kD, 8, 1>(a, stream);
     launch_one<DT, kD, 4, 1>(a, stream);
 }
@@ -264,20 +341,23 @@ int64_t attention_slots(const Sequences& s, int side, int64_t tile) {
 //                               768  124 142 345    170 183 464    235 237 494
 //                              1024                                291 301 679
 //    (between 128 and 256 all four waves' times rise with the workgroups)
-//  - eight waves for heads of more than 96 elements and long sequences.  These load each
-//    tile half as often and leave more registers to fragments that are read ahead, but
-//    wait for each other twice as many, and their 256 rows cross the mask's edge further.
-//    Heads of 128, four against eight waves, forward and dq, TFLOP/s of their products:
-//    sequences of 8192 980 and 1055 against 1038 and 1122, of 4096 874 and 967 against
-//    894 and 1020, of 2048 859 and 849 against 856 and 836.  They have to be enough to
-//    fill the CUs.
+//  - eight waves for heads of more than 64 elements whose queries see many keys.  These
+//    load each tile half as often, and in the forward pass their halves take turns; but
+//    they wait for each other twice as many, and their 256 rows cross the mask's edges
+//    further.  Four against eight waves, forward, TFLOP/s of the products that count: causal
+//    heads of 128, 8192 rows 981 and 1071, 4096 869 and 963, 2048 867 and 838, 1024 665 and
+//    609; without a mask, 2048 rows 923 and 1028; 8192 rows, window 1000, 162 and 178 us; heads of
+//    96, 4096 rows 827 and 904, 2048 780 and 767.  dq, heads of 128: 8192 rows 1055 and
+//    1122, 4096 967 and 1020, 2048 849 and 836.  They have to be enough to fill the CUs.
 AttentionShape attention_shape(const Sequences& s, int side) {
     const int heads = side == 0 ? s.heads : s.kv_heads;
     const int64_t groups = attention_slots(s, side, 128) * heads;
     if (groups < (s.dim > 64 ? 160 : 240)) return AttentionShape::kSplit;
     if (groups < (side == 0 ? 640 : 800)) return AttentionShape::kPairs;
-    const bool wide = s.count > 0 && s.rows[1 - side] / s.count >= 3500 && attention_slots(s, side, 256) * heads >= 512;
-    return wide && s.dim > 96 ? AttentionShape::kWide : AttentionShape::kPlain;
+    int64_t seen = s.rows[1 - side] / s.count / (s.causal ? 2 : 1);
+    if (s.window > 0 && s.window < seen) seen = s.window;
+    const bool wide = seen >= 1750 && attention_slots(s, side, 256) * heads >= 512;
+    return wide && s.dim > 64 ? AttentionShape::kWide : AttentionShape::kPlain;
 }
 
 int64_t attention_groups(const Sequences& s) {
