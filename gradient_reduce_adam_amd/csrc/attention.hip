@@ -11,13 +11,14 @@
 // the vector units.  Few queries: two or all four of the waves have the same 32, and
 // share the keys of a tile.
 //
-// What bounds it.  Heads of 128: matrix pipes and vector units each 47% of the time that
-// the CUs are busy, two waves a SIMD (o, the queries and two tiles on their way fill the
-// registers), at 1.9 to 2 GHz: 4 x 4096 rows of 32 heads, causal, bf16 607 us, 905 TFLOP/s
-// of the products that count, 1040 to 1070 at 8192 rows; a large library product reaches
-// 1420.  Heads of 64: the exponentials; 16 of a quarter of the rate, with their scaling,
-// sum, maximum and rounding, take 450 cycles beside 256 of products, and the vector units
-// are busy 68%: 32 x 1024 rows of 12 heads, f16 93 us.
+// What bounds it.  Heads of 128: matrix pipes and vector units each 54% of the time that
+// the CUs are busy (47% without turns), two waves a SIMD (o, the queries and two tiles on
+// their way fill the registers), at the clock that power allows, 1.9 GHz: 4 x 4096 rows of
+// 32 heads, causal, bf16 587 to 602 us, 913 to 937 TFLOP/s of the products that count, 1071
+// at 8192 rows; a large library product reaches 1420.  Heads of 64: the exponentials; 16 of
+// a quarter of the rate, with their scaling, sum, maximum and rounding, take 450 cycles
+// beside 256 of products, and the vector units are busy 70%: 32 x 1024 rows of 12 heads,
+// f16 93 us.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
