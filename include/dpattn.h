@@ -111,9 +111,10 @@ dp_status dpa_rotary(const dpa_rotary_desc* rotary, int64_t tokens, int32_t dim,
  *   j <= place           with causal != 0
  *   j >  place - window  with window > 0 (0: no window)
  * Rows of no sequence (padding between or behind them) are neither read nor
- * written, in any tensor.  An infinity or NaN in a key or value may reach other
- * queries of its sequence than those that see it: a masked score counts 0 times
- * the value, as in the product by a matrix of probabilities.
+ * written, in any tensor.  An infinity or NaN in a row may reach the results of
+ * other rows of its sequence, those that the mask keeps from it among them: a
+ * masked score counts 0 times the value, as in the product by a matrix of
+ * probabilities.
  * A call has fewer than 2^23 tiles: (rows / 128 + sequences) times heads. */
 typedef struct dpa_attention_desc {
     int32_t heads;    /* of the queries, 1 .. DPA_MAX_HEADS, a multiple of kv_heads */

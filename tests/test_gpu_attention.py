@@ -187,6 +187,16 @@ def test_long_sequences(L, M, H, D, causal, window):
     c.check(**c.places())
 
 
+@pytest.mark.parametrize("spans,spans_k,H,K,D,dt,causal,window", [
+    (cut(300), cut(1801), 256, 2, 80, "bf16", False, 0), (cut(700), cut(3700), 200, 4, 96, "f16", True, 1800),
+    (cut(513), cut(5000), 256, 1, 72, "bf16", True, 4000), (cut(5400, 0, 1), None, 24, 4, 88, "bf16", False, 0),
+    (cut(2050, 1800), None, 80, 8, 128, "f16", False, 1900)])
+def test_many_keys(spans, spans_k, H, K, D, dt, causal, window):
+    """Queries that see many keys: workgroups of eight waves, for heads of more than 64 elements."""
+    c = Case(spans, H, K, D, dt, seed=D, spans_k=spans_k, causal=causal, window=window, device="cuda")
+    c.check(**c.places())
+
+
 @pytest.mark.parametrize("dt", ["bf16", "f16"])
 @pytest.mark.parametrize("sigma", [0.0, 0.05, 4.0, 12.0])
 def test_flat_and_steep_rows(sigma, dt):
