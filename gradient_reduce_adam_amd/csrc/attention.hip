@@ -2,7 +2,7 @@
 // the logarithm of each row's sum, in one pass over the keys.
 //
 // A workgroup takes 128 queries of one head and goes over the keys that they see in
-// tiles of 64 rows of k and v.  Each of its four waves has 32 queries:
+// tiles of 64 rows of k and v, or 32.  Each of its four waves has 32 queries:
 //   S^T = k q^T       rows are keys, columns queries: a lane holds its query's scores
 //   p = exp2(c S - c m), c = scale log2(e), m a running maximum of the query
 //   out^T += v^T p     p goes into the product from the registers it is in
@@ -29,13 +29,21 @@ namespace {
 
 using namespace attn;
 
+// Tiles of 32 keys leave heads of 72 to 96 elements registers for a third wave a SIMD: 8 x
+// 1024 rows of 32 heads of 96 76 us, with 64 keys 79.  (A fourth for heads of 64 gained
+// nothing: 16384 rows of 12 heads 267 us with 64 keys, 280 with 32.)
+template <int kD, int kWaves, int kShare>
+constexpr int keys_of_tile() {
+    return kShare > 1 ? 32 * kShare : kWaves == 4 && kD > 64 && kD <= 96 ? 32 : 64;
+}
+
 // kShare: so many neighbouring waves have the same 32 queries, and 32 keys each of
-// every tile; with 1 a wave takes all 64 keys.
+// every tile; with 1 a wave takes all its keys.
 template <dp_dtype DT, int kD, int kWaves, int kShare>
-__global__ void __launch_bounds__(64 * kWaves, kWaves == 4 && kShare == 1 ? 2 : 1) k_attention(AttentionArgs a) {
+__global__ void __launch_bounds__(64 * kWaves, kWaves == 4 && kShare == 1 ? (kD > 64 && kD <= 96 ? 3 : 2) : 1) k_attention(AttentionArgs a) {
     using T = Tile<kD>;
-    constexpr int kRows = 32 * kWaves / kShare, kKeys = kShare == 1 ? 64 : 32 * kShare, kBlocks = (kD + 31) / 32;
-    constexpr int kOwn = kShare == 1 ? 2 : 1;  // times 32 keys of a tile that a wave takes
+    constexpr int kRows = 32 * kWaves / kShare, kKeys = keys_of_tile<kD, kWaves, kShare>(), kBlocks = (kD + 31) / 32;
+    constexpr int kOwn = kKeys / kShare / 32;  // times 32 keys of a tile that a wave takes
     constexpr int kTileBytes = kKeys * T::kRowBytes;
     constexpr bool kTurns = kWaves == 8 && kShare == 1;  // halves of the waves in turns
     // two turns of a k and a v tile; then, where waves share queries, their sums and maxima
