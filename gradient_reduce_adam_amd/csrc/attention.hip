@@ -356,7 +356,7 @@ int64_t attention_slots(const Sequences& s, int side, int64_t tile) {
 //    further.  Four against eight waves, forward, TFLOP/s of the products that count: causal
 //    heads of 128, 8192 rows 981 and 1071, 4096 869 and 963, 2048 867 and 838, 1024 665 and
 //    609; without a mask, 2048 rows 923 and 1028; 8192 rows, window 1000, 162 and 178 us; heads of
-//    96, 4096 rows 827 and 904, 2048 780 and 767.  dq, heads of 128: 8192 rows 1055 and
+//    96, 4096 rows 819 and 881, 2048 751 and 742.  dq, heads of 128: 8192 rows 1055 and
 //    1122, 4096 967 and 1020, 2048 849 and 836.  They have to be enough to fill the CUs.
 AttentionShape attention_shape(const Sequences& s, int side) {
     const int heads = side == 0 ? s.heads : s.kv_heads;
