@@ -5,8 +5,10 @@
 // between the two (50257 logits of 16 bits are 28 registers of 1024 threads) and
 // is read from memory once: read, greatest logit, sums, gradient, write.  The
 // teacher's list is gathered beside it into LDS, with a bit for each token of the list,
-// by which the sums leave these tokens out of the rest.  The gradient is written as
-// if no token were listed; then the listed ones and the label are written again.
+// by which the sums leave these tokens out of the rest.  Where the rest lies far below
+// the row's greatest logit, it is summed again relative to its own greatest one (kFaint).
+// The gradient is written as if no token were listed; then the listed ones and the
+// label are written again.
 // Memory bound: 16384 x 32000 bf16 logits with their gradient 393 to 405 us, 5.2 to 5.3 TB/s of
 // what is read and written once (a large copy 4.9); losses alone, 4096 x 50257 binary32, 130
 // us, 6.3 TB/s.
@@ -22,11 +24,24 @@ namespace {
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kInf = __builtin_inff();
+constexpr float kMost = 3.402823466e38f;
+
+// Exponentials relative to the row's greatest logit are zero from 87 temperatures below
+// it on, but the remainder's term, p' log(p' / q'), grows with this distance.  A sum of
+// the tokens outside the list below kFaint is taken anew, relative to the greatest of
+// them: above it, the terms that are lost, at most 2^18 of 2^-126, are less than 2^-44 of
+// the sum.  So it is where the gradient's factor, others / sum, leaves binary32.
+constexpr float kFaint = 0x1p-64f;
 
 __device__ __forceinline__ float wave_max(float x) {
 #pragma unroll
     for (int m = 1; m < 64; m <<= 1) x = fmaxf(x, __shfl_xor(x, m));
     return x;
+}
+
+// A value that all lanes have, in a scalar register.
+__device__ __forceinline__ float uniform(float x) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, x)));
 }
 
 __device__ __forceinline__ float load_any(dp_dtype dt, const void* p, int64_t i) {
@@ -198,6 +213,17 @@ __global__ void __launch_bounds__(kThreads) k_distill(DistillArgs a, dp_dtype te
             }
         }
     };
+    // The same for the few rows whose remainder is faint: from memory again, in little code.
+    const auto walk = [&](auto&& use) {
+#pragma unroll 1
+        for (int i = tid; i < row.pieces; i += kThreads) {
+            typename R::Piece q = row.load(i);
+            float x[kN];
+            row.settle(i, q);
+            expand<DT, kN>(q, x);
+            use(i, x);
+        }
+    };
     for (int i = tid; i < (row.vocab + row.shift + 31) / 32; i += kThreads) bits[i] = 0;
     bool twice = false;
     const auto mark = [&]() {
@@ -213,6 +239,8 @@ __global__ void __launch_bounds__(kThreads) k_distill(DistillArgs a, dp_dtype te
     const float c = kLog2e * heat;
     float held[kHold ? kPieces : 1][kN];
     float s[kSums] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    // Which elements of piece i are tokens of the list.
+    const auto listed_of = [&](int i) { return bits[(i < row.pieces ? i : 0) * kN >> 5] >> (i * kN & 31); };
     // A piece's part of the sums of the row at both temperatures, and of the tokens
     // outside the list.  At 2 the exponential without the temperature is the square.
     const auto add = [&](int i, const float* x, float peak, float peak1, float* e) {
@@ -222,7 +250,7 @@ __global__ void __launch_bounds__(kThreads) k_distill(DistillArgs a, dp_dtype te
             s[0] += e[j];
         }
         if (rest) {
-            const unsigned int listed = bits[(i < row.pieces ? i : 0) * kN >> 5] >> (i * kN & 31);
+            const unsigned int listed = listed_of(i);
 #pragma unroll
             for (int j = 0; j < kN; ++j) s[1] += listed >> j & 1 ? 0.0f : e[j];
         }
@@ -287,9 +315,9 @@ __global__ void __launch_bounds__(kThreads) k_distill(DistillArgs a, dp_dtype te
 
     // 2. the sums, and those of the list's probabilities and of their products with
     // log p / q
-    const float peak = top * c, peak1 = square ? 2.0f * peak : top * kLog2e;
+    const float peak = uniform(top * c), peak1 = uniform(square ? 2.0f * peak : top * kLog2e);
     const auto plain = [&](float z, float e) { return square ? e * e : __builtin_amdgcn_exp2f(__builtin_fmaf(z, kLog2e, -peak1)); };
-    const float base = rest ? total : list == -kInf ? 0.0f : list;
+    const float base = uniform(rest ? total : list == -kInf ? 0.0f : list);
     if constexpr (kKept == kStream) {
         const float less = __builtin_amdgcn_exp2f(own - peak), less1 = __builtin_amdgcn_exp2f(own1 - peak1);
         s[0] *= less;
@@ -319,16 +347,51 @@ __global__ void __launch_bounds__(kThreads) k_distill(DistillArgs a, dp_dtype te
         s[n] = 0.0f;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) s[n] += sums[n][w];
+        s[n] = uniform(s[n]);
     }
     if (!both) s[2] = s[0];
 
     const float log_all = kLn2 * __builtin_amdgcn_logf(s[0]);
+    const float factor = a.scale * weight, soft = factor * a.soft * a.temperature;
     float kl = 0.0f, mass = 0.0f, others = 0.0f, norm = 1.0f;  // norm: of the list's p
+    float low = peak;  // the reference of s[1]
+    bool faint = false;
     if (rest) {
         others = 1.0f - s[3];
+        faint = others > 0.0f && (s[1] < kFaint || !(fabsf(soft * (others / s[1])) <= kMost));
+        if (faint) {
+            float high = -kInf;
+            walk([&](int i, const float* x) {
+                const unsigned int listed = listed_of(i);
+#pragma unroll
+                for (int j = 0; j < kN; ++j) high = listed >> j & 1 ? high : fmaxf(high, x[j]);
+            });
+            high = wave_max(high);
+            if ((tid & 63) == 0) tops[0][tid >> 6] = high;
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) high = fmaxf(high, tops[0][w]);
+            low = uniform(high * c);
+            float sum = 0.0f;
+            if (high != -kInf)  // else there is no such token, or none that the student gives anything to
+                walk([&](int i, const float* x) {
+                    const unsigned int listed = listed_of(i);
+#pragma unroll
+                    for (int j = 0; j < kN; ++j)
+                        sum += listed >> j & 1 ? 0.0f : __builtin_amdgcn_exp2f(__builtin_fmaf(x[j], c, -low));
+                });
+            sum = wave_sum(sum);
+            if ((tid & 63) == 0) sums[0][tid >> 6] = sum;
+            __syncthreads();
+            s[1] = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) s[1] += sums[0][w];
+            s[1] = uniform(s[1]);
+        }
         if (!(others > 0.0f) || s[1] == 0.0f) others = s[3] != s[3] ? s[3] : 0.0f;
         kl = s[4] + s[3] * log_all;
-        if (others > 0.0f) kl += others * (kLn2 * __builtin_amdgcn_logf(others) - (kLn2 * __builtin_amdgcn_logf(s[1]) - log_all));
+        if (others > 0.0f)
+            kl += others * (kLn2 * __builtin_amdgcn_logf(others) - (kLn2 * (__builtin_amdgcn_logf(s[1]) + (low - peak)) - log_all));
         mass = s[3] + others;
     } else if (list != -kInf) {
         norm = 1.0f / s[3];
@@ -342,10 +405,21 @@ __global__ void __launch_bounds__(kThreads) k_distill(DistillArgs a, dp_dtype te
     __syncthreads();  // in place: every logit of the list and the label's are read
 
     // 3. the gradient of the tokens outside the list, then of the others
-    const float factor = a.scale * weight, soft = factor * a.soft * a.temperature;
-    const float hard = label >= 0 ? factor * a.hard / s[2] : 0.0f;
-    const float in = soft * (mass / s[0]), over = in - (others > 0.0f ? soft * (others / s[1]) : 0.0f);
-    each([&](int i, const float* x, int k) {
+    const float hard = uniform(label >= 0 ? factor * a.hard / s[2] : 0.0f);
+    const float in = uniform(soft * (mass / s[0])), share = uniform(others > 0.0f ? soft * (others / s[1]) : 0.0f);
+    faint = faint && others > 0.0f;  // then what the remainder takes is written with its own reference
+    const float over = uniform(faint ? in : in - share);
+    if (faint) walk([&](int i, const float* x) {
+        float g[kN];
+#pragma unroll
+        for (int j = 0; j < kN; ++j) {
+            const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(x[j], c, -peak));
+            g[j] = __builtin_fmaf(both ? plain(x[j], e) : e, hard, e * in);
+            g[j] -= share * __builtin_amdgcn_exp2f(__builtin_fmaf(x[j], c, -low));
+        }
+        row.store(out, i, g);
+    });
+    else each([&](int i, const float* x, int k) {
         float g[kN];
         const auto power = [&](int j) { return kHold ? held[k][j] : __builtin_amdgcn_exp2f(__builtin_fmaf(x[j], c, -peak)); };
         if (both && square) {  // e over + e^2 hard
@@ -365,9 +439,10 @@ __global__ void __launch_bounds__(kThreads) k_distill(DistillArgs a, dp_dtype te
         if (i < row.pieces) row.store(out, i, g);
     });
     __syncthreads();
-    const auto again = [&](int id, float z, float p, float coefficient) {
+    const auto again = [&](int id, float z, float p, float coefficient, bool remainder) {
         const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(z, c, -peak));
         float g = e * coefficient - soft * p;
+        if (remainder) g -= share * __builtin_amdgcn_exp2f(__builtin_fmaf(z, c, -low));
         const float e1 = both ? plain(z, e) : e;
         g += e1 * hard;
         if (id == label) g -= factor * a.hard;
@@ -386,11 +461,11 @@ __global__ void __launch_bounds__(kThreads) k_distill(DistillArgs a, dp_dtype te
                 }
             if (earlier) continue;
         }
-        again(ids[k], student[k], p, in);
+        again(ids[k], student[k], p, in, false);
     }
     if (tid == 0 && label >= 0) {
         const int at = label + row.shift;
-        if (!(bits[at >> 5] >> (at & 31) & 1)) again(label, target, 0.0f, over);
+        if (!(bits[at >> 5] >> (at & 31) & 1)) again(label, target, 0.0f, over, faint);
     }
 }
 
