@@ -393,10 +393,10 @@ __global__ void __launch_bounds__(kThreads) k_distill(DistillArgs a, dp_dtype te
         if (others > 0.0f)
             kl += others * (kLn2 * __builtin_amdgcn_logf(others) - (kLn2 * (__builtin_amdgcn_logf(s[1]) + (low - peak)) - log_all));
         mass = s[3] + others;
-    } else if (list != -kInf) {
+    } else if (s[3] != 0.0f) {  // a list; one of nothing but NaN, too, whose maximum is -infinity
         norm = 1.0f / s[3];
         kl = s[4] * norm - kLn2 * __builtin_amdgcn_logf(s[3]) + log_all;
-        mass = 1.0f;
+        mass = s[3] != s[3] ? s[3] : 1.0f;
     }
     const float ce = kLn2 * (__builtin_amdgcn_logf(s[2]) - __builtin_fmaf(target, both ? kLog2e : c, both ? -peak1 : -peak));
     if (a.loss && tid == 0)

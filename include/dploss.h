@@ -37,11 +37,13 @@ extern "C" {
  * alone, p_k = exp(y_k / tau) / sum_j exp(y_j / tau), and there is no p'.  With them,
  * total = log(sum of exp(y / tau) over the teacher's whole vocabulary),
  * p_k = exp(y_k / tau - total), and the remaining probability p' = max(0, 1 -
- * sum_k p_k) is compared with what the student gives to all tokens outside the
- * list, q' = sum of q over them (no such term where p' or q' is 0).  Entries whose id lies outside [0, vocab) are padding and not part of
- * the list; an id may occur more than once (each occurrence is a term).  A row whose list is empty, or
- * holds nothing but -infinity, has KL = 0.  A label outside [0, vocab), or labels null, leave CE out.
- * Statistics and sums are binary32. */
+ * sum_k p_k) is compared with what the student gives to all tokens outside the list,
+ * q' = sum of q over them (no such term where p' or q' is 0).  Entries whose id lies
+ * outside [0, vocab) are padding and not part of the list; an id may occur more than once
+ * (each occurrence is a term).  A row whose list is empty, or holds nothing but -infinity,
+ * has KL = 0.  A NaN among the teacher's logits of a row makes its loss and its gradient
+ * NaN.  A label outside [0, vocab), or labels null, leave CE out.  Statistics and sums are
+ * binary32. */
 typedef struct dpd_distill_desc {
     double temperature; /* > 0 */
     double soft, hard;  /* finite */
