@@ -40,8 +40,9 @@ extern "C" {
  * sum_k p_k) is compared with what the student gives to all tokens outside the list,
  * q' = sum of q over them (no such term where p' or q' is 0).  Entries whose id lies
  * outside [0, vocab) are padding and not part of the list; an id may occur more than once
- * (each occurrence is a term).  A row whose list is empty, or holds nothing but -infinity,
- * has KL = 0.  A NaN among the teacher's logits of a row makes its loss and its gradient
+ * (each occurrence is a term).  A row whose list is empty has KL = 0, and so, without
+ * totals, has one that holds nothing but -infinity (with them its tokens have p_k = 0, and
+ * KL = -log q').  A NaN among the teacher's logits of a row makes its loss and its gradient
  * NaN.  A label outside [0, vocab), or labels null, leave CE out.  Statistics and sums are
  * binary32. */
 typedef struct dpd_distill_desc {

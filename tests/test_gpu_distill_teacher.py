@@ -1,8 +1,10 @@
-"""A teacher's rows that are broken, in the distillation on the GPU."""
+"""A teacher's rows that are broken or hold nothing, in the distillation on the GPU."""
+import math
+
 import pytest
 import torch
 
-from test_gpu_distill import Case
+from test_gpu_distill import INF, Case
 
 pytestmark = pytest.mark.gpu
 NAN = float("nan")
@@ -23,3 +25,22 @@ def test_nan_reaches_the_loss_and_the_whole_gradient(tail, T, V, dt):
     c.call()
     assert torch.isnan(c.loss[:2]).all() and torch.isnan(c.dlogits[:2]).all()
     assert torch.isfinite(c.loss[2:]).all() and torch.isfinite(c.dlogits[2:]).all()
+
+
+def test_lists_of_minus_infinity():
+    """Without totals such a list is no list.  With them its tokens have the teacher's probability 0, and the remainder is
+    all of it: KL = -log(what the student gives to the tokens outside the list)."""
+    c = Case(3, 100, 5, "f32", weight=False, labels=False)
+    c.teacher[1] = -INF
+    c.call()
+    assert c.loss[1] == 0 and (c.dlogits[1] == 0).all()
+    c = Case(3, 100, 5, "f32", tail=True, weight=False, labels=False, seed=1)
+    c.ids[1] = torch.arange(5, device="cuda")
+    c.teacher[1] = -INF
+    c.call()
+    logq = torch.log_softmax(c.logits[1].double().cpu(), 0)
+    want = -torch.logsumexp(logq[5:], 0).item()
+    assert want > 0.01 and math.isclose(c.loss[1].item(), want, rel_tol=1e-5)
+    q = logq.exp()
+    grad = torch.where(torch.arange(100) < 5, q, q - q / q[5:].sum())
+    assert ((c.dlogits[1].double().cpu() - grad).abs() <= 1e-6).all()
