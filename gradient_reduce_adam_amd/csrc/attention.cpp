@@ -16,6 +16,9 @@ namespace {
 constexpr int64_t kMaxGroups = (int64_t{1} << 23) - 1;  // of up to 512 threads, fewer than 2^32 in a launch
 constexpr int64_t kMaxStride = int64_t{1} << 36;        // 2^24 rows stay within 63 bits
 constexpr int64_t kMaxRow = (int64_t{1} << 31) - 1;      // of the attention: a row in bytes within 32 bits
+// lse / scale, at which the scores of the backward pass start, stays within binary32 for
+// any sum of 2^24 exponentials, and so does scale log2(e)
+constexpr float kMinScale = 0x1p-100f, kMaxScale = 0x1p100f;
 constexpr int32_t kMaxRotaryDim = 4096;
 constexpr int32_t kMaxWindow = 1 << 26;  // beyond any two rows' distance
 
@@ -59,8 +62,8 @@ dp_status check_attention(const char* where, const dpa_attention_desc* d, dp_dty
     if (d->dim < 8 || d->dim > DPA_MAX_DIM || d->dim % 8 != 0)
         return fail(DP_ERR_INVALID_ARG, "%s: heads of %d elements (a multiple of 8 up to %d)", where, d->dim, DPA_MAX_DIM);
     const float scale = static_cast<float>(d->scale);
-    if (!(scale > 0.0f) || !std::isfinite(scale) || !std::isfinite(1.0f / scale) || !std::isnormal(scale))
-        return fail(DP_ERR_INVALID_ARG, "%s: the scale must be a positive binary32 number", where);
+    if (!(scale >= kMinScale && scale <= kMaxScale))
+        return fail(DP_ERR_INVALID_ARG, "%s: a scale of %g outside [2^-100, 2^100]", where, d->scale);
     if (d->window < 0) return fail(DP_ERR_INVALID_ARG, "%s: a window of %lld", where, ll(d->window));
     dp_status st = check_tokens(where, "query rows", d->tokens);
     if (st == DP_OK) st = check_tokens(where, "key rows", d->tokens_k);

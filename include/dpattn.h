@@ -122,7 +122,7 @@ typedef struct dpa_attention_desc {
     int32_t dim;      /* a multiple of 8 up to DPA_MAX_DIM */
     int32_t causal;
     int64_t window;
-    double scale; /* factor of the products, a positive binary32 number */
+    double scale; /* factor of the products, 2^-100 .. 2^100, taken as binary32 */
     int64_t tokens, tokens_k, sequences;
     const void* offsets;
     const void* offsets_k;
