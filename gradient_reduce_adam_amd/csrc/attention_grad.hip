@@ -172,6 +172,12 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves == 4 && kShare == 1 ? 2 : 
     }
 }
 
+// p of a long row lies below f16's normal numbers, 2^-14, where a bit is lost with each
+// power of two: in the product for dv it is taken 2^12 times, as p <= 1 (to the rounding of
+// its scores) leaves room for.  ds has no such bound, so it is rounded as it is.
+template <dp_dtype DT>
+constexpr float kLift = DT == DP_F16 ? 0x1p12f : 1.0f;
+
 // v's fragments are read from LDS for each tile: in registers they would leave too few
 // for two waves a SIMD (heads of 128: 925 us, from LDS 601) or three (of 64).
 // kShare: so many neighbouring waves have the same 32 keys, and share the queries of
@@ -274,6 +280,7 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves == 8 || kShare == 4 ? 1 : 
                 for (int e = 8 * n; e < 8 * n + 8; ++e) {
                     s[e] = __builtin_amdgcn_exp2f(c * s[e]);
                     dp[e] *= s[e];
+                    s[e] *= kLift<DT>;
                 }
                 p[n] = pack8<DT>(s, n);
                 w[n] = pack8<DT>(dp, n);
@@ -331,7 +338,7 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves == 8 || kShare == 4 ? 1 : 
                 add_block(at_dv, kBlocks, w, wave, 1.0f, sum_v);
             }
             store_block<DT>(pk, 32 * wave, key < M, sq.dim, sum_k, sq.scale);
-            store_block<DT>(pv, 32 * wave, key < M, sq.dim, sum_v, 1.0f);
+            store_block<DT>(pv, 32 * wave, key < M, sq.dim, sum_v, 1.0f / kLift<DT>);
         }
     } else if constexpr (kShare == 2) {  // the even wave of a pair sums dk, the odd one dv, a block at a time
         static_assert(kWaves * 4096 <= kValues + 2 * kTurn, "the shares fit the tiles' memory");
@@ -342,11 +349,11 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves == 8 || kShare == 4 ? 1 : 
             __syncthreads();
             f32x16 sum = wave & 1 ? dv[x] : dk[x];
             add_block((lds_u8*)lds, 1, wave ^ 1, 0, 1.0f, sum);
-            store_block<DT>(wave & 1 ? pv : pk, 32 * x, key < M, sq.dim, sum, wave & 1 ? 1.0f : sq.scale);
+            store_block<DT>(wave & 1 ? pv : pk, 32 * x, key < M, sq.dim, sum, wave & 1 ? 1.0f / kLift<DT> : sq.scale);
         }
     } else {
         store_columns<DT, kD>(a.dk, at.begin[1] + key, hk, key < M, sq.dim, dk, sq.scale);
-        store_columns<DT, kD>(a.dv, at.begin[1] + key, hk, key < M, sq.dim, dv, 1.0f);
+        store_columns<DT, kD>(a.dv, at.begin[1] + key, hk, key < M, sq.dim, dv, 1.0f / kLift<DT>);
     }
 }
 

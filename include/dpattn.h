@@ -146,7 +146,9 @@ dp_status dpa_attention_workspace(int64_t tokens, int32_t heads, size_t* bytes);
  *   ds_ij = p_ij (dout_i v_j - dout_i out_i)
  *   dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i
  * with p computed again from lse; p and ds are rounded to dtype before their
- * products.  dk and dv of a key head are sums over the query heads that read it.
+ * products.  In f16 ds keeps its bits only from 2^-14 (6e-5) on, is 0 below 2^-25 and
+ * infinite from 65520 on, and it falls with the length of a row: dout wants the loss scale
+ * that f16 gradients take anyway.  (p keeps its bits down to 2^-26 in both passes.)  dk and dv of a key head are sums over the query heads that read it.
  * A key that no query sees, and a query that sees no key, get zeros.  (Inputs
  * that repeat a head or a row by a stride of 0 get the gradient of each
  * repetition; dq, dk and dv are tensors of their own, as is every output.) */
