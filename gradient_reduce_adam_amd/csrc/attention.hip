@@ -37,6 +37,12 @@ constexpr int keys_of_tile() {
     return kShare > 1 ? 32 * kShare : kWaves == 4 && kD > 64 && kD <= 96 ? 32 : 64;
 }
 
+// Probabilities are taken 2^kLift times, so that those far below the row's greatest, of
+// which a long row may have many, stay in f16's normal range: with the running maximum's
+// 2^8 they are below 2^15.  It costs nothing, for c m carries it.
+template <dp_dtype DT>
+constexpr float kLift = DT == DP_F16 ? 7.0f : 0.0f;
+
 // kShare: so many neighbouring waves have the same 32 queries, and 32 keys each of
 // every tile; with 1 a wave takes all its keys.
 template <dp_dtype DT, int kD, int kWaves, int kShare>
@@ -122,7 +128,7 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves == 4 && kShare == 1 ? (kD 
                 m = top;
             }
             __builtin_amdgcn_sched_barrier(0);
-            const float less = m == -kInf ? 0.0f : c * m;
+            const float less = m == -kInf ? 0.0f : c * m - kLift<DT>;
             float part[2] = {0.0f, 0.0f};
 #pragma unroll
             for (int j = 0; j < kOwn; ++j)
@@ -297,7 +303,7 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves == 4 && kShare == 1 ? (kD 
         store_columns<DT, kD>(a.out, at.begin[0] + i, h, i < L, sq.dim, o, total == 0.0f ? 0.0f : 1.0f / total);
     }
     if (i < L && half == 0 && wave % kShare == 0)
-        a.lse[h * sq.rows[0] + at.begin[0] + i] = total == 0.0f ? -kInf : sq.scale * m + kLn2 * __builtin_amdgcn_logf(total);
+        a.lse[h * sq.rows[0] + at.begin[0] + i] = total == 0.0f ? -kInf : sq.scale * m + kLn2 * (__builtin_amdgcn_logf(total) - kLift<DT>);
 }
 
 template <dp_dtype DT, int kD, int kWaves, int kShare>

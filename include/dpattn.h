@@ -148,7 +148,8 @@ dp_status dpa_attention_workspace(int64_t tokens, int32_t heads, size_t* bytes);
  * with p computed again from lse; p and ds are rounded to dtype before their
  * products.  In f16 ds keeps its bits only from 2^-14 (6e-5) on, is 0 below 2^-25 and
  * infinite from 65520 on, and it falls with the length of a row: dout wants the loss scale
- * that f16 gradients take anyway.  (p keeps its bits down to 2^-26 in both passes.)  dk and dv of a key head are sums over the query heads that read it.
+ * that f16 gradients take anyway.  (p keeps its bits down to 2^-26; in dpa_attention to
+ * 2^-21 of the row's greatest.)  dk and dv of a key head are sums over the query heads that read it.
  * A key that no query sees, and a query that sees no key, get zeros.  (Inputs
  * that repeat a head or a row by a stride of 0 get the gradient of each
  * repetition; dq, dk and dv are tensors of their own, as is every output.) */

@@ -36,3 +36,26 @@ def test_value_gradients_of_long_flat_rows(M, L, H, K, dt):
     err = (dv.double() - want).abs()
     bound = (2 * u + (64 + 4 * math.log(M) + 2 * (L * H // K + 4)) * E) * want + 2.0 ** -25
     assert (err <= bound).all(), (err / bound).max().item()
+
+
+@pytest.mark.parametrize("H", [1, 260, 700])
+@pytest.mark.parametrize("below", [10.0, 14.0, 17.0])
+def test_far_keys_behind_a_near_one(below, H):
+    """One key above M others whose probabilities are e^-below of its own: together they have a share of the output that
+    none of them has bits for, relative to a maximum of 1, in f16's normal range.  Two values, 1 for the first key and 2
+    for the others: out = 1 + the others' share; their p is off by u of it.  A sum goes over at most M / 8 partial sums, each
+    off by e of a total of 1."""
+    M, D = 200001, 8
+    k = torch.zeros((M, 1, D), dtype=torch.float16, device="cuda")
+    q = torch.zeros((1, H, D), dtype=torch.float16, device="cuda")
+    v = torch.full((M, 1, D), 2.0, dtype=torch.float16, device="cuda")
+    k[0], q[..., 0], v[0] = 1.0, below, 1.0
+    k[0, 0, 1:] = 0
+    out, lse = torch.zeros_like(q), torch.zeros((H, 1), device="cuda")
+    dp.dpa_attention(dp.Attention(scale=1.0), q, k, v, out, lse)
+    share = (M - 1) * math.exp(-below)
+    share /= 1 + share
+    sums = (M / 8 + 64) * E * (1 + share)
+    bound = U * 2 * share + U * (1 + share) + sums
+    assert ((out.double() - (1 + share)).abs() <= bound).all(), ((out.double() - 1 - share).abs().max().item(), bound)
+    assert ((lse.double() - (below + math.log1p((M - 1) * math.exp(-below)))).abs() <= 64 * E * (below + 1) + sums).all()
