@@ -38,10 +38,11 @@ constexpr int keys_of_tile() {
 }
 
 // Probabilities are taken 2^kLift times, so that those far below the row's greatest, of
-// which a long row may have many, stay in f16's normal range: with the running maximum's
-// 2^8 they are below 2^15.  It costs nothing, for c m carries it.
+// which a long row may have many, stay in f16's normal range.  It costs nothing, for c m
+// carries it.  Room is left for the running maximum's 2^8, and for c m as rounded, by up to
+// one at scores of 2^24.
 template <dp_dtype DT>
-constexpr float kLift = DT == DP_F16 ? 7.0f : 0.0f;
+constexpr float kLift = DT == DP_F16 ? 6.0f : 0.0f;
 
 // kShare: so many neighbouring waves have the same 32 queries, and 32 keys each of
 // every tile; with 1 a wave takes all its keys.

@@ -173,10 +173,11 @@ __global__ void __launch_bounds__(64 * kWaves, kWaves == 4 && kShare == 1 ? 2 : 
 }
 
 // p of a long row lies below f16's normal numbers, 2^-14, where a bit is lost with each
-// power of two: in the product for dv it is taken 2^12 times, as p <= 1 (to the rounding of
-// its scores) leaves room for.  ds has no such bound, so it is rounded as it is.
+// power of two: in the product for dv it is taken 2^10 times, enough for the flat rows of 2^24
+// keys.  Room is left for p > 1: scores of 2^24 and their lse are off by some powers of two.
+// ds has no such bound, so it is rounded as it is.
 template <dp_dtype DT>
-constexpr float kLift = DT == DP_F16 ? 0x1p12f : 1.0f;
+constexpr float kLift = DT == DP_F16 ? 0x1p10f : 1.0f;
 
 // v's fragments are read from LDS for each tile: in registers they would leave too few
 // for two waves a SIMD (heads of 128: 925 us, from LDS 601) or three (of 64).

@@ -133,7 +133,9 @@ typedef struct dpa_attention_desc {
  * query i sees; lse[h * tokens + i] = log(sum_j exp(scale q_i k_j)), binary32.  A
  * query that sees no key gets a row of zeros and lse = -infinity.  dtype is
  * DP_BF16 or DP_F16, of all four tensors; products are exact and summed in
- * binary32, and p is rounded to dtype before its product with v. */
+ * binary32, and p is rounded to dtype before its product with v.  Scores scale q_i k_j lie
+ * within 2^24 of 0, where binary32 numbers are one apart: beyond, rows are unspecified (in
+ * dpa_attention_backward p is off by some 2^-22 |lse| of itself). */
 dp_status dpa_attention(const dpa_attention_desc* attention, dp_dtype dtype, const dpa_rows* q, const dpa_rows* k,
                         const dpa_rows* v, const dpa_rows* out, float* lse, hipStream_t stream);
 
@@ -148,10 +150,10 @@ dp_status dpa_attention_workspace(int64_t tokens, int32_t heads, size_t* bytes);
  * with p computed again from lse; p and ds are rounded to dtype before their
  * products.  In f16 ds keeps its bits only from 2^-14 (6e-5) on, is 0 below 2^-25 and
  * infinite from 65520 on, and it falls with the length of a row: dout wants the loss scale
- * that f16 gradients take anyway.  (p keeps its bits down to 2^-26; in dpa_attention to
- * 2^-21 of the row's greatest.)  dk and dv of a key head are sums over the query heads that read it.
- * A key that no query sees, and a query that sees no key, get zeros.  (Inputs
- * that repeat a head or a row by a stride of 0 get the gradient of each
+ * that f16 gradients take anyway.  (p keeps its bits down to 2^-24; in dpa_attention to
+ * 2^-20 of the row's greatest.)  dk and dv of a key head are sums over the query heads
+ * that read it.  A key that no query sees, and a query that sees no key, get zeros.
+ * (Inputs that repeat a head or a row by a stride of 0 get the gradient of each
  * repetition; dq, dk and dv are tensors of their own, as is every output.) */
 dp_status dpa_attention_backward(const dpa_attention_desc* attention, dp_dtype dtype, const dpa_rows* q,
                                  const dpa_rows* k, const dpa_rows* v, const dpa_rows* out, const float* lse,
