@@ -44,7 +44,7 @@ extern "C" {
  * totals, has one that holds nothing but -infinity (with them its tokens have p_k = 0, and
  * KL = -log q').  A NaN among the teacher's logits of a row makes its loss and its gradient
  * NaN.  A label outside [0, vocab), or labels null, leave CE out.  Statistics and sums are
- * binary32. */
+ * binary32; z and z / tau lie within 2^24 of 0, where its numbers are one apart. */
 typedef struct dpd_distill_desc {
     double temperature; /* > 0 */
     double soft, hard;  /* finite */
