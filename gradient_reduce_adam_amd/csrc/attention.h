@@ -303,13 +303,14 @@ __device__ __forceinline__ int64_t offset_at(const Sequences& s, int side, int64
 __device__ __forceinline__ int neighbour(int i, int n) { return n % 8 == 0 ? i % 8 * (n / 8) + i / 8 : i; }
 
 // The tile of this workgroup, of kRows rows of the queries (side 0) or keys (1), for
-// one of `heads` heads; false where it has none.  Tiles come in the order of their
-// work, the most first (`last_first`: in a sequence from its end), for all
-// sequences and heads at once, so that what is left at the end of the launch is
+// one of `heads` heads; false where it has none.  Tiles of sequences of one length come
+// in the order of their work, the most first (`last_first`: in a sequence from its end),
+// for all sequences and heads at once, so that what is left at the end of the launch is
 // small: head by head instead, a fifth to a quarter of the CUs' time was lost there.
 //
-// With offsets, tiles are found by slots in the order of the sequences, heaviest
-// first in each.  Sequence s has the slots from begin / kRows + s on: these rise
+// With offsets, tiles are found by slots in the order of the sequences, for all heads at
+// once, and heaviest first in each sequence only: a long one behind short ones starts late
+// (8191 packed rows: CUs busy 69 to 83% of the time).  Sequence s has the slots from begin / kRows + s on: these rise
 // with s, and as the next sequence begins behind the last row of this one, there are
 // enough of them for all its tiles.  Some are left over.
 template <int kRows>

@@ -14,11 +14,11 @@
 // What bounds it.  Heads of 128: matrix pipes and vector units each 54% of the time that
 // the CUs are busy (47% without turns), two waves a SIMD (o, the queries and two tiles on
 // their way fill the registers), at the clock that power allows, 1.9 GHz: 4 x 4096 rows of
-// 32 heads, causal, bf16 587 to 602 us, 913 to 937 TFLOP/s of the products that count, 1071
-// at 8192 rows; a large library product reaches 1420.  Heads of 64: the exponentials; 16 of
+// 32 heads, causal, bf16 587 to 637 us on several machines, 863 to 937 TFLOP/s of the products
+// that count, 1071 at 8192 rows; a large library product reaches 1420.  Heads of 64: the exponentials; 16 of
 // a quarter of the rate, with their scaling, sum, maximum and rounding, take 450 cycles
 // beside 256 of products, and the vector units are busy 70%: 32 x 1024 rows of 12 heads,
-// f16 93 us.
+// f16 90 to 97 us.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -365,6 +365,8 @@ int64_t attention_slots(const Sequences& s, int side, int64_t tile) {
 //    609; without a mask, 2048 rows 923 and 1028; 8192 rows, window 1000, 162 and 178 us; heads of
 //    96, 4096 rows 819 and 881, 2048 751 and 742.  dq, heads of 128: 8192 rows 1055 and
 //    1122, 4096 967 and 1020, 2048 849 and 836.  They have to be enough to fill the CUs.
+// Rows and keys are what the tensors have, for offsets are in device memory: padding counts,
+// and a batch of one long sequence and many short ones gets the rule of their mean length.
 AttentionShape attention_shape(const Sequences& s, int side) {
     const int heads = side == 0 ? s.heads : s.kv_heads;
     const int64_t groups = attention_slots(s, side, 128) * heads;

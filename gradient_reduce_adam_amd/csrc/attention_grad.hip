@@ -16,10 +16,10 @@
 //
 // What bounds them: matrix pipes busy 52% (dq) and 47% (dk and dv) of the time that the
 // CUs are, for heads of 128 with two waves a SIMD at 2.0 to 2.1 GHz.  2 x 4096 rows of 32
-// heads of 128, causal, bf16: dq 395 us, 1040 TFLOP/s of its three products, dk and dv 548
-// us, 1000 of their four.  In dkv half of the products read both operands from LDS, which is
-// busy 39%.  Heads of 64, 32 x 1024 rows of 12 heads, f16: 121 and 145 us, the vector
-// units busy 50% and 42%, the matrix pipes 35%.
+// heads of 128, causal, bf16: dq 395 to 420 us, 980 to 1040 TFLOP/s of its three products, dk
+// and dv 548 to 575 us, 955 to 1000 of their four.  In dkv half of the products read both operands from LDS, which is
+// busy 39%.  Heads of 64, 32 x 1024 rows of 12 heads, f16: 122 and 148 us, the vector
+// units busy 51% and 48%, the matrix pipes 36 and 37%.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -372,8 +372,8 @@ void launch_dkv(const AttentionArgs& a, hipStream_t stream) {
 
 // In k_attention_dkv heads of more than 96 elements take eight waves and tiles of 64
 // queries (2 x 4096 rows of 32 heads of 128: 546 us, four waves and 32 queries 573);
-// smaller ones leave room for three waves a SIMD, which four waves fill better (heads of
-// 64, 1024 rows: 143 us against 169).
+// those of up to 64 leave room for three waves a SIMD, which four waves fill better (heads of
+// 64, 1024 rows: 143 us against 169), those of 72 to 96 for two.
 template <dp_dtype DT, int kD>
 void launch_both(const AttentionArgs& a, hipStream_t stream) {
     constexpr bool kLarge = kD > 96;
