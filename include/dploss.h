@@ -57,7 +57,8 @@ typedef struct dpd_distill_desc {
 /* loss[t] for `tokens` rows (binary32; null: not wanted) and, unless dlogits is
  * null,
  *   dlogits[t] = scale * weight[t] * d loss[t] / d z[t]
- * in one reading of the logits.  weight: binary32 factors of the rows (a mask,
+ * in one reading of the logits (rows longer than the registers hold, and those whose
+ * remainder lies far below their greatest logit, are read again).  weight: binary32 factors of the rows (a mask,
  * 1 / rows), null for 1; a row of weight 0 is not read and gets loss 0 and zeros.
  * logits and dlogits: rows of vocab elements of dtype (DP_F32, DP_F16, DP_BF16), ld
  * apart; dlogits may be logits itself with its stride, in place.  teacher: rows
